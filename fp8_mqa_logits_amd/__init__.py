@@ -643,3 +643,8 @@ def read_stats(workspace: torch.Tensor) -> dict:
             "fail_reasons": [int(h[26]), int(h[27]), int(h[28]), int(h[29])],
             # two-level source calls: rows the exact block scan served
             "rows_block_scan": int(h[32])}
+
+
+from .attend import (KVLayout, mqa_attend_paged, mqa_attend_topk, mqa_kv_append,  # noqa: E402
+                     mqa_kv_read, workspace_size_attend)
+from .attend import EXPORTS as ATTEND_EXPORTS  # noqa: E402

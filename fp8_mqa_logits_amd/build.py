@@ -9,8 +9,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libmqa_topk.so")
-SOURCES = ["fused.hip", "dense.hip", "probe.hip", "api.hip"]
-HEADERS = ["common.h", "launch.h"]
+SOURCES = ["fused.hip", "dense.hip", "probe.hip", "api.hip", "kvcache.hip", "attend.hip",
+           "attend_api.hip"]
+HEADERS = ["common.h", "launch.h", "attend.h"]
 
 
 def hipcc() -> str:
@@ -31,7 +32,7 @@ def stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + \
-           [os.path.join(ROOT, "include", "mqa_topk.h")]
+           [os.path.join(ROOT, "include", h) for h in ("mqa_topk.h", "mqa_attend.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -400,6 +400,21 @@ int static_batch(const DeviceInfo& d) {
 
 }  // namespace
 
+// What attend_api.hip shares with this file: the device check and the text of
+// mqa_strerror.
+namespace mqa {
+int device_cus(int device) {
+  const DeviceInfo* d = device_info(device);
+  return d ? d->cus : 0;
+}
+int current_device_cus() {
+  const DeviceInfo* d = current_device();
+  return d ? d->cus : 0;
+}
+int launch_failed(int hip_code) { return launch_error(hip_code); }
+int workspace_failed(const char* what) { return workspace_error_text(what); }
+}  // namespace mqa
+
 extern "C" {
 
 size_t workspace_size(int rows, int device) {

@@ -1,0 +1,205 @@
+// C ABI of the paged 8-bit key/value cache: argument checks, workspace layout
+// and launches. The declarations and their contracts are in
+// include/mqa_attend.h.
+#include <hip/hip_runtime.h>
+
+#include "attend.h"
+#include "launch.h"
+#include "mqa_attend.h"
+
+namespace {
+
+using mqa::AttendParams;
+using mqa::KvCache;
+using mqa::KvMoveParams;
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+bool power_of_two(int x) { return x > 0 && (x & (x - 1)) == 0; }
+
+// Bytes of a page (0: sizes out of range). A page stays below 2^31 bytes, so
+// that offsets inside it fit 32 bits.
+int64_t page_bytes(int kv_heads, int head_dim, int page_size, int block) {
+  if (kv_heads < 1 || kv_heads > MQA_MAX_ATTEND_HEADS || (head_dim != 64 && head_dim != 128) ||
+      !power_of_two(page_size) || page_size < 16 || page_size > 65536 || !power_of_two(block) ||
+      block < 16 || block > page_size)
+    return 0;
+  const int64_t n = 2 * (int64_t)kv_heads * ((int64_t)page_size * head_dim + page_size / block * 4);
+  const int64_t padded = (n + 127) / 128 * 128;
+  return padded < ((int64_t)1 << 31) ? padded : 0;
+}
+
+// NULL and ALIGN part of a cache's checks.
+int cache_pointers(const mqa_kv_cache* c) {
+  if (!c || !c->pages || !c->table) return MQA_ERR_NULL;
+  return aligned(c->pages, 16) && aligned(c->table, 4) && c->page_stride % 16 == 0 ? MQA_OK
+                                                                                  : MQA_ERR_ALIGN;
+}
+
+bool cache_shape(const mqa_kv_cache* c) {
+  const int64_t n = page_bytes(c->kv_heads, c->head_dim, c->page_size, c->block);
+  return n > 0 && c->page_stride >= n && c->page_stride < ((int64_t)1 << 40) && c->num_pages >= 1 &&
+         c->table_stride >= 1 && (c->codes == MQA_CODES_E4M3 || c->codes == MQA_CODES_INT8);
+}
+
+KvCache kernel_cache(const mqa_kv_cache* c) {
+  KvCache k{};
+  k.pages = static_cast<uint8_t*>(c->pages);
+  k.table = c->table;
+  k.page_stride = c->page_stride;
+  k.num_pages = c->num_pages;
+  k.table_stride = c->table_stride;
+  k.kv_heads = c->kv_heads;
+  k.head_dim = c->head_dim;
+  k.page_shift = __builtin_ctz((unsigned)c->page_size);
+  k.block_shift = __builtin_ctz((unsigned)c->block);
+  k.codes = c->codes;
+  const int64_t cap = (int64_t)c->table_stride * c->page_size;
+  k.cap = (int)(cap < MQA_MAX_KEYS ? cap : MQA_MAX_KEYS);
+  k.scales_at = 2 * c->kv_heads * c->page_size * c->head_dim;
+  return k;
+}
+
+bool rows_ok(int requests, int R) {
+  return requests >= 1 && R >= 1 && (int64_t)requests * R <= MQA_MAX_ROWS;
+}
+
+int move(const mqa_kv_cache* cache, KvMoveParams& p, int (*launch)(const KvMoveParams*, hipStream_t),
+         void* stream) {
+  if (!mqa::current_device_cus()) return MQA_ERR_DEVICE;
+  p.c = kernel_cache(cache);
+  const int rc = launch(&p, static_cast<hipStream_t>(stream));
+  return rc != 0 ? mqa::launch_failed(rc) : MQA_OK;
+}
+
+int attend(const mqa_kv_cache* cache, const void* q, int64_t q_row, int64_t q_head, int dtype,
+           const int32_t* indices, int width, const int32_t* starts, const int32_t* ends,
+           void* out, float* lse, int requests, int R, int heads, float scale, void* workspace,
+           size_t workspace_bytes, int positions, void* stream) {
+  if (!cache || !q || !starts || !ends || !out || !workspace) return MQA_ERR_NULL;
+  const int rc = cache_pointers(cache);
+  if (rc != MQA_OK) return rc;
+  if (!aligned(q, 16) || q_row % 8 != 0 || q_head % 8 != 0 || !aligned(starts, 4) ||
+      !aligned(ends, 4) || !aligned(indices, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 256))
+    return MQA_ERR_ALIGN;
+  if (!cache_shape(cache) || !rows_ok(requests, R) || heads < 1 || heads > MQA_MAX_ATTEND_HEADS ||
+      heads % cache->kv_heads != 0 || (dtype != MQA_BF16 && dtype != MQA_FP16) || q_row < 0 ||
+      q_head < 0 || !(scale >= 0.f) || scale > 3.4e38f ||
+      (indices && (width < 1 || width > MQA_MAX_LIST)))
+    return MQA_ERR_SHAPE;
+  int device = -1;
+  if (!mqa::current_device_cus() || hipGetDevice(&device) != hipSuccess) return MQA_ERR_DEVICE;
+  const size_t need = workspace_size_attend(requests, R, heads, cache->kv_heads, cache->head_dim,
+                                            positions, device);
+  if (need == 0 || workspace_bytes < need)
+    return mqa::workspace_failed("the workspace is smaller than workspace_size_attend()");
+  AttendParams p{};
+  p.c = kernel_cache(cache);
+  p.q = q;
+  p.q_row = q_row;
+  p.q_head = q_head;
+  p.starts = starts;
+  p.ends = ends;
+  p.indices = indices;
+  p.width = width;
+  p.out = out;
+  p.lse = lse;
+  p.requests = requests;
+  p.R = R;
+  p.rows = requests * R;
+  p.heads = heads;
+  p.group = heads / cache->kv_heads;
+  p.dtype = dtype;
+  p.scale = scale;
+  const int err = mqa_attend_launch(&p, static_cast<hipStream_t>(stream));
+  return err != 0 ? mqa::launch_failed(err) : MQA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mqa_kv_page_bytes(int kv_heads, int head_dim, int page_size, int block) {
+  return (size_t)page_bytes(kv_heads, head_dim, page_size, block);
+}
+
+int mqa_kv_append(const mqa_kv_cache* cache, const void* k, int64_t k_row_stride,
+                  int64_t k_head_stride, const void* v, int64_t v_row_stride,
+                  int64_t v_head_stride, int dtype, const int32_t* starts, const int32_t* counts,
+                  int requests, int R, void* stream) {
+  if (!cache || !k || !v || !starts) return MQA_ERR_NULL;
+  const int rc = cache_pointers(cache);
+  if (rc != MQA_OK) return rc;
+  const int unit = dtype == MQA_FP32 ? 4 : 8;  // elements in 16 bytes
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(starts, 4) || !aligned(counts, 4) ||
+      k_row_stride % unit != 0 || k_head_stride % unit != 0 || v_row_stride % unit != 0 ||
+      v_head_stride % unit != 0)
+    return MQA_ERR_ALIGN;
+  if (!cache_shape(cache) || !rows_ok(requests, R) || dtype < MQA_BF16 || dtype > MQA_FP32 ||
+      k_row_stride < 0 || k_head_stride < 0 || v_row_stride < 0 || v_head_stride < 0)
+    return MQA_ERR_SHAPE;
+  KvMoveParams p{};
+  p.k = k;
+  p.v = v;
+  p.k_row = k_row_stride;
+  p.k_head = k_head_stride;
+  p.v_row = v_row_stride;
+  p.v_head = v_head_stride;
+  p.starts = starts;
+  p.counts = counts;
+  p.requests = requests;
+  p.R = R;
+  p.dtype = dtype;
+  return move(cache, p, mqa_kv_append_launch, stream);
+}
+
+int mqa_kv_read(const mqa_kv_cache* cache, void* k, void* v, int dtype, const int32_t* starts,
+                const int32_t* counts, int requests, int R, void* stream) {
+  if (!cache || !k || !v || !starts) return MQA_ERR_NULL;
+  const int rc = cache_pointers(cache);
+  if (rc != MQA_OK) return rc;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(starts, 4) || !aligned(counts, 4))
+    return MQA_ERR_ALIGN;
+  if (!cache_shape(cache) || !rows_ok(requests, R) || dtype < MQA_BF16 || dtype > MQA_FP32)
+    return MQA_ERR_SHAPE;
+  KvMoveParams p{};
+  p.ko = k;
+  p.vo = v;
+  p.starts = starts;
+  p.counts = counts;
+  p.requests = requests;
+  p.R = R;
+  p.dtype = dtype;
+  return move(cache, p, mqa_kv_read_launch, stream);
+}
+
+size_t workspace_size_attend(int requests, int R, int heads, int kv_heads, int head_dim,
+                             int positions, int device) {
+  if (!rows_ok(requests, R) || kv_heads < 1 || heads < kv_heads || heads > MQA_MAX_ATTEND_HEADS ||
+      heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128) || positions < 1 ||
+      !mqa::device_cus(device))
+    return 0;
+  return 256;
+}
+
+int mqa_attend_paged(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
+                     int64_t q_head_stride, int dtype, const int32_t* starts, const int32_t* ends,
+                     void* out, float* lse, int requests, int R, int heads, float scale,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  const int64_t cap = cache ? (int64_t)cache->table_stride * cache->page_size : 0;
+  return attend(cache, q, q_row_stride, q_head_stride, dtype, nullptr, 0, starts, ends, out, lse,
+                requests, R, heads, scale, workspace, workspace_bytes,
+                (int)(cap < MQA_MAX_KEYS ? cap : MQA_MAX_KEYS), stream);
+}
+
+int mqa_attend_topk(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
+                    int64_t q_head_stride, int dtype, const int32_t* indices, int width,
+                    const int32_t* starts, const int32_t* ends, void* out, float* lse,
+                    int requests, int R, int heads, float scale, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (!indices) return MQA_ERR_NULL;
+  return attend(cache, q, q_row_stride, q_head_stride, dtype, indices, width, starts, ends, out,
+                lse, requests, R, heads, scale, workspace, workspace_bytes, width, stream);
+}
+
+}  // extern "C"

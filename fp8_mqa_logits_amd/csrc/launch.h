@@ -140,6 +140,13 @@ constexpr int kMaxBatchRows = 16384;
 // the key's nhat bit pattern in the others.
 constexpr uint32_t kKeyMask = 0xFFFFFu;
 
+// api.hip: compute units of a gfx950 device (0: none), and the error codes
+// whose text mqa_strerror gives.
+int device_cus(int device);
+int current_device_cus();
+int launch_failed(int hip_code);
+int workspace_failed(const char* what);
+
 }  // namespace mqa
 
 extern "C" {

@@ -48,6 +48,12 @@ struct AttendParams {
   float* lse;
   int requests, R, rows, heads, group, dtype;
   float scale;
+  // How the work is cut: tiles of `cols` columns (rows x the query heads of a
+  // key head) per request or listed row, each tile's keys in `splits` parts.
+  int cols, tiles, splits;
+  int64_t block0;  // first workgroup of this launch
+  float* part_ml;  // [item][split][cols][2] reference point and sum
+  float* part_o;   // [item][split][cols][head_dim]
 };
 
 // Byte offsets of a page's parts: all below 2^31 (checked on the host).

@@ -4,99 +4,596 @@
 //     m = max_j S_j,  l = sum_j exp(S_j - m)
 //     out = sum_j exp(S_j - m) * vs_j * vc_j / l,   lse = m + ln l
 // over the positions j of the row's range, or over its listed positions.
+//
+// Numbers. Codes of either kind are exact in bf16 and in fp16, so q . kc runs
+// on the matrix unit in q's own type with fp32 sums, and the scales come in
+// afterwards, in fp32. The probabilities go to the second product in fp16
+// whatever q's type (11 bits; bf16's 8 would add an error as large as the
+// rounding of a bf16 output), as P = 2^7 exp2(S' - m) vs / vref with S' in
+// units of ln 2 and vref the largest value scale met so far: at most 2^15, and
+// full precision down to 2^-21 of the row's largest. Reference points move
+// lazily: m only when a score passes it by more than 8 (P <= 2^15 until then),
+// vref when a larger scale is met; both times the sums are rescaled. l sums the
+// fp32 P before its rounding.
 #include "attend.h"
 #include "launch.h"
 
 namespace mqa {
 namespace {
 
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLowest = -3.4028234e38f;  // m of a column that has seen nothing
+constexpr float kLag = 8.f;                // how far scores may pass m
+constexpr float kBias = 7.f;               // P = 2^kBias at a score of m
+constexpr uint32_t kNone = ~0u;            // token of a key that no row sees
 
-__device__ __forceinline__ float element(const void* base, int64_t at, int type) {
-  const uint16_t u = static_cast<const uint16_t*>(base)[at];
-  return type == kBf16 ? __uint_as_float((uint32_t)u << 16) : (float)__builtin_bit_cast(_Float16, u);
+// 4 codes of one dword -> 4 values of the matrix unit's type.
+template <int T, int C>
+__device__ __forceinline__ uint2 widen4(uint32_t w) {
+  if constexpr (C == kE4m3) {
+    if constexpr (T == kBf16) {
+      return uint2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, 1.f, false)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, 1.f, true))};
+    } else {
+      return uint2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.f, false)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w, 1.f, true))};
+    }
+  } else if constexpr (T == kBf16) {
+    const v2bf a{(__bf16)(float)(int8_t)w, (__bf16)(float)(int8_t)(w >> 8)};
+    const v2bf b{(__bf16)(float)(int8_t)(w >> 16), (__bf16)(float)(int8_t)(w >> 24)};
+    return uint2{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
+  } else {
+    // the byte as the low mantissa bits of 1024 + (code + 128), exact in fp16
+    w ^= 0x80808080u;
+    const v2h off{(_Float16)-1152.f, (_Float16)-1152.f};
+    const v2h a = __builtin_bit_cast(v2h, __builtin_amdgcn_perm(0x64646464u, w, 0x04010400u)) + off;
+    const v2h b = __builtin_bit_cast(v2h, __builtin_amdgcn_perm(0x64646464u, w, 0x04030402u)) + off;
+    return uint2{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
+  }
 }
 
-__device__ __forceinline__ float code_value(uint32_t byte, int codes) {
-  return codes == kE4m3 ? __builtin_amdgcn_cvt_f32_fp8((int)byte, 0) : (float)(int8_t)byte;
+template <int T, int C>
+__device__ __forceinline__ v4u widen8(uint32_t lo, uint32_t hi) {
+  const uint2 a = widen4<T, C>(lo), b = widen4<T, C>(hi);
+  return v4u{a.x, a.y, b.x, b.y};
 }
 
-// One wave per (row, query head): a lane scores one of 64 positions at a time,
-// then the wave adds the 64 value rows, a lane owning head_dim / 64 columns.
-__global__ __launch_bounds__(64) void attend_wave_kernel(AttendParams p) {
+template <int T>
+__device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
+  if constexpr (T == kBf16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a),
+                                                   __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a),
+                                                  __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+}
+
+// Bytes w[i] of four dwords (rows) -> t[b] = bytes b of the four rows.
+__device__ __forceinline__ void transpose4(const uint32_t* w, uint32_t* t) {
+  const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u);  // w0.0 w1.0 w0.1 w1.1
+  const uint32_t b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u);
+  const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u);
+  const uint32_t d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+  t[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
+  t[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
+  t[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
+  t[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
+}
+
+// 0xFF in each byte of w that is an e4m3 NaN (0x7F or 0xFF).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  const uint32_t t = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  return (t >> 7) * 0xFFu;
+}
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) x = __builtin_fmaxf(x, __shfl_xor(x, o, 64));
+  return x;
+}
+
+__device__ __forceinline__ uint16_t to_type(float x, int type) {
+  return type == kBf16 ? __builtin_bit_cast(uint16_t, (__bf16)x)
+                       : __builtin_bit_cast(uint16_t, (_Float16)x);
+}
+
+// A row's range, clamped as the contract says.
+__device__ __forceinline__ void row_range(const AttendParams& p, int row, int& s, int& e) {
+  s = p.starts[row];
+  e = p.ends[row];
+  s = s < 0 ? 0 : (s > p.c.cap ? p.c.cap : s);
+  e = e < s ? s : (e > p.c.cap ? p.c.cap : e);
+}
+
+// Slot of a request's position in the pool: page * page_size + slot.
+__device__ __forceinline__ uint32_t token_of(const KvCache& c, int request, int pos) {
+  int page = c.table[(int64_t)request * c.table_stride + (pos >> c.page_shift)];
+  page = page < 0 ? 0 : (page >= c.num_pages ? c.num_pages - 1 : page);
+  return ((uint32_t)page << c.page_shift) + (uint32_t)(pos & ((1 << c.page_shift) - 1));
+}
+
+// ---------------------------------------------------------------------------
+// Few columns. A column is a (row, query head) pair; the columns of one
+// request and key head see the same keys and share a workgroup, 16 NT of them
+// at most (lists: the heads of one row). The keys are split over the
+// workgroup's four waves and over p.splits workgroups, 32 at a time.
+//
+// Per wave and step, with g = lane / 16 and n = lane % 16:
+//   S^T = K Q^T, 16 keys x 16 columns per v_mfma_f32_16x16x32: lane (g, n)
+//     loads 16-byte pieces of key n and gets the scores of keys 4g + i,
+//     column n;
+//   O^T += V^T P^T: the lane's eight scores (keys 4g + i of both halves of
+//     the step) are its own operand as they stand, without a move between
+//     lanes, when V's operand takes its keys in the same order: lane (g, n)
+//     loads D / 16 consecutive codes of each of those eight keys (a wave's
+//     load covers whole rows), and a byte transpose in registers makes them
+//     the operands of D / 16 products, product u holding columns
+//     d = D/16 * (4g + i) + u of the output.
+// Nothing passes through LDS but a key's token and scales. The tokens are
+// looked up two steps ahead, the codes are loaded one step ahead.
+//
+// Bound by the cache's bytes for few heads a key head, by the two widenings
+// for many.
+template <int T, int C, int D, int NT, bool LIST>
+__global__ __launch_bounds__(256, NT == 4 ? 1 : 2) void attend_narrow_kernel(AttendParams p) {
+  constexpr int KC = D / 64;       // 16-byte pieces of a key per lane
+  constexpr int U = D / 16;        // products per step and column tile
+  constexpr int VW = D / 64;       // dwords of a value per lane
+  constexpr int COLS = 16 * NT;
+  constexpr int US = U < 8 / NT ? U : 8 / NT;  // products merged per round
   const KvCache& c = p.c;
-  const int row = blockIdx.x, head = blockIdx.y, h = head / p.group;
-  const int l = threadIdx.x, D = c.head_dim, request = row / p.R;
-  __shared__ float q[128];
-  __shared__ float prob[64];
-  __shared__ int64_t vrow[64];
-  for (int d = l; d < D; d += 64)
-    q[d] = element(p.q, row * p.q_row + head * p.q_head + d, p.dtype);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, n = lane & 15;
+  const int64_t block = p.block0 + blockIdx.x;
+  const int split = (int)(block % p.splits);
+  const int64_t item = block / p.splits;
+  const int h = (int)(item % c.kv_heads), tile = (int)(item / c.kv_heads % p.tiles);
+  const int unit = (int)(item / c.kv_heads / p.tiles);  // the request, or the row of a list
+  const int per_unit = LIST ? 1 : p.R;
+  const int request = LIST ? unit / p.R : unit;
+  const int columns = per_unit * p.group;        // of the unit
+
+  __shared__ __align__(16) uint32_t s_tok[4][2][32];
+  __shared__ __align__(16) float s_ks[4][32], s_vs[4][32];
+  __shared__ float s_part[4][US * 16][COLS];
+  __shared__ float s_m[4][COLS], s_l[4][COLS];
+
+  // this lane's columns and the tile's range of positions
+  const int row_lo = unit * per_unit + tile * COLS / p.group;
+  const int last = tile * COLS + COLS < columns ? tile * COLS + COLS : columns;
+  const int row_hi = unit * per_unit + (last - 1) / p.group;
+  int lo, hi, in_lo, in_hi;  // seen by some row, seen by every row
+  {
+    const int r = row_lo + lane <= row_hi ? row_lo + lane : row_hi;  // at most COLS rows
+    row_range(p, r, in_lo, in_hi);
+    lo = in_lo < in_hi ? in_lo : c.cap;
+    hi = in_lo < in_hi ? in_hi : 0;
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+      lo = min(lo, __shfl_xor(lo, o, 64));
+      hi = max(hi, __shfl_xor(hi, o, 64));
+      in_lo = max(in_lo, __shfl_xor(in_lo, o, 64));
+      in_hi = min(in_hi, __shfl_xor(in_hi, o, 64));
+    }
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    in_lo = __builtin_amdgcn_readfirstlane(in_lo);
+    in_hi = __builtin_amdgcn_readfirstlane(in_hi);
+  }
+  int col_s[NT], col_e[NT];
+  v4u q[NT][2 * KC];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int col = tile * COLS + 16 * t + n;
+    const bool real = col < columns;
+    const int row = unit * per_unit + (real ? col / p.group : 0);
+    const int head = h * p.group + (real ? col % p.group : 0);
+    row_range(p, row, col_s[t], col_e[t]);
+    const uint16_t* src = static_cast<const uint16_t*>(p.q) + row * p.q_row + head * p.q_head;
+#pragma unroll
+    for (int k = 0; k < 2 * KC; ++k) {
+      q[t][k] = *reinterpret_cast<const v4u*>(src + 64 * (k >> 1) + 16 * g + 8 * (k & 1));
+      if (!real) q[t][k] = v4u{0, 0, 0, 0};
+    }
+  }
+  // the part of the keys (list entries) that this workgroup takes, in steps
+  // of 32 from a multiple of 16, so that a half step lies in one block
+  const int first = LIST ? 0 : lo & ~15;
+  const int end = LIST ? p.width : hi;
+  const int steps = end > first ? (end - first + 31) / 32 : 0;
+  const int per_split = ((steps + p.splits - 1) / p.splits + 3) & ~3;
+  const int step_lo = split * per_split + wave;
+  const int step_hi = steps < (split + 1) * per_split ? steps : (split + 1) * per_split;
+
+  const float cs = p.scale * kLog2e;
+  float m[NT], l[NT], vref = 0.f;
+  v4f acc[NT][U];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    m[t] = kLowest;
+    l[t] = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) acc[t][u] = v4f{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // a key's token (kNone: no row sees it); lanes 32.. repeat lanes 0..31
+  auto listed = [&](int st) {
+    if constexpr (LIST) {
+      const int at = st * 32 + (lane & 31);
+      return st < step_hi && at < p.width ? p.indices[(int64_t)unit * p.width + at] : -1;
+    } else {
+      return 0;
+    }
+  };
+  auto token = [&](int st, int x) -> uint32_t {
+    int pos;
+    if constexpr (LIST) {
+      if (x < 0 || x >= col_e[0] - col_s[0]) return kNone;
+      pos = col_s[0] + x;
+    } else {
+      pos = first + st * 32 + (lane & 31);
+      if (st >= step_hi || pos < lo || pos >= hi) return kNone;
+    }
+    return token_of(c, request, pos);
+  };
+  const uint8_t* const kbase = c.pages + code_at(c, 0, h, 0);
+  const uint8_t* const vbase = c.pages + code_at(c, 1, h, 0);
+  const uint32_t slot_mask = (1u << c.page_shift) - 1;
+  auto code_offset = [&](uint32_t tok) -> int64_t {
+    tok = tok == kNone ? 0u : tok;
+    return (int64_t)(tok >> c.page_shift) * c.page_stride + (tok & slot_mask) * D;
+  };
+  struct Step {
+    v4u k[2][KC];
+    uint32_t v[8][VW];
+    float ks, vs;   // of key lane % 32
+    uint32_t tok;   // of key lane % 32
+  };
+  auto load = [&](Step& s, uint32_t tok, int buf) {
+    s.tok = tok;
+    s_tok[wave][buf][lane & 31] = tok;
+    __builtin_amdgcn_wave_barrier();
+    const uint32_t t0 = tok == kNone ? 0u : tok;
+    const uint8_t* page = c.pages + (int64_t)(t0 >> c.page_shift) * c.page_stride;
+    s.ks = *reinterpret_cast<const float*>(page + scale_at(c, 0, h, t0 & slot_mask));
+    s.vs = *reinterpret_cast<const float*>(page + scale_at(c, 1, h, t0 & slot_mask));
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const uint8_t* at = kbase + code_offset(s_tok[wave][buf][16 * b + n]) + 16 * g;
+#pragma unroll
+      for (int k = 0; k < KC; ++k) s.k[b][k] = *reinterpret_cast<const v4u*>(at + 64 * k);
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const v4u four = *reinterpret_cast<const v4u*>(&s_tok[wave][buf][16 * b + 4 * g]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* at = vbase + code_offset(four[i]) + 4 * VW * n;
+        if constexpr (VW == 2) {
+          const uint2 x = *reinterpret_cast<const uint2*>(at);
+          s.v[4 * b + i][0] = x.x;
+          s.v[4 * b + i][1] = x.y;
+        } else {
+          s.v[4 * b + i][0] = *reinterpret_cast<const uint32_t*>(at);
+        }
+      }
+    }
+  };
+
+  auto compute = [&](Step& s, int st, int buf) {
+    const bool valid = s.tok != kNone;
+    s_ks[wave][lane & 31] = s.ks * cs;
+    s_vs[wave][lane & 31] = s.vs;
+    __builtin_amdgcn_wave_barrier();
+    const int pos0 = first + st * 32;
+    const bool clean = __all(valid) && (LIST || (pos0 >= in_lo && pos0 + 32 <= in_hi));
+    if (__any(valid && s.vs > vref && s.vs < __builtin_inff())) {
+      const float r =  // (at least the least normal number, whose inverse is one)
+          __builtin_fmaxf(wave_max(valid && s.vs < __builtin_inff() ? s.vs : 0.f), 0x1p-126f);
+      const float keep = vref / r;
+      vref = r;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < U; ++u) acc[t][u] *= keep;
+    }
+    v4f x[NT][2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      v4u kf[2 * KC];
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+        kf[2 * k] = widen8<T, C>(s.k[b][k][0], s.k[b][k][1]);
+        kf[2 * k + 1] = widen8<T, C>(s.k[b][k][2], s.k[b][k][3]);
+      }
+      const v4f f = *reinterpret_cast<const v4f*>(&s_ks[wave][16 * b + 4 * g]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        v4f a{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 2 * KC; ++k) a = mfma<T>(kf[k], q[t][k], a);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[t][b][i] = a[i] * f[i];
+      }
+    }
+    const float inv = vref > 0.f ? 1.f / vref : 0.f;
+    v4f vr[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      vr[b] = *reinterpret_cast<const v4f*>(&s_vs[wave][16 * b + 4 * g]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) vr[b][i] *= inv;
+    }
+    uint32_t seen[NT];  // bit 4 b + i
+    uint32_t poison = 0;
+    if (!clean) {
+      uint32_t live = 0;  // keys that some row sees
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const v4u four = *reinterpret_cast<const v4u*>(&s_tok[wave][buf][16 * b + 4 * g]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) live |= (four[i] != kNone ? 1u : 0u) << (4 * b + i);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        seen[t] = live;
+        if constexpr (!LIST) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int pos = pos0 + 16 * (j >> 2) + 4 * g + (j & 3);
+            if (pos < col_s[t] || pos >= col_e[t]) seen[t] &= ~(1u << j);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (!(seen[t] >> j & 1)) x[t][j >> 2][j & 3] = -__builtin_inff();
+      }
+      // values that no row sees become 0; a NaN code, which some rows may
+      // see and others not, becomes 0 too and is put back through the P of
+      // the rows that see it (0 * NaN would reach the others)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          if (!(live >> j & 1)) s.v[j][w] = 0;
+          if constexpr (C == kE4m3) {
+            const uint32_t b = nan_bytes(s.v[j][w]);
+            s.v[j][w] &= ~b;
+            bad |= b;
+          }
+        }
+        if constexpr (C == kE4m3) {
+          const uint64_t who = __ballot(bad != 0);
+          if (who >> (16 * g) & 0xFFFF) poison |= 1u << j;
+        }
+      }
+    }
+    v4u pf[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float top = x[t][0][0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) top = __builtin_fmaxf(top, x[t][j >> 2][j & 3]);
+      if (__any(top > m[t] + kLag)) {
+        top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
+        top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
+        const float to = __builtin_fmaxf(m[t], top);
+        const float keep = __builtin_amdgcn_exp2f(m[t] - to);
+        m[t] = to;
+        l[t] *= keep;
+#pragma unroll
+        for (int u = 0; u < U; ++u) acc[t][u] *= keep;
+      }
+      float pr[8];
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        pr[j] = __builtin_amdgcn_exp2f(x[t][j >> 2][j & 3] - (m[t] - kBias));
+        if (!clean && !(seen[t] >> j & 1)) pr[j] = 0.f;
+        sum += pr[j];
+        pr[j] *= vr[j >> 2][j & 3];
+        if (!clean) {
+          if (!(seen[t] >> j & 1)) pr[j] = 0.f;
+          else if (poison >> j & 1) pr[j] = __builtin_nanf("");
+        }
+      }
+      l[t] += sum;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        pf[t][i] = __builtin_bit_cast(uint32_t, v2h{(_Float16)pr[2 * i], (_Float16)pr[2 * i + 1]});
+    }
+#pragma unroll
+    for (int w = 0; w < VW; ++w) {
+      uint32_t in[4], a[4], b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) in[j] = s.v[j][w];
+      transpose4(in, a);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) in[j] = s.v[4 + j][w];
+      transpose4(in, b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const v4u vf = widen8<kFp16, C>(a[i], b[i]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[t][4 * w + i] = mfma<kFp16>(vf, pf[t], acc[t][4 * w + i]);
+      }
+    }
+  };
+
+  Step s0, s1;
+  int st = step_lo;
+  if (st < step_hi) {
+    uint32_t tok = token(st, listed(st));
+    int x = listed(st + 4);
+    load(s0, tok, 0);
+    tok = token(st + 4, x);
+    x = listed(st + 8);
+    while (true) {
+      load(s1, tok, 1);
+      tok = token(st + 8, x);
+      x = listed(st + 12);
+      compute(s0, st, 0);
+      st += 4;
+      if (st >= step_hi) break;
+      load(s0, tok, 0);
+      tok = token(st + 8, x);
+      x = listed(st + 12);
+      compute(s1, st, 1);
+      st += 4;
+      if (st >= step_hi) break;
+    }
+  }
+
+  // the four waves' sums to one reference point, a round of products at a time
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    l[t] += __shfl_xor(l[t], 16, 64);
+    l[t] += __shfl_xor(l[t], 32, 64);
+    if (g == 0) {
+      s_m[wave][16 * t + n] = m[t];
+      s_l[wave][16 * t + n] = l[t];
+    }
+  }
   __syncthreads();
-  int s = p.starts[row], e = p.ends[row];
-  s = s < 0 ? 0 : (s > c.cap ? c.cap : s);
-  e = e < s ? s : (e > c.cap ? c.cap : e);
-  const int n = p.indices ? p.width : e - s;
-  float m = -__builtin_inff(), sum = 0.f, acc[2] = {0.f, 0.f};
-  for (int at = 0; at < n; at += 64) {
-    bool seen = at + l < n;
-    int x = at + l;
-    if (p.indices && seen) {
-      x = p.indices[(int64_t)row * p.width + at + l];
-      seen = x >= 0 && x < e - s;
+  float part[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    float top = kLowest;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) top = __builtin_fmaxf(top, s_m[w][16 * t + n]);
+    part[t] = __builtin_amdgcn_exp2f(m[t] - top) * vref;
+  }
+  const int col = threadIdx.x % COLS;  // the column this thread writes
+  const int at_col = tile * COLS + col;
+  float top = kLowest, sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) top = __builtin_fmaxf(top, s_m[w][col]);
+#pragma unroll
+  for (int w = 0; w < 4; ++w) sum += s_l[w][col] * __builtin_amdgcn_exp2f(s_m[w][col] - top);
+  const bool real = at_col < columns;
+  const int row = unit * per_unit + (real ? at_col / p.group : 0);
+  const int head = h * p.group + (real ? at_col % p.group : 0);
+  const bool direct = p.splits == 1;
+  const float inv = direct ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+  const int64_t slot = block * COLS + col;
+  if (threadIdx.x < COLS) {
+    if (direct) {
+      if (real && p.lse)
+        p.lse[(int64_t)row * p.heads + head] =
+            sum == 0.f ? -__builtin_inff() : (top - kBias) * kLn2 + __builtin_logf(sum);
+    } else {
+      p.part_ml[2 * slot] = top;
+      p.part_ml[2 * slot + 1] = sum;
     }
-    const int pos = seen ? s + x : s;
-    float score = -__builtin_inff(), vs = 0.f;
-    if (seen) {
-      int page = c.table[(int64_t)request * c.table_stride + (pos >> c.page_shift)];
-      page = page < 0 ? 0 : (page >= c.num_pages ? c.num_pages - 1 : page);
-      const uint8_t* base = c.pages + (int64_t)page * c.page_stride;
-      const int slot = pos & ((1 << c.page_shift) - 1);
-      const uint8_t* k = base + code_at(c, 0, h, slot);
-      float dot = 0.f;
-      for (int d = 0; d < D; ++d) dot = __builtin_fmaf(q[d], code_value(k[d], c.codes), dot);
-      score = dot * *reinterpret_cast<const float*>(base + scale_at(c, 0, h, slot)) *
-              (p.scale * kLog2e);
-      vs = *reinterpret_cast<const float*>(base + scale_at(c, 1, h, slot));
-      vrow[l] = (int64_t)page * c.page_stride + code_at(c, 1, h, slot);
-    }
-    float top = score;
-    for (int o = 32; o >= 1; o >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o, 64));
-    top = __builtin_fmaxf(top, m);
-    const float ref = top == -__builtin_inff() ? 0.f : top;
-    const float keep = __builtin_amdgcn_exp2f(m - ref);
-    const float pr = seen ? __builtin_amdgcn_exp2f(score - ref) : 0.f;
-    float add = pr;
-    for (int o = 32; o >= 1; o >>= 1) add += __shfl_xor(add, o, 64);
-    sum = sum * keep + add;
-    m = top;
-    acc[0] *= keep;
-    acc[1] *= keep;
-    prob[l] = pr * vs;
-    const uint64_t live = __ballot(seen);
-    __syncthreads();
-    for (int j = 0; j < 64; ++j) {
-      if (!(live >> j & 1)) continue;
-      for (int i = 0; i < D / 64; ++i)
-        acc[i] = __builtin_fmaf(prob[j], code_value(c.pages[vrow[j] + l + 64 * i], c.codes), acc[i]);
+  }
+  for (int u0 = 0; u0 < U; u0 += US) {
+    if (u0) __syncthreads();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (u < u0 || u >= u0 + US) continue;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          s_part[wave][(u - u0) * 16 + 4 * g + i][16 * t + n] = acc[t][u][i] * part[t];
     }
     __syncthreads();
+    for (int i = threadIdx.x / COLS; i < US * 16; i += 256 / COLS) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) v += s_part[w][i][col];
+      const int d = U * (i & 15) + u0 + (i >> 4);
+      if (!direct)
+        p.part_o[slot * D + d] = v;
+      else if (real)
+        static_cast<uint16_t*>(p.out)[((int64_t)row * p.heads + head) * D + d] = to_type(v * inv, T);
+    }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  for (int i = 0; i < D / 64; ++i) {
-    const int64_t o = ((int64_t)row * p.heads + head) * D + l + 64 * i;
-    const float v = acc[i] * inv;
-    static_cast<uint16_t*>(p.out)[o] = p.dtype == kBf16 ? __builtin_bit_cast(uint16_t, (__bf16)v)
-                                                        : __builtin_bit_cast(uint16_t, (_Float16)v);
+}
+
+// Joins the splits of a (row, query head), in order: a thread a column of the
+// output. A split that saw nothing has l = 0 (and its sums are zero too).
+template <int T>
+__global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
+  const int D = p.c.head_dim;
+  const int64_t pair = (p.block0 + blockIdx.x) * (256 / D) + threadIdx.x / D;
+  if (pair >= (int64_t)p.rows * p.heads) return;
+  const int d = threadIdx.x % D;
+  const int row = (int)(pair / p.heads), head = (int)(pair % p.heads), h = head / p.group;
+  const int per_unit = p.indices ? 1 : p.R;
+  const int unit = row / per_unit;
+  const int column = row % per_unit * p.group + head % p.group;
+  const int64_t item = ((int64_t)unit * p.tiles + column / p.cols) * p.c.kv_heads + h;
+  const int64_t first = item * p.splits * p.cols + column % p.cols;
+  float top = kLowest;
+  for (int s = 0; s < p.splits; ++s)
+    top = __builtin_fmaxf(top, p.part_ml[2 * (first + (int64_t)s * p.cols)]);
+  float sum = 0.f, v = 0.f;
+  for (int s = 0; s < p.splits; ++s) {
+    const int64_t at = first + (int64_t)s * p.cols;
+    const float w = __builtin_amdgcn_exp2f(p.part_ml[2 * at] - top);
+    sum = __builtin_fmaf(p.part_ml[2 * at + 1], w, sum);
+    v = __builtin_fmaf(p.part_o[at * D + d], w, v);
   }
-  if (l == 0 && p.lse) p.lse[(int64_t)row * p.heads + head] = m * kLn2 + __builtin_logf(sum);
+  static_cast<uint16_t*>(p.out)[pair * D + d] = to_type(sum == 0.f ? 0.f : v / sum, T);
+  if (d == 0 && p.lse)
+    p.lse[pair] = sum == 0.f ? -__builtin_inff() : (top - kBias) * kLn2 + __builtin_logf(sum);
+}
+
+// A launch's grid stays below 2^32 threads: more workgroups go in several.
+template <class Launch>
+void in_pieces(AttendParams p, int64_t blocks, Launch launch) {
+  constexpr int64_t kMost = 1 << 22;
+  for (p.block0 = 0; p.block0 < blocks; p.block0 += kMost)
+    launch(p, dim3((unsigned)(blocks - p.block0 < kMost ? blocks - p.block0 : kMost)));
+}
+
+template <int T, int C, int D, int NT>
+void narrow(const AttendParams& all, hipStream_t s) {
+  const int64_t units = all.indices ? all.rows : all.requests;
+  in_pieces(all, units * all.tiles * all.c.kv_heads * all.splits,
+            [&](const AttendParams& p, dim3 grid) {
+              if (p.indices)
+                attend_narrow_kernel<T, C, D, NT, true><<<grid, 256, 0, s>>>(p);
+              else
+                attend_narrow_kernel<T, C, D, NT, false><<<grid, 256, 0, s>>>(p);
+            });
+  if (all.splits > 1) {
+    const int64_t pairs = (int64_t)all.rows * all.heads, per = 256 / D;
+    in_pieces(all, (pairs + per - 1) / per, [&](const AttendParams& p, dim3 grid) {
+      attend_join_kernel<T><<<grid, 256, 0, s>>>(p);
+    });
+  }
+}
+
+template <int T, int C, int D>
+void narrow_cols(const AttendParams& p, hipStream_t s) {
+  if (p.cols == 16) narrow<T, C, D, 1>(p, s);
+  if (p.cols == 32) narrow<T, C, D, 2>(p, s);
+  if (p.cols == 64) narrow<T, C, D, 4>(p, s);
+}
+
+template <int T, int C>
+void narrow_dim(const AttendParams& p, hipStream_t s) {
+  p.c.head_dim == 64 ? narrow_cols<T, C, 64>(p, s) : narrow_cols<T, C, 128>(p, s);
 }
 
 }  // namespace
 }  // namespace mqa
 
 extern "C" int mqa_attend_launch(const mqa::AttendParams* p, hipStream_t s) {
-  mqa::attend_wave_kernel<<<dim3(p->rows, p->heads), 64, 0, s>>>(*p);
+  using namespace mqa;
+  const bool e = p->c.codes == kE4m3;
+  if (p->dtype == kBf16) e ? narrow_dim<kBf16, kE4m3>(*p, s) : narrow_dim<kBf16, kInt8>(*p, s);
+  if (p->dtype == kFp16) e ? narrow_dim<kFp16, kE4m3>(*p, s) : narrow_dim<kFp16, kInt8>(*p, s);
   return (int)hipGetLastError();
 }

@@ -39,7 +39,8 @@ int cache_pointers(const mqa_kv_cache* c) {
 bool cache_shape(const mqa_kv_cache* c) {
   const int64_t n = page_bytes(c->kv_heads, c->head_dim, c->page_size, c->block);
   return n > 0 && c->page_stride >= n && c->page_stride < ((int64_t)1 << 40) && c->num_pages >= 1 &&
-         c->table_stride >= 1 && (c->codes == MQA_CODES_E4M3 || c->codes == MQA_CODES_INT8);
+         (int64_t)c->num_pages * c->page_size < ((int64_t)1 << 32) - 1 && c->table_stride >= 1 &&
+         (c->codes == MQA_CODES_E4M3 || c->codes == MQA_CODES_INT8);
 }
 
 KvCache kernel_cache(const mqa_kv_cache* c) {
@@ -62,6 +63,31 @@ KvCache kernel_cache(const mqa_kv_cache* c) {
 
 bool rows_ok(int requests, int R) {
   return requests >= 1 && R >= 1 && (int64_t)requests * R <= MQA_MAX_ROWS;
+}
+
+// How an attention call is cut (AttendParams), from what the host knows.
+struct Plan {
+  int cols, tiles, splits;
+  size_t ml, o, total;  // workspace offsets
+};
+
+Plan plan(int requests, int R, int heads, int kv_heads, int head_dim, int positions, bool list,
+          int cus) {
+  Plan a{};
+  const int group = heads / kv_heads, columns = list ? group : R * group;
+  a.cols = columns <= 16 ? 16 : (columns <= 32 ? 32 : 64);
+  a.tiles = (columns + a.cols - 1) / a.cols;
+  const int64_t items = (int64_t)(list ? requests * R : requests) * a.tiles * kv_heads;
+  // enough workgroups for the device, 256 keys in each at least
+  const int64_t want = ((int64_t)6 * cus + items - 1) / items, most = (positions + 255) / 256;
+  a.splits = (int)(want < most ? want : most);
+  a.splits = a.splits < 1 ? 1 : (a.splits > 64 ? 64 : a.splits);
+  const int64_t slots = a.splits > 1 ? items * a.splits * a.cols : 0;
+  a.ml = 0;
+  a.o = (size_t)((slots * 8 + 255) / 256 * 256);
+  a.total = a.o + (size_t)slots * head_dim * 4;
+  if (a.total == 0) a.total = 256;
+  return a;
 }
 
 int move(const mqa_kv_cache* cache, KvMoveParams& p, int (*launch)(const KvMoveParams*, hipStream_t),
@@ -89,9 +115,9 @@ int attend(const mqa_kv_cache* cache, const void* q, int64_t q_row, int64_t q_he
     return MQA_ERR_SHAPE;
   int device = -1;
   if (!mqa::current_device_cus() || hipGetDevice(&device) != hipSuccess) return MQA_ERR_DEVICE;
-  const size_t need = workspace_size_attend(requests, R, heads, cache->kv_heads, cache->head_dim,
-                                            positions, device);
-  if (need == 0 || workspace_bytes < need)
+  const Plan a = plan(requests, R, heads, cache->kv_heads, cache->head_dim, positions,
+                      indices != nullptr, mqa::device_cus(device));
+  if (workspace_bytes < a.total)
     return mqa::workspace_failed("the workspace is smaller than workspace_size_attend()");
   AttendParams p{};
   p.c = kernel_cache(cache);
@@ -111,6 +137,11 @@ int attend(const mqa_kv_cache* cache, const void* q, int64_t q_row, int64_t q_he
   p.group = heads / cache->kv_heads;
   p.dtype = dtype;
   p.scale = scale;
+  p.cols = a.cols;
+  p.tiles = a.tiles;
+  p.splits = a.splits;
+  p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + a.ml);
+  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + a.o);
   const int err = mqa_attend_launch(&p, static_cast<hipStream_t>(stream));
   return err != 0 ? mqa::launch_failed(err) : MQA_OK;
 }
@@ -179,7 +210,10 @@ size_t workspace_size_attend(int requests, int R, int heads, int kv_heads, int h
       heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128) || positions < 1 ||
       !mqa::device_cus(device))
     return 0;
-  return 256;
+  const int cus = mqa::device_cus(device);
+  const size_t range = plan(requests, R, heads, kv_heads, head_dim, positions, false, cus).total;
+  const size_t list = plan(requests, R, heads, kv_heads, head_dim, positions, true, cus).total;
+  return range > list ? range : list;
 }
 
 int mqa_attend_paged(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,

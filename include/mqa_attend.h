@@ -52,7 +52,7 @@ typedef struct mqa_kv_cache {
   const int32_t* table; /* [requests][table_stride] int32, 4-B aligned */
   int64_t page_stride;  /* bytes from a page to the next: a multiple of 16,
                            >= mqa_kv_page_bytes() */
-  int32_t num_pages;    /* >= 1 */
+  int32_t num_pages;    /* >= 1; num_pages * page_size < 2^32 - 1 */
   int32_t table_stride; /* >= 1 */
   int32_t kv_heads;     /* 1 .. MQA_MAX_ATTEND_HEADS */
   int32_t head_dim;     /* 64 or 128 */

@@ -76,10 +76,12 @@ Plan plan(int requests, int R, int heads, int kv_heads, int head_dim, int positi
   Plan a{};
   const int group = heads / kv_heads, columns = list ? group : R * group;
   a.cols = columns <= 16 ? 16 : (columns <= 32 ? 32 : 64);
+  if (!list && columns > 64) a.cols = columns <= 128 ? 128 : 256;
   a.tiles = (columns + a.cols - 1) / a.cols;
   const int64_t items = (int64_t)(list ? requests * R : requests) * a.tiles * kv_heads;
   // enough workgroups for the device, 256 keys in each at least
-  const int64_t want = ((int64_t)6 * cus + items - 1) / items, most = (positions + 255) / 256;
+  const int64_t want = ((int64_t)(a.cols > 64 ? 1 : 6) * cus + items - 1) / items;
+  const int64_t most = (positions + 255) / 256;
   a.splits = (int)(want < most ? want : most);
   a.splits = a.splits < 1 ? 1 : (a.splits > 64 ? 64 : a.splits);
   const int64_t slots = a.splits > 1 ? items * a.splits * a.cols : 0;

@@ -15,6 +15,8 @@
 // lazily: m only when a score passes it by more than 8 (P <= 2^15 until then),
 // vref when a larger scale is met; both times the sums are rescaled. l sums the
 // fp32 P before its rounding.
+#include <type_traits>
+
 #include "attend.h"
 #include "launch.h"
 
@@ -537,17 +539,14 @@ __global__ __launch_bounds__(256, NT == 4 ? 1 : 2) void attend_narrow_kernel(Att
 }
 
 // ---------------------------------------------------------------------------
-// Many columns: 128 NQ columns of one request and key head per workgroup, 32
-// NQ in each of its four waves, every wave over all keys of the workgroup's
-// part. Tiles of 64 keys pass through LDS once for the workgroup, widened on
-// the way in: keys as [key][d], values transposed as [d][key] in the order in
-// which a lane holds its scores, both with 16-byte slots exchanged so that
-// the 32 lanes of a read touch all banks.
+// Many columns: 32 W columns of one request and key head per workgroup, 32 in
+// each of its W waves, every wave over all keys of the workgroup's part. Tiles
+// of 64 keys pass through LDS once for the workgroup, widened on the way in:
+// keys as [key][d], values transposed as [d][key] in the order in which a lane
+// holds its scores, both with rows padded by 16 bytes so that 16 lanes of a
+// read touch all banks.
 //   S^T = K Q^T   32 keys x 32 columns per v_mfma_f32_32x32x16, Q in registers
 //   O^T += V^T P^T   P straight from the scores' registers
-// With 32 NQ = 64 columns a wave reads each operand from LDS once for two
-// products, half of what LDS can deliver in the products' time; with 32 it
-// would be all of it.
 //
 // Half tiles j = 0, 1, .. run as a pipeline inside the wave: the products of
 // S(j + 1) and of P(j - 1) V are independent of the exponentials of S(j), so
@@ -556,13 +555,14 @@ __global__ __launch_bounds__(256, NT == 4 ? 1 : 2) void attend_narrow_kernel(Att
 // LDS; its values follow during the second half and are first read after the
 // next barrier. m and vref only move by powers of two, so that the P in flight
 // can be rescaled exactly.
-template <int T, int C, int D, int NQ>
-__global__ __launch_bounds__(256, 1) void attend_wide_kernel(AttendParams p) {
+template <int T, int C, int D, int W>
+__global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) {
+  constexpr int THREADS = 64 * W;
   constexpr int KS = D / 16;          // products a half's scores take
   constexpr int DT = D / 32;          // tiles of the output's columns
-  constexpr int KCH = D / 64;         // 16-byte pieces of keys a thread stages
-  constexpr int KSLOTS = D / 8;       // 16-byte slots of a staged key
-  constexpr int WCOLS = 32 * NQ, COLS = 4 * WCOLS;
+  constexpr int PIECES = 4 * D;       // 16-byte pieces of a tile's keys; 4 x 4 pieces of its values
+  constexpr int EACH = (PIECES + THREADS - 1) / THREADS;  // of each, per thread
+  constexpr int COLS = 32 * W;
   const KvCache& c = p.c;
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int hh = lane >> 5, n = lane & 31;
@@ -575,17 +575,18 @@ __global__ __launch_bounds__(256, 1) void attend_wide_kernel(AttendParams p) {
   const int tile = p.tiles - 1 - (int)(item / c.kv_heads % p.tiles);
   const int columns = p.R * p.group;
 
-  __shared__ __align__(16) uint8_t s_k[2][64 * D * 2];
-  __shared__ __align__(16) uint8_t s_v[2][64 * D * 2];
-  __shared__ __align__(16) float s_scale[2][8];
+  constexpr int KROW = 2 * D + 16, VROW = 2 * 64 + 16;  // bytes of a staged key, of a column
+  __shared__ __align__(16) uint8_t s_k[2][64 * KROW];
+  __shared__ __align__(16) uint8_t s_v[2][D * VROW];
+  __shared__ __align__(16) float s_scale[2][THREADS];  // 8 scales, over and over
   __shared__ uint32_t s_poison[3][2];
-  __shared__ int s_range[4][4];
+  __shared__ int s_range[4][W];
 
   const int row_lo = unit * p.R + tile * COLS / p.group;
   const int last = tile * COLS + COLS < columns ? tile * COLS + COLS : columns;
   const int row_hi = unit * p.R + (last - 1) / p.group;
   int lo = c.cap, hi = 0, in_lo = 0, in_hi = c.cap;  // seen by some row, seen by every row
-  for (int r = row_lo + t; r <= row_hi; r += 256) {
+  for (int r = row_lo + t; r <= row_hi; r += THREADS) {
     int s, e;
     row_range(p, r, s, e);
     if (s < e) {  // (rows that see nothing are left out)
@@ -609,9 +610,12 @@ __global__ __launch_bounds__(256, 1) void attend_wide_kernel(AttendParams p) {
     s_range[3][wave] = in_hi;
   }
   if (t < 6) s_poison[t >> 1][t & 1] = 0;
+  // the first half adds no values: P = 0 times what is staged "before" them
+  for (int x = t; x < D * VROW / 16; x += THREADS)
+    reinterpret_cast<v4u*>(s_v[1])[x] = v4u{0, 0, 0, 0};
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < W; ++w) {
     lo = min(lo, s_range[0][w]);
     hi = max(hi, s_range[1][w]);
     in_lo = max(in_lo, s_range[2][w]);
@@ -622,21 +626,20 @@ __global__ __launch_bounds__(256, 1) void attend_wide_kernel(AttendParams p) {
   in_lo = __builtin_amdgcn_readfirstlane(in_lo);
   in_hi = __builtin_amdgcn_readfirstlane(in_hi);
 
-  // this wave's columns
-  int col_s[NQ], col_e[NQ];
-  v4u q[NQ][KS];
-#pragma unroll
-  for (int a = 0; a < NQ; ++a) {
-    const int col = tile * COLS + wave * WCOLS + 32 * a + n;
-    const bool real = col < columns;
-    const int row = unit * p.R + (real ? col / p.group : 0);
-    const int head = h * p.group + (real ? col % p.group : 0);
-    row_range(p, row, col_s[a], col_e[a]);
+  // this lane's column
+  const int at_col = wave * 32 + n, col = tile * COLS + at_col;
+  const bool real = col < columns;
+  const int row = unit * p.R + (real ? col / p.group : 0);
+  const int head = h * p.group + (real ? col % p.group : 0);
+  int col_s, col_e;
+  row_range(p, row, col_s, col_e);
+  v4u q[KS];
+  {
     const uint16_t* src = static_cast<const uint16_t*>(p.q) + row * p.q_row + head * p.q_head;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
-      q[a][k] = *reinterpret_cast<const v4u*>(src + 16 * k + 8 * hh);
-      if (!real) q[a][k] = v4u{0, 0, 0, 0};
+      q[k] = *reinterpret_cast<const v4u*>(src + 16 * k + 8 * hh);
+      if (!real) q[k] = v4u{0, 0, 0, 0};
     }
   }
 
@@ -649,10 +652,14 @@ __global__ __launch_bounds__(256, 1) void attend_wide_kernel(AttendParams p) {
   const int tiles = min(all - tile_lo, per_split);
   const int base = first + tile_lo * 64;
 
-  // staging: thread t takes KCH pieces of keys, and four columns of eight
-  // values (threads below 2 D): the order of keys 16 g + 4 h + {0..3, 8..11}
-  const int v_kg = t / (D / 4), v_d = t % (D / 4) * 4;
-  const bool v_mine = t < 2 * D;
+  // staging: piece x = t + THREADS r of the keys is 16 bytes of key x / (D /
+  // 16); of the values, columns 4 (x % (D / 4)) .. + 3 of keys 4 y .. 4 y + 3,
+  // y = x / (D / 4)
+  auto piece = [&](int r) { return t + THREADS * r; };
+  auto mine = [&](int r) { return PIECES % THREADS == 0 || piece(r) < PIECES; };
+  auto k_key = [&](int r) { return piece(r) / (D / 16); };
+  auto v_key = [&](int r) { return piece(r) / (D / 4) * 4; };
+  auto v_d = [&](int r) { return piece(r) % (D / 4) * 4; };
   auto group_page = [&](int i, int g) -> int {  // page of group g of tile i; -1: no row sees it
     const int pos = base + i * 64 + 16 * g;
     if (i >= tiles || pos >= hi || pos + 16 <= lo) return -1;
@@ -663,174 +670,168 @@ __global__ __launch_bounds__(256, 1) void attend_wide_kernel(AttendParams p) {
   auto slot_of = [&](int i, int key) {
     return (base + i * 64 + key) & ((1 << c.page_shift) - 1);
   };
-  auto k_key = [&](int r) { return (t + 256 * r) / (D / 16); };
-  v4u kreg[KCH];
-  uint32_t vreg[8];
+  v4u kreg[EACH];
+  uint32_t vreg[EACH][4];
   float sreg = 0.f;
-  int kpage[KCH], vpage, spage;
+  int kpage[EACH], vpage[EACH], spage;
   auto find_k = [&](int i) {
 #pragma unroll
-    for (int r = 0; r < KCH; ++r) kpage[r] = group_page(i, k_key(r) >> 4);
-    spage = t < 8 ? group_page(i, t & 3) : -1;
+    for (int r = 0; r < EACH; ++r) kpage[r] = mine(r) ? group_page(i, k_key(r) >> 4) : -1;
+    spage = group_page(i, t & 3);
   };
-  auto find_v = [&](int i) { vpage = group_page(i, v_kg >> 1); };
+  auto find_v = [&](int i) {
+#pragma unroll
+    for (int r = 0; r < EACH; ++r) vpage[r] = mine(r) ? group_page(i, v_key(r) >> 4) : -1;
+  };
   auto load_k = [&](int i) {
 #pragma unroll
-    for (int r = 0; r < KCH; ++r)
+    for (int r = 0; r < EACH; ++r)
       kreg[r] = *reinterpret_cast<const v4u*>(
           page_at(kpage[r]) + code_at(c, 0, h, kpage[r] < 0 ? 0 : slot_of(i, k_key(r))) +
-          16 * ((t + 256 * r) % (D / 16)));
-    if (t < 8)
-      sreg = spage < 0 ? 0.f
-                       : *reinterpret_cast<const float*>(
-                             page_at(spage) + scale_at(c, t >> 2, h, slot_of(i, 16 * (t & 3))));
+          16 * (piece(r) % (D / 16)));
+    const float x = *reinterpret_cast<const float*>(
+        page_at(spage) + scale_at(c, t >> 2 & 1, h, spage < 0 ? 0 : slot_of(i, 16 * (t & 3))));
+    sreg = spage < 0 ? 0.f : x;
   };
   auto load_v = [&](int i) {
-    if (!v_mine) return;
-    const uint8_t* at = page_at(vpage) +
-                        code_at(c, 1, h, vpage < 0 ? 0 : slot_of(i, 16 * (v_kg >> 1) + 4 * (v_kg & 1))) +
-                        v_d;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      vreg[j] = *reinterpret_cast<const uint32_t*>(at + (j < 4 ? j : j + 4) * D);
+    for (int r = 0; r < EACH; ++r) {
+      const uint8_t* at =
+          page_at(vpage[r]) + code_at(c, 1, h, vpage[r] < 0 ? 0 : slot_of(i, v_key(r))) + v_d(r);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) vreg[r][j] = *reinterpret_cast<const uint32_t*>(at + j * D);
+    }
   };
-  auto k_slot = [&](int key, int slot) {
-    return key * (D * 2) + 16 * (slot ^ (D == 128 ? key & 15 : (key >> 1) & 7));
-  };
-  auto v_slot = [&](int d, int slot) { return d * 128 + 16 * (slot ^ (((d >> 1) ^ (d >> 4)) & 7)); };
+  auto k_slot = [&](int key, int slot) { return key * KROW + 16 * slot; };
+  auto v_slot = [&](int d, int slot) { return d * VROW + 16 * slot; };
   auto inside = [&](int i) {  // every row sees every key of tile i
     return base + i * 64 >= in_lo && base + i * 64 + 64 <= in_hi;
   };
   auto stage_k = [&](int i) {
     uint8_t* const to = s_k[i & 1];
 #pragma unroll
-    for (int r = 0; r < KCH; ++r) {
-      const int key = k_key(r), piece = (t + 256 * r) % (D / 16);
-      *reinterpret_cast<v4u*>(to + k_slot(key, 2 * piece)) = widen8<T, C>(kreg[r][0], kreg[r][1]);
-      *reinterpret_cast<v4u*>(to + k_slot(key, 2 * piece + 1)) =
+    for (int r = 0; r < EACH; ++r) {
+      if (!mine(r)) continue;
+      const int x = piece(r) % (D / 16);
+      *reinterpret_cast<v4u*>(to + k_slot(k_key(r), 2 * x)) = widen8<T, C>(kreg[r][0], kreg[r][1]);
+      *reinterpret_cast<v4u*>(to + k_slot(k_key(r), 2 * x + 1)) =
           widen8<T, C>(kreg[r][2], kreg[r][3]);
     }
-    if (t < 8) s_scale[i & 1][t] = sreg;
+    s_scale[i & 1][t] = sreg;
   };
   // values that no row sees become 0; a NaN code, which some rows may see and
   // others not, becomes 0 too and is put back through the P of the rows that
   // see it (0 * NaN would reach the others)
   auto clean_v = [&](int i) {
     if (t == 0) s_poison[(i + 1) % 3][0] = s_poison[(i + 1) % 3][1] = 0;
-    if (inside(i) || !v_mine) return;
+    if (inside(i)) return;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int key = 16 * (v_kg >> 1) + 4 * (v_kg & 1) + (j < 4 ? j : j + 4);
-      const int pos = base + i * 64 + key;
-      if (i >= tiles || pos < lo || pos >= hi) vreg[j] = 0;
-      if constexpr (C == kE4m3) {
-        const uint32_t bad = nan_bytes(vreg[j]);
-        if (bad) {
-          vreg[j] &= ~bad;
-          atomicOr(&s_poison[i % 3][key >> 5], 1u << (key & 31));
+    for (int r = 0; r < EACH; ++r) {
+      if (!mine(r)) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int key = v_key(r) + j, pos = base + i * 64 + key;
+        if (i >= tiles || pos < lo || pos >= hi) vreg[r][j] = 0;
+        if constexpr (C == kE4m3) {
+          const uint32_t bad = nan_bytes(vreg[r][j]);
+          if (bad) {
+            vreg[r][j] &= ~bad;
+            atomicOr(&s_poison[i % 3][key >> 5], 1u << (key & 31));
+          }
         }
       }
     }
   };
+  // keys 16 g + {0..3, 8..11} share slot 2 g, {4..7, 12..15} slot 2 g + 1
   auto stage_v = [&](int i) {
-    if (!v_mine) return;
-    uint32_t a[4], b[4];
-    transpose4(vreg, a);
-    transpose4(vreg + 4, b);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<v4u*>(s_v[i & 1] + v_slot(v_d + j, v_kg)) = widen8<kFp16, C>(a[j], b[j]);
+    for (int r = 0; r < EACH; ++r) {
+      if (!mine(r)) continue;
+      uint32_t a[4];
+      transpose4(vreg[r], a);
+      const int y = v_key(r) >> 2, slot = 2 * (y >> 2) + (y & 1), half = y >> 1 & 1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint2*>(s_v[i & 1] + v_slot(v_d(r) + j, slot) + 8 * half) =
+            widen4<kFp16, C>(a[j]);
+    }
   };
 
   const float cs = p.scale * kLog2e;
-  float m[NQ], l[NQ], vref = 0x1p-126f;
-  v16f acc[NQ][DT];
+  float m = kLowest, l = 0.f, vref = 0x1p-126f;
+  v16f acc[DT];
 #pragma unroll
-  for (int a = 0; a < NQ; ++a) {
-    m[a] = kLowest;
-    l[a] = 0.f;
-#pragma unroll
-    for (int d = 0; d < DT; ++d) acc[a][d] = v16f{};
-  }
-  struct Half {
-    v16f x[NQ];
-  };
+  for (int d = 0; d < DT; ++d) acc[d] = v16f{};
   struct Prob {
-    v4u f[NQ][2];  // of keys 16 g + ..
+    v4u f[2];  // of the half's two groups of keys
   };
-  // scales of the current tile, per group of 16 keys
-  float fk[4], vs[4], vr[4], lv[4], iv[4];
+  // of the current tile, per group of 16 keys (the same in all lanes): the
+  // factor of the scores; vs / vref, its logarithm + kBias and its inverse
+  float fk[4], vr[4], lv[4], iv[4];
   uint32_t poison[2] = {0, 0};
   bool plain = false;  // every row sees every key, and the scales are ordinary
 
-  auto derive = [&]() {
+  auto uniform = [](float x) {
+    return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
+  };
+  auto rescale_pending = [&](Prob& pr, float keep) {
+    const _Float16 k16 = (_Float16)keep;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      vr[g] = vs[g] / vref;
-      lv[g] = __builtin_amdgcn_logf(vr[g]) + kBias;
-      iv[g] = 1.f / vr[g];
-    }
+    for (int k = 0; k < 2; ++k)
+      pr.f[k] = __builtin_bit_cast(v4u, __builtin_bit_cast(v8h, pr.f[k]) * k16);
   };
   auto take_scales = [&](int i, Prob& pending) {
     const float* s = s_scale[i & 1];
-    float most = 0.f;
-    bool ordinary = true;
+    float most = 0.f, vs[4];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      fk[g] = s[g] * cs;
-      vs[g] = s[4 + g];
+      fk[g] = uniform(s[g] * cs);
+      vs[g] = uniform(s[4 + g]);
       most = vs[g] < __builtin_inff() ? __builtin_fmaxf(most, vs[g]) : most;
     }
-    if (most > vref) {  // (the same for all lanes)
+    if (most > vref) {
       const uint32_t u = __float_as_uint(most);
       const float to = __uint_as_float((u & 0x7FFFFFu) ? (u & 0x7F800000u) + 0x800000u : u);
       const float keep = vref / to;
-      const _Float16 k16 = (_Float16)keep;
 #pragma unroll
-      for (int a = 0; a < NQ; ++a) {
-#pragma unroll
-        for (int d = 0; d < DT; ++d) acc[a][d] *= keep;
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          pending.f[a][k] =
-              __builtin_bit_cast(v4u, __builtin_bit_cast(v8h, pending.f[a][k]) * k16);
-      }
-      vref = to;
+      for (int d = 0; d < DT; ++d) acc[d] *= keep;
+      rescale_pending(pending, keep);
+      vref = uniform(to);
     }
-    derive();
+    bool ordinary = true;
+    const float down = 1.f / vref;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) ordinary = ordinary && vr[g] >= 0x1p-60f && vr[g] <= 1.f;
+    for (int g = 0; g < 4; ++g) {
+      vr[g] = uniform(vs[g] * down);
+      lv[g] = uniform(__builtin_amdgcn_logf(vr[g]) + kBias);
+      iv[g] = uniform(__builtin_amdgcn_rcpf(vr[g]));
+      ordinary = ordinary && vr[g] >= 0x1p-60f && vr[g] <= 1.f;
+    }
     poison[0] = s_poison[i % 3][0];
     poison[1] = s_poison[i % 3][1];
-    plain = __builtin_amdgcn_readfirstlane((int)(ordinary && inside(i)));
+    plain = ordinary && inside(i);
   };
-  auto scores = [&](Half& s, int i, int half) {
-    const uint8_t* const from = s_k[i & 1];
+  auto scores = [&](v16f& s, int i, int half) {
+    const uint8_t* const from = s_k[i & 1] + k_slot(n, hh);
+    s = v16f{};
 #pragma unroll
-    for (int a = 0; a < NQ; ++a) s.x[a] = v16f{};
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const v4u kf = *reinterpret_cast<const v4u*>(from + k_slot(32 * half + n, 2 * k + hh));
-#pragma unroll
-      for (int a = 0; a < NQ; ++a) s.x[a] = mfma32<T>(kf, q[a][k], s.x[a]);
-    }
+    for (int k = 0; k < KS; ++k)
+      s = mfma32<T>(*reinterpret_cast<const v4u*>(from + k_slot(32 * half, 2 * k)), q[k], s);
   };
   auto values = [&](const Prob& pr, int i, int half) {
-    const uint8_t* const from = s_v[i & 1];
+    const uint8_t* const from = s_v[i & 1] + v_slot(n, hh);
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        const v4u vf =
-            *reinterpret_cast<const v4u*>(from + v_slot(32 * d + n, 2 * (2 * half + k) + hh));
-#pragma unroll
-        for (int a = 0; a < NQ; ++a) acc[a][d] = mfma32<kFp16>(vf, pr.f[a][k], acc[a][d]);
-      }
+      for (int d = 0; d < DT; ++d)
+        acc[d] = mfma32<kFp16>(
+            *reinterpret_cast<const v4u*>(from + v_slot(32 * d, 2 * (2 * half + k))), pr.f[k],
+            acc[d]);
   };
   // bit 8 (e / 4) + e % 4: whether the column sees the key of its score e
-  auto seen_keys = [&](int a, int i, int half) -> uint32_t {
+  auto seen_keys = [&](int i, int half) -> uint32_t {
     const int pos = base + i * 64 + 32 * half;
-    const int from = max(col_s[a] - pos, 0), to = min(col_e[a] - pos, 32);
+    const int from = max(col_s - pos, 0), to = min(col_e - pos, 32);
     if (from >= to) return 0u;
     return (~0u << from & ~0u >> (32 - to)) >> (4 * hh);
   };
@@ -838,31 +839,31 @@ __global__ __launch_bounds__(256, 1) void attend_wide_kernel(AttendParams p) {
   auto bit = [&](uint32_t mask, int e) -> uint32_t {
     return (uint32_t)__builtin_amdgcn_sbfe((int)mask, 8 * (e >> 2) + (e & 3), 1);
   };
-  // scores -> probabilities of one half
-  auto soft = [&](const Half& s, Prob& pr, int half) {
+  auto pack = [&](const float* e) {
+    v4u f;
 #pragma unroll
-    for (int a = 0; a < NQ; ++a)
+    for (int j = 0; j < 4; ++j)
+      f[j] = __builtin_bit_cast(uint32_t, v2h{(_Float16)e[2 * j], (_Float16)e[2 * j + 1]});
+    return f;
+  };
+  // scores -> probabilities of one half
+  auto soft = [&](auto is_plain, const v16f& s, Prob& pr, int i, int half) {
+    if constexpr (is_plain.value) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int g = 2 * half + k;
-        const float off = lv[g] - m[a];
+        const float off = lv[g] - m;
         float e[8], sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s.x[a][8 * k + j], fk[g], off));
+          e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * k + j], fk[g], off));
           sum += e[j];
         }
-        l[a] = __builtin_fmaf(sum, iv[g], l[a]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          pr.f[a][k][j] =
-              __builtin_bit_cast(uint32_t, v2h{(_Float16)e[2 * j], (_Float16)e[2 * j + 1]});
+        l = __builtin_fmaf(sum, iv[g], l);
+        pr.f[k] = pack(e);
       }
-  };
-  auto soft_any = [&](const Half& s, Prob& pr, int i, int half) {
-#pragma unroll
-    for (int a = 0; a < NQ; ++a) {
-      const uint32_t sees = seen_keys(a, i, half), ill = sees & (poison[half] >> (4 * hh));
+    } else {
+      const uint32_t sees = seen_keys(i, half), ill = sees & (poison[half] >> (4 * hh));
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int g = 2 * half + k;
@@ -870,72 +871,61 @@ __global__ __launch_bounds__(256, 1) void attend_wide_kernel(AttendParams p) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {  // (masks by bits: what is unseen may be NaN)
           const uint32_t see = bit(sees, 8 * k + j);
-          const float x = __builtin_amdgcn_exp2f(
-              __builtin_fmaf(s.x[a][8 * k + j], fk[g], -(m[a] - kBias)));
+          const float x =
+              __builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * k + j], fk[g], -(m - kBias)));
           const float y = __uint_as_float(__float_as_uint(x) & see);
-          l[a] += y;
+          l += y;
           e[j] = __uint_as_float((__float_as_uint(y * vr[g]) & see) |
                                  (bit(ill, 8 * k + j) & 0x7FC00000u));
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          pr.f[a][k][j] =
-              __builtin_bit_cast(uint32_t, v2h{(_Float16)e[2 * j], (_Float16)e[2 * j + 1]});
+        pr.f[k] = pack(e);
       }
+    }
+  };
+  // a half's largest score in this lane
+  auto largest = [&](auto is_plain, const v16f& s, int i, int half) {
+    if constexpr (is_plain.value) {
+      float x = s[0], y = s[8];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) {
+        x = __builtin_fmaxf(x, s[j]);
+        y = __builtin_fmaxf(y, s[8 + j]);
+      }
+      return __builtin_fmaxf(x * fk[2 * half], y * fk[2 * half + 1]);
+    } else {
+      const uint32_t sees = seen_keys(i, half);
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const uint32_t see = bit(sees, e);
+        const float x = s[e] * fk[2 * half + (e >> 3)];
+        top = __builtin_fmaxf(
+            top, __uint_as_float((__float_as_uint(x) & see) | (~see & 0xFF800000u)));
+      }
+      return top;
     }
   };
   // moves m where a score passes it by more than kLag; `pending`: the P not
   // yet in the sums
-  auto settle = [&](const Half& s, Prob& pending, int i, int half) {
-    float top[NQ];
-    bool any = false;
+  auto settle = [&](float top, Prob& pending) {
+    if (!__any(top > m + kLag)) return;
+    const float x = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
+    const float to = __builtin_fmaxf(m, __builtin_ceilf(x));
+    const float keep = __builtin_amdgcn_exp2f(m - to);
+    m = to;
+    l *= keep;
 #pragma unroll
-    for (int a = 0; a < NQ; ++a) {
-      if (plain) {
-        float x = s.x[a][0], y = s.x[a][8];
-#pragma unroll
-        for (int j = 1; j < 8; ++j) {
-          x = __builtin_fmaxf(x, s.x[a][j]);
-          y = __builtin_fmaxf(y, s.x[a][8 + j]);
-        }
-        top[a] = __builtin_fmaxf(x * fk[2 * half], y * fk[2 * half + 1]);
-      } else {
-        const uint32_t sees = seen_keys(a, i, half);
-        top[a] = -__builtin_inff();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const uint32_t see = bit(sees, e);
-          const float x = s.x[a][e] * fk[2 * half + (e >> 3)];
-          top[a] = __builtin_fmaxf(
-              top[a], __uint_as_float((__float_as_uint(x) & see) | (~see & 0xFF800000u)));
-        }
-      }
-      any = any || top[a] > m[a] + kLag;
-    }
-    if (!__any(any)) return;
-#pragma unroll
-    for (int a = 0; a < NQ; ++a) {
-      const float x = __builtin_fmaxf(top[a], __shfl_xor(top[a], 32, 64));
-      const float to = __builtin_fmaxf(m[a], __builtin_ceilf(x));
-      const float keep = __builtin_amdgcn_exp2f(m[a] - to);
-      const _Float16 k16 = (_Float16)keep;
-      m[a] = to;
-      l[a] *= keep;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) acc[a][d] *= keep;
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        pending.f[a][k] = __builtin_bit_cast(v4u, __builtin_bit_cast(v8h, pending.f[a][k]) * k16);
-    }
+    for (int d = 0; d < DT; ++d) acc[d] *= keep;
+    rescale_pending(pending, keep);
   };
 
   if (tiles > 0) {
-    Half s0, s1;
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    v16f s0, s1;
     Prob p0, p1;
 #pragma unroll
-    for (int a = 0; a < NQ; ++a)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) p0.f[a][k] = p1.f[a][k] = v4u{0, 0, 0, 0};
+    for (int k = 0; k < 2; ++k) p0.f[k] = p1.f[k] = v4u{0, 0, 0, 0};
     find_k(0);
     find_v(0);
     load_k(0);
@@ -952,81 +942,86 @@ __global__ __launch_bounds__(256, 1) void attend_wide_kernel(AttendParams p) {
     __syncthreads();
     take_scales(0, p0);
     scores(s0, 0, 0);
-    settle(s0, p0, 0, 0);
-    for (int i = 0; i < tiles; ++i) {
-      // first half: s0 -> p0, scores of the second, values of the last tile's
-      // second
+    settle(plain ? largest(yes, s0, 0, 0) : largest(no, s0, 0, 0), p0);
+    // first half: s0 -> p0, scores of the second, values of the last tile's
+    // second; keys of the next tile into LDS
+    auto half0 = [&](auto is_plain, int i) {
       scores(s1, i, 1);
-      if (plain)
-        soft(s0, p0, 0);
-      else
-        soft_any(s0, p0, i, 0);
-      if (i > 0) values(p1, i - 1, 1);
-      settle(s1, p0, i, 1);
+      soft(is_plain, s0, p0, i, 0);
+      values(p1, i - 1, 1);
       stage_k(i + 1);
-      clean_v(i + 1);
       load_k(i + 2);
-      find_k(i + 3);
-      __syncthreads();
-      // second half: s1 -> p1, scores of the next tile's first, values of
-      // this tile's first
+      settle(largest(is_plain, s1, i, 1), p0);
+    };
+    // second half: s1 -> p1, scores of the next tile's first, values of this
+    // tile's first; values of the next tile into LDS
+    auto half1 = [&](auto is_plain, int i) {
       scores(s0, i + 1, 0);
-      if (plain)
-        soft(s1, p1, 1);
-      else
-        soft_any(s1, p1, i, 1);
+      soft(is_plain, s1, p1, i, 1);
       values(p0, i, 0);
       stage_v(i + 1);
       load_v(i + 2);
+    };
+    for (int i = 0; i < tiles; ++i) {
+      if (plain) {
+        asm volatile("; plain" ::: "memory");
+        half0(yes, i);
+      } else {
+        asm volatile("; any" ::: "memory");
+        half0(no, i);
+      }
+      clean_v(i + 1);
+      find_k(i + 3);
+      __syncthreads();
+      if (plain) {
+        asm volatile("; plain" ::: "memory");
+        half1(yes, i);
+      } else {
+        asm volatile("; any" ::: "memory");
+        half1(no, i);
+      }
       find_v(i + 3);
       if (i + 1 < tiles) {
         take_scales(i + 1, p1);
-        settle(s0, p1, i + 1, 0);
+        settle(plain ? largest(yes, s0, i + 1, 0) : largest(no, s0, i + 1, 0), p1);
       }
     }
     values(p1, tiles - 1, 1);
   }
 
   const bool direct = p.splits == 1;
+  const float both = l + __shfl_xor(l, 32, 64);
+  const float sum = col_s >= col_e ? 0.f : both;  // (sums of a row that sees nothing)
+  const int64_t slot = (((int64_t)unit * p.tiles + tile) * c.kv_heads + h) * p.splits * COLS +
+                       (int64_t)split * COLS + at_col;
+  if (!real) return;
+  if (hh == 0) {
+    if (!direct) {
+      p.part_ml[2 * slot] = m;
+      p.part_ml[2 * slot + 1] = sum;
+    } else if (p.lse) {
+      p.lse[(int64_t)row * p.heads + head] =
+          sum == 0.f ? -__builtin_inff() : (m - kBias) * kLn2 + __builtin_logf(sum);
+    }
+  }
+  const float by = direct ? vref / sum : vref;
 #pragma unroll
-  for (int a = 0; a < NQ; ++a) {
-    const int at_col = wave * WCOLS + 32 * a + n, col = tile * COLS + at_col;
-    const bool none = col_s[a] >= col_e[a];  // sums of a row that sees nothing
-    const float both = l[a] + __shfl_xor(l[a], 32, 64);
-    const float sum = none ? 0.f : both;
-    const int64_t slot =
-        (((int64_t)unit * p.tiles + tile) * c.kv_heads + h) * p.splits * COLS +
-        (int64_t)split * COLS + at_col;
-    if (col >= columns) continue;
-    const int row = unit * p.R + col / p.group, head = h * p.group + col % p.group;
-    if (hh == 0) {
-      if (!direct) {
-        p.part_ml[2 * slot] = m[a];
-        p.part_ml[2 * slot + 1] = sum;
-      } else if (p.lse) {
-        p.lse[(int64_t)row * p.heads + head] =
-            sum == 0.f ? -__builtin_inff() : (m[a] - kBias) * kLn2 + __builtin_logf(sum);
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int at = 32 * d + 8 * e + 4 * hh;
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = sum == 0.f ? 0.f : acc[d][4 * e + j] * by;
+      if (direct) {
+        const uint32_t x = to_type(v[0], T) | (uint32_t)to_type(v[1], T) << 16;
+        const uint32_t y = to_type(v[2], T) | (uint32_t)to_type(v[3], T) << 16;
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) +
+                                  ((int64_t)row * p.heads + head) * D + at) = uint2{x, y};
+      } else {
+        *reinterpret_cast<float4*>(p.part_o + slot * D + at) = float4{v[0], v[1], v[2], v[3]};
       }
     }
-    const float by = direct ? vref / sum : vref;
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int at = 32 * d + 8 * e + 4 * hh;
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = sum == 0.f ? 0.f : acc[a][d][4 * e + j] * by;
-        if (direct) {
-          const uint32_t x = to_type(v[0], T) | (uint32_t)to_type(v[1], T) << 16;
-          const uint32_t y = to_type(v[2], T) | (uint32_t)to_type(v[3], T) << 16;
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) +
-                                    ((int64_t)row * p.heads + head) * D + at) = uint2{x, y};
-        } else {
-          *reinterpret_cast<float4*>(p.part_o + slot * D + at) = float4{v[0], v[1], v[2], v[3]};
-        }
-      }
-  }
 }
 
 // Joins the splits of a (row, query head), in order: a thread a column of the
@@ -1084,8 +1079,8 @@ void attend(const AttendParams& all, hipStream_t s) {
               if (p.cols == 16) narrow<T, C, D, 1>(p, grid, s);
               if (p.cols == 32) narrow<T, C, D, 2>(p, grid, s);
               if (p.cols == 64) narrow<T, C, D, 4>(p, grid, s);
-              if (p.cols == 128) attend_wide_kernel<T, C, D, 1><<<grid, 256, 0, s>>>(p);
-              if (p.cols == 256) attend_wide_kernel<T, C, D, 2><<<grid, 256, 0, s>>>(p);
+              if (p.cols == 128) attend_wide_kernel<T, C, D, 4><<<grid, 256, 0, s>>>(p);
+              if (p.cols == 256) attend_wide_kernel<T, C, D, 8><<<grid, 512, 0, s>>>(p);
             });
   if (all.splits > 1) {
     const int64_t pairs = (int64_t)all.rows * all.heads, per = 256 / D;

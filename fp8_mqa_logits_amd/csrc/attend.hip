@@ -627,14 +627,14 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   in_hi = __builtin_amdgcn_readfirstlane(in_hi);
 
   // this lane's column
-  const int at_col = wave * 32 + n, col = tile * COLS + at_col;
-  const bool real = col < columns;
-  const int row = unit * p.R + (real ? col / p.group : 0);
-  const int head = h * p.group + (real ? col % p.group : 0);
-  int col_s, col_e;
-  row_range(p, row, col_s, col_e);
+  int at_col = wave * 32 + n, col_s, col_e;
   v4u q[KS];
   {
+    const int col = tile * COLS + at_col;
+    const bool real = col < columns;
+    const int row = unit * p.R + (real ? col / p.group : 0);
+    const int head = h * p.group + (real ? col % p.group : 0);
+    row_range(p, row, col_s, col_e);
     const uint16_t* src = static_cast<const uint16_t*>(p.q) + row * p.q_row + head * p.q_head;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
@@ -660,11 +660,13 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   auto k_key = [&](int r) { return piece(r) / (D / 16); };
   auto v_key = [&](int r) { return piece(r) / (D / 4) * 4; };
   auto v_d = [&](int r) { return piece(r) % (D / 4) * 4; };
+  const int32_t* const table = c.table + (int64_t)unit * c.table_stride;
   auto group_page = [&](int i, int g) -> int {  // page of group g of tile i; -1: no row sees it
     const int pos = base + i * 64 + 16 * g;
-    if (i >= tiles || pos >= hi || pos + 16 <= lo) return -1;
-    const int page = c.table[(int64_t)unit * c.table_stride + (pos >> c.page_shift)];
-    return page < 0 ? 0 : (page >= c.num_pages ? c.num_pages - 1 : page);
+    // (loaded in any case, from a place that is one: no branch in the loop)
+    int page = table[min(max(pos, lo), hi - 1) >> c.page_shift];
+    page = min(max(page, 0), c.num_pages - 1);
+    return i >= tiles || pos >= hi || pos + 16 <= lo ? -1 : page;
   };
   auto page_at = [&](int page) { return c.pages + (int64_t)(page < 0 ? 0 : page) * c.page_stride; };
   auto slot_of = [&](int i, int key) {
@@ -758,7 +760,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   };
 
   const float cs = p.scale * kLog2e;
-  float m = kLowest, l = 0.f, vref = 0x1p-126f;
+  float m = kLowest, l = 0.f, vref = 0x1p-126f, down = 0x1p126f;  // down = 1 / vref
   v16f acc[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d) acc[d] = v16f{};
@@ -768,7 +770,6 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   // of the current tile, per group of 16 keys (the same in all lanes): the
   // factor of the scores; vs / vref, its logarithm + kBias and its inverse
   float fk[4], vr[4], lv[4], iv[4];
-  uint32_t poison[2] = {0, 0};
   bool plain = false;  // every row sees every key, and the scales are ordinary
 
   auto uniform = [](float x) {
@@ -780,26 +781,18 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     for (int k = 0; k < 2; ++k)
       pr.f[k] = __builtin_bit_cast(v4u, __builtin_bit_cast(v8h, pr.f[k]) * k16);
   };
-  auto take_scales = [&](int i, Prob& pending) {
+  float most = 0.f;
+  auto take_scales = [&](int i) {
     const float* s = s_scale[i & 1];
-    float most = 0.f, vs[4];
+    float vs[4];
+    most = 0.f;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       fk[g] = uniform(s[g] * cs);
       vs[g] = uniform(s[4 + g]);
       most = vs[g] < __builtin_inff() ? __builtin_fmaxf(most, vs[g]) : most;
     }
-    if (most > vref) {
-      const uint32_t u = __float_as_uint(most);
-      const float to = __uint_as_float((u & 0x7FFFFFu) ? (u & 0x7F800000u) + 0x800000u : u);
-      const float keep = vref / to;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) acc[d] *= keep;
-      rescale_pending(pending, keep);
-      vref = uniform(to);
-    }
     bool ordinary = true;
-    const float down = 1.f / vref;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       vr[g] = uniform(vs[g] * down);
@@ -807,9 +800,20 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
       iv[g] = uniform(__builtin_amdgcn_rcpf(vr[g]));
       ordinary = ordinary && vr[g] >= 0x1p-60f && vr[g] <= 1.f;
     }
-    poison[0] = s_poison[i % 3][0];
-    poison[1] = s_poison[i % 3][1];
-    plain = ordinary && inside(i);
+    plain = __builtin_amdgcn_readfirstlane((int)(ordinary && inside(i)));
+  };
+  // moves vref where a scale of tile i passes it
+  auto settle_scales = [&](int i, Prob& pending) {
+    if (most <= vref) return;
+    const uint32_t u = __float_as_uint(most);
+    const float to = __uint_as_float((u & 0x7FFFFFu) ? (u & 0x7F800000u) + 0x800000u : u);
+    const float keep = vref / to;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) acc[d] *= keep;
+    rescale_pending(pending, keep);
+    vref = uniform(to);
+    down = uniform(1.f / to);
+    take_scales(i);
   };
   auto scores = [&](v16f& s, int i, int half) {
     const uint8_t* const from = s_k[i & 1] + k_slot(n, hh);
@@ -863,7 +867,8 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
         pr.f[k] = pack(e);
       }
     } else {
-      const uint32_t sees = seen_keys(i, half), ill = sees & (poison[half] >> (4 * hh));
+      const uint32_t sees = seen_keys(i, half);
+      const uint32_t ill = sees & (s_poison[i % 3][half] >> (4 * hh));
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int g = 2 * half + k;
@@ -907,8 +912,9 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   };
   // moves m where a score passes it by more than kLag; `pending`: the P not
   // yet in the sums
+  auto passes = [&](float top) { return __any(top > m + kLag); };
   auto settle = [&](float top, Prob& pending) {
-    if (!__any(top > m + kLag)) return;
+    if (!passes(top)) return;
     const float x = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
     const float to = __builtin_fmaxf(m, __builtin_ceilf(x));
     const float keep = __builtin_amdgcn_exp2f(m - to);
@@ -940,18 +946,25 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     find_k(2);
     find_v(2);
     __syncthreads();
-    take_scales(0, p0);
-    scores(s0, 0, 0);
-    settle(plain ? largest(yes, s0, 0, 0) : largest(no, s0, 0, 0), p0);
+    // holds the exponentials next to the products (they are used after a branch
+    // only, and would be moved behind it)
+    auto keep_here = [](Prob& pr, float& x) {
+      asm volatile("" : "+v"(pr.f[0]), "+v"(pr.f[1]), "+v"(x));
+    };
     // first half: s0 -> p0, scores of the second, values of the last tile's
-    // second; keys of the next tile into LDS
+    // second; keys of the next tile into LDS. The largest of the scores.
     auto half0 = [&](auto is_plain, int i) {
       scores(s1, i, 1);
       soft(is_plain, s0, p0, i, 0);
       values(p1, i - 1, 1);
       stage_k(i + 1);
       load_k(i + 2);
-      settle(largest(is_plain, s1, i, 1), p0);
+      const float top = largest(is_plain, s1, i, 1);
+      keep_here(p0, l);
+      clean_v(i + 1);
+      find_k(i + 3);
+      __syncthreads();
+      return top;
     };
     // second half: s1 -> p1, scores of the next tile's first, values of this
     // tile's first; values of the next tile into LDS
@@ -961,30 +974,47 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
       values(p0, i, 0);
       stage_v(i + 1);
       load_v(i + 2);
-    };
-    for (int i = 0; i < tiles; ++i) {
-      if (plain) {
-        asm volatile("; plain" ::: "memory");
-        half0(yes, i);
-      } else {
-        asm volatile("; any" ::: "memory");
-        half0(no, i);
-      }
-      clean_v(i + 1);
-      find_k(i + 3);
-      __syncthreads();
-      if (plain) {
-        asm volatile("; plain" ::: "memory");
-        half1(yes, i);
-      } else {
-        asm volatile("; any" ::: "memory");
-        half1(no, i);
-      }
+      keep_here(p1, l);
       find_v(i + 3);
-      if (i + 1 < tiles) {
-        take_scales(i + 1, p1);
-        settle(plain ? largest(yes, s0, i + 1, 0) : largest(no, s0, i + 1, 0), p1);
+    };
+    // The tiles that need nothing but the pipeline run in a loop of their own,
+    // whose sums stay in place; it is left where a reference point has to move
+    // or a tile needs masks.
+    int i = 0;
+    take_scales(0);
+    settle_scales(0, p0);
+    scores(s0, 0, 0);
+    settle(largest(no, s0, 0, 0), p0);
+    while (true) {
+      float top;
+      if (plain) {
+        bool within = false;
+        while (true) {
+          top = half0(yes, i);
+          if (passes(top)) {
+            within = true;
+            break;
+          }
+          half1(yes, i);
+          if (++i >= tiles) break;
+          take_scales(i);
+          if (!plain || most > vref || passes(largest(yes, s0, i, 0))) break;
+        }
+        if (i >= tiles) break;
+        if (!within) {
+          settle_scales(i, p1);
+          settle(largest(no, s0, i, 0), p1);
+          continue;
+        }
+      } else {
+        top = half0(no, i);
       }
+      settle(top, p0);
+      half1(no, i);
+      if (++i >= tiles) break;
+      take_scales(i);
+      settle_scales(i, p1);
+      settle(largest(no, s0, i, 0), p1);
     }
     values(p1, tiles - 1, 1);
   }
@@ -994,7 +1024,10 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   const float sum = col_s >= col_e ? 0.f : both;  // (sums of a row that sees nothing)
   const int64_t slot = (((int64_t)unit * p.tiles + tile) * c.kv_heads + h) * p.splits * COLS +
                        (int64_t)split * COLS + at_col;
-  if (!real) return;
+  asm("" : "+v"(at_col));  // (the row and head are computed anew, not kept in the loop)
+  const int col = tile * COLS + at_col;
+  if (col >= columns) return;
+  const int row = unit * p.R + col / p.group, head = h * p.group + col % p.group;
   if (hh == 0) {
     if (!direct) {
       p.part_ml[2 * slot] = m;

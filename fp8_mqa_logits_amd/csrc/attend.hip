@@ -660,46 +660,49 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   auto k_key = [&](int r) { return piece(r) / (D / 16); };
   auto v_key = [&](int r) { return piece(r) / (D / 4) * 4; };
   auto v_d = [&](int r) { return piece(r) % (D / 4) * 4; };
+  // A group of 16 keys that no row sees is read from the nearest one that some
+  // row sees (masked later; no branch in the loop). Its table entry is loaded a
+  // tile before its use, and only looked at then.
   const int32_t* const table = c.table + (int64_t)unit * c.table_stride;
-  auto group_page = [&](int i, int g) -> int {  // page of group g of tile i; -1: no row sees it
-    const int pos = base + i * 64 + 16 * g;
-    // (loaded in any case, from a place that is one: no branch in the loop)
-    int page = table[min(max(pos, lo), hi - 1) >> c.page_shift];
-    page = min(max(page, 0), c.num_pages - 1);
-    return i >= tiles || pos >= hi || pos + 16 <= lo ? -1 : page;
+  auto group_pos = [&](int i, int g) {
+    return min(max(base + i * 64 + 16 * g, lo), hi - 1) & ~15;
   };
-  auto page_at = [&](int page) { return c.pages + (int64_t)(page < 0 ? 0 : page) * c.page_stride; };
+  auto group_entry = [&](int i, int g) { return table[group_pos(i, g) >> c.page_shift]; };
+  auto page_at = [&](int entry) {
+    return c.pages + (int64_t)min(max(entry, 0), c.num_pages - 1) * c.page_stride;
+  };
   auto slot_of = [&](int i, int key) {
-    return (base + i * 64 + key) & ((1 << c.page_shift) - 1);
+    return (group_pos(i, key >> 4) + (key & 15)) & ((1 << c.page_shift) - 1);
   };
   v4u kreg[EACH];
   uint32_t vreg[EACH][4];
   float sreg = 0.f;
-  int kpage[EACH], vpage[EACH], spage;
+  int kentry[EACH], ventry[EACH], sentry;
+  // (of a workgroup with more threads than pieces, the others read piece 0 too)
+  auto k_of = [&](int r) { return mine(r) ? k_key(r) : 0; };
+  auto v_of = [&](int r) { return mine(r) ? v_key(r) : 0; };
   auto find_k = [&](int i) {
 #pragma unroll
-    for (int r = 0; r < EACH; ++r) kpage[r] = mine(r) ? group_page(i, k_key(r) >> 4) : -1;
-    spage = group_page(i, t & 3);
+    for (int r = 0; r < EACH; ++r) kentry[r] = group_entry(i, k_of(r) >> 4);
+    sentry = group_entry(i, t & 3);
   };
   auto find_v = [&](int i) {
 #pragma unroll
-    for (int r = 0; r < EACH; ++r) vpage[r] = mine(r) ? group_page(i, v_key(r) >> 4) : -1;
+    for (int r = 0; r < EACH; ++r) ventry[r] = group_entry(i, v_of(r) >> 4);
   };
   auto load_k = [&](int i) {
 #pragma unroll
     for (int r = 0; r < EACH; ++r)
-      kreg[r] = *reinterpret_cast<const v4u*>(
-          page_at(kpage[r]) + code_at(c, 0, h, kpage[r] < 0 ? 0 : slot_of(i, k_key(r))) +
-          16 * (piece(r) % (D / 16)));
-    const float x = *reinterpret_cast<const float*>(
-        page_at(spage) + scale_at(c, t >> 2 & 1, h, spage < 0 ? 0 : slot_of(i, 16 * (t & 3))));
-    sreg = spage < 0 ? 0.f : x;
+      kreg[r] = *reinterpret_cast<const v4u*>(page_at(kentry[r]) +
+                                              code_at(c, 0, h, slot_of(i, k_of(r))) +
+                                              16 * (piece(r) % (D / 16)));
+    sreg = *reinterpret_cast<const float*>(page_at(sentry) +
+                                           scale_at(c, t >> 2 & 1, h, slot_of(i, 16 * (t & 3))));
   };
   auto load_v = [&](int i) {
 #pragma unroll
     for (int r = 0; r < EACH; ++r) {
-      const uint8_t* at =
-          page_at(vpage[r]) + code_at(c, 1, h, vpage[r] < 0 ? 0 : slot_of(i, v_key(r))) + v_d(r);
+      const uint8_t* at = page_at(ventry[r]) + code_at(c, 1, h, slot_of(i, v_of(r))) + v_d(r);
 #pragma unroll
       for (int j = 0; j < 4; ++j) vreg[r][j] = *reinterpret_cast<const uint32_t*>(at + j * D);
     }

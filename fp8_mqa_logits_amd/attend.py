@@ -62,7 +62,7 @@ class KVLayout:
     heads of head_dim (64 or 128) 8-bit codes ("e4m3" or "int8") for
     page_size tokens, and an fp32 scale for each block of tokens and head
     (page_size and block powers of two, 16 <= block <= page_size)."""
-    __slots__ = ("kv_heads", "head_dim", "page_size", "block", "codes")
+    __slots__ = ("kv_heads", "head_dim", "page_size", "block", "codes", "_bytes")
 
     def __init__(self, kv_heads: int, head_dim: int, page_size: int = 64, block: int = 64,
                  codes: str = "e4m3"):
@@ -70,6 +70,7 @@ class KVLayout:
             raise ValueError(f"codes: {codes!r} not in {tuple(CODES)}")
         self.kv_heads, self.head_dim = int(kv_heads), int(head_dim)
         self.page_size, self.block, self.codes = int(page_size), int(block), codes
+        self._bytes = 0
 
     def __repr__(self):
         return (f"KVLayout(kv_heads={self.kv_heads}, head_dim={self.head_dim}, "
@@ -78,12 +79,14 @@ class KVLayout:
     @property
     def page_bytes(self) -> int:
         """Bytes of a page; raises for sizes that no page can have."""
-        n = int(_load().mqa_kv_page_bytes(self.kv_heads, self.head_dim, self.page_size,
-                                          self.block))
-        if n == 0:
-            raise ValueError(f"{self}: head_dim must be 64 or 128, page_size and block powers of "
-                             "two, 16 <= block <= page_size <= 65536, a page below 2 GiB")
-        return n
+        if not self._bytes:
+            n = int(_load().mqa_kv_page_bytes(self.kv_heads, self.head_dim, self.page_size,
+                                              self.block))
+            if n == 0:
+                raise ValueError(f"{self}: head_dim must be 64 or 128, page_size and block powers "
+                                 "of two, 16 <= block <= page_size <= 65536, a page below 2 GiB")
+            self._bytes = n
+        return self._bytes
 
     def alloc(self, num_pages: int, device="cuda") -> torch.Tensor:
         """A zeroed pool of pages [num_pages, page_bytes] uint8."""
@@ -156,25 +159,31 @@ def _raise(code: int, where: str):
         raise MQAError(code, where)
 
 
-class _Launch:
-    """The device made current and the stream that the call runs on; buffers
-    that the binding allocates belong to that stream."""
-
-    def __init__(self, dev, stream):
-        self.stack = contextlib.ExitStack()
-        if torch.cuda.current_device() != dev.index:
-            self.stack.enter_context(torch.cuda.device(dev))
-        if stream is not None:
-            self.stack.enter_context(torch.cuda.stream(stream))
+@contextlib.contextmanager
+def _elsewhere(dev, stream):
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield
         else:
-            stream = torch.cuda.current_stream(dev)
-        self.handle = stream.cuda_stream
+            with torch.cuda.stream(stream):
+                yield
 
-    def __enter__(self):
-        return self.handle
 
-    def __exit__(self, *exc):
-        return self.stack.__exit__(*exc)
+_HERE = contextlib.nullcontext()
+
+
+def _launch(dev, stream):
+    """The device made current and the stream that the call runs on; buffers
+    that the binding allocates inside belong to that stream."""
+    if stream is None and torch.cuda.current_device() == dev.index:
+        return _HERE
+    return _elsewhere(dev, stream)
+
+
+def _stream(dev, stream) -> int:
+    # torch.cuda.current_stream() builds a Stream object to the same end, at
+    # a tenth of a small call's time
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
 
 
 def mqa_kv_append(layout: KVLayout, k, v, cache, page_table, starts, counts=None,
@@ -195,7 +204,8 @@ def mqa_kv_append(layout: KVLayout, k, v, cache, page_table, starts, counts=None
     _dense(starts, "starts", torch.int32, (requests,), dev)
     if counts is not None:
         _dense(counts, "counts", torch.int32, (requests,), dev)
-    with _Launch(dev, stream) as s:
+    with _launch(dev, stream):
+        s = _stream(dev, stream)
         rc = _load().mqa_kv_append(c, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
                                    v.stride(0), v.stride(1), DTYPES[k.dtype], starts.data_ptr(),
                                    None if counts is None else counts.data_ptr(), requests, R, s)
@@ -218,7 +228,8 @@ def mqa_kv_read(layout: KVLayout, cache, page_table, starts, counts, rows_per_re
     if counts is not None:
         _dense(counts, "counts", torch.int32, (requests,), dev)
     shape = (requests * R, layout.kv_heads, layout.head_dim)
-    with _Launch(dev, stream) as s:
+    with _launch(dev, stream):
+        s = _stream(dev, stream)
         if out is None:
             out = (torch.empty(shape, dtype=dtype, device=dev),
                    torch.empty(shape, dtype=dtype, device=dev))
@@ -266,7 +277,8 @@ def _attend(layout, q, cache, page_table, indices, starts, ends, scale, out, lse
     if scale is None:
         scale = 1.0 / math.sqrt(layout.head_dim)
     lib = _load()
-    with _Launch(dev, stream) as s:
+    with _launch(dev, stream):
+        s = _stream(dev, stream)
         if out is None:
             out = torch.empty(shape, dtype=q.dtype, device=dev)
         else:

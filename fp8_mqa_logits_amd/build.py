@@ -1,8 +1,10 @@
 """Build libmqa_topk.so (the HIP kernels and the C ABI) in-tree for gfx950."""
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import subprocess
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -10,8 +12,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libmqa_topk.so")
 SOURCES = ["fused.hip", "dense.hip", "probe.hip", "api.hip", "kvcache.hip", "attend.hip",
-           "attend_api.hip"]
-HEADERS = ["common.h", "launch.h", "attend.h"]
+           "attend_narrow.hip", "attend_list.hip", "attend_wide.hip", "attend_api.hip"]
+HEADERS = ["common.h", "launch.h", "attend.h", "attend_tiles.h"]
 
 
 def hipcc() -> str:
@@ -19,12 +21,16 @@ def hipcc() -> str:
     return os.path.join(rocm, "bin", "hipcc")
 
 
-def command(out: str) -> list[str]:
-    return [hipcc(), "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
-            # packed fp32 VALU forms are kept out of the generated code
-            "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-            "-I", os.path.join(ROOT, "include"), "-o", out] + \
-           [os.path.join(CSRC, s) for s in SOURCES]
+FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
+         # packed fp32 VALU forms are kept out of the generated code
+         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+         "-I", os.path.join(ROOT, "include")]
+
+
+def run(args: list[str]) -> None:
+    res = subprocess.run([hipcc()] + args, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("hipcc failed:\n" + res.stdout + res.stderr)
 
 
 def stale() -> bool:
@@ -41,11 +47,13 @@ def build(force: bool = True) -> str:
     if not force and not stale():
         return LIB
     os.makedirs(LIB_DIR, exist_ok=True)
-    tmp = LIB + ".tmp"
-    res = subprocess.run(command(tmp), capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + res.stdout + res.stderr)
-    os.replace(tmp, LIB)
+    with tempfile.TemporaryDirectory() as tmp:
+        objects = [os.path.join(tmp, name + ".o") for name in SOURCES]
+        with concurrent.futures.ThreadPoolExecutor(min(len(SOURCES), os.cpu_count() or 1, 8)) as pool:
+            list(pool.map(lambda i: run(FLAGS + ["-c", os.path.join(CSRC, SOURCES[i]), "-o",
+                                                 objects[i]]), range(len(SOURCES))))
+        run(["--offload-arch=gfx950", "-shared", "-fPIC", "-o", LIB + ".tmp"] + objects)
+    os.replace(LIB + ".tmp", LIB)
     return LIB
 
 

@@ -11,6 +11,7 @@ namespace mqa {
 
 enum { kE4m3 = 0, kInt8 = 1 };
 enum { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
+constexpr int kMaxSplits = 64;  // parts of a tile's keys
 
 struct KvCache {
   uint8_t* pages;

@@ -71,20 +71,24 @@ struct Plan {
   size_t ml, o, total;  // workspace offsets
 };
 
+// The widest tile whose workgroups, each with 512 keys at least, give every
+// compute unit one; the narrowest where none does (window_333: 20 -> us).
 Plan plan(int requests, int R, int heads, int kv_heads, int head_dim, int positions, bool list,
           int cus) {
   Plan a{};
   const int group = heads / kv_heads, columns = list ? group : R * group;
-  a.cols = columns <= 16 ? 16 : (columns <= 32 ? 32 : 64);
-  if (!list && columns > 64) a.cols = columns <= 128 ? 128 : 256;
+  const int64_t units = (int64_t)(list ? requests * R : requests) * kv_heads;
+  const int64_t most = positions < 1024 ? 1 : positions / 512;
+  a.cols = 16;
+  while (a.cols < columns && a.cols < (list ? 64 : 256)) a.cols *= 2;
+  auto items = [&]() { return units * ((columns + a.cols - 1) / a.cols); };
+  while (!list && a.cols > 16 && items() * most < cus) a.cols /= 2;
   a.tiles = (columns + a.cols - 1) / a.cols;
-  const int64_t items = (int64_t)(list ? requests * R : requests) * a.tiles * kv_heads;
-  // enough workgroups for the device, 256 keys in each at least
-  const int64_t want = ((int64_t)(a.cols > 64 ? 1 : 6) * cus + items - 1) / items;
-  const int64_t most = (positions + 255) / 256;
+  // splits: enough workgroups for the device
+  const int64_t want = ((int64_t)(a.cols > 64 ? 1 : 6) * cus + items() - 1) / items();
   a.splits = (int)(want < most ? want : most);
-  a.splits = a.splits < 1 ? 1 : (a.splits > 64 ? 64 : a.splits);
-  const int64_t slots = a.splits > 1 ? items * a.splits * a.cols : 0;
+  a.splits = a.splits < 1 ? 1 : (a.splits > mqa::kMaxSplits ? mqa::kMaxSplits : a.splits);
+  const int64_t slots = a.splits > 1 ? items() * a.splits * a.cols : 0;
   a.ml = 0;
   a.o = (size_t)((slots * 8 + 255) / 256 * 256);
   a.total = a.o + (size_t)slots * head_dim * 4;

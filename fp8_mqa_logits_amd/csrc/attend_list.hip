@@ -1,0 +1,279 @@
+// Attention over listed positions (see attend_tiles.h for the sums).
+#include "attend_tiles.h"
+
+namespace mqa {
+namespace {
+
+constexpr uint32_t kNone = ~0u;  // token of an entry that names no position
+
+// A workgroup takes one row and 16 HW of the query heads of one key head, and
+// one of p.splits parts of the row's list, 32 entries and KW = 4 / HW waves at
+// a time. HW waves share 32 entries: each loads its part of their rows (16
+// bytes a lane, whole rows next to each other), a step ahead, into registers
+// and then into LDS, and every one of them reads all of it for its own 16
+// heads, with the products of attend_narrow.hip. (One wave for all heads would
+// widen each code once, not HW times, but its sums leave room for one wave per
+// SIMD only, and a gather's latency shows: 1.14 ms for 4096 rows of 64 heads
+// and 2048 positions.) The rows' 16-byte slots are exchanged so that the lanes
+// of a read touch all banks.
+//
+// A step's tokens (slots in the pool) are found by lanes 0 .. 31, an entry
+// each, two steps ahead, and go to the other lanes by permutation; scales go
+// through LDS, a wave for itself.
+template <int T, int C, int D, int HW>
+__global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
+  constexpr int KW = 4 / HW;
+  constexpr int KC = D / 64;       // 16-byte pieces of a key per lane and product
+  constexpr int U = D / 16;        // products per step
+  constexpr int VW = D / 64;       // dwords of a value per lane
+  constexpr int PIECES = D / 16;   // 16-byte pieces of a row
+  constexpr int GROUP = 64 * HW;   // threads that share 32 entries
+  constexpr int EACH = 64 * PIECES / GROUP;  // pieces of 32 keys and 32 values per thread
+  constexpr int COLS = 16 * HW, BUFS = HW == 1 ? 1 : 2;
+  const KvCache& c = p.c;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, n = lane & 15;
+  const int hw = wave % HW, kb = wave / HW, gt = hw * 64 + lane;
+  const int64_t block = p.block0 + blockIdx.x;
+  const int split = (int)(block % p.splits);
+  const int64_t item = block / p.splits;
+  const int h = (int)(item % c.kv_heads), tile = (int)(item / c.kv_heads % p.tiles);
+  const int row = (int)(item / c.kv_heads / p.tiles);
+
+  __shared__ union {
+    struct {
+      uint8_t rows[KW][BUFS][64 * D];  // 32 keys, 32 values
+      float ks[4][32], vs[4][32];
+    } step;
+    Finish<D, 1, HW, KW> finish;
+  } sh;
+
+  int s, e;
+  row_range(p, row, s, e);
+  v4u q[2 * KC];
+  {
+    const int col = tile * COLS + 16 * hw + n;
+    const bool real = col < p.group;
+    const uint16_t* src = static_cast<const uint16_t*>(p.q) + row * p.q_row +
+                          (h * p.group + (real ? col : 0)) * p.q_head;
+#pragma unroll
+    for (int k = 0; k < 2 * KC; ++k) {
+      q[k] = *reinterpret_cast<const v4u*>(src + 64 * (k >> 1) + 16 * g + 8 * (k & 1));
+      if (!real) q[k] = v4u{0, 0, 0, 0};
+    }
+  }
+  const int steps = (p.width + 31) / 32;
+  const int per_split = ((steps + p.splits - 1) / p.splits + KW - 1) / KW * KW;
+  const int step_lo = split * per_split;
+  const int rounds = (min(steps, step_lo + per_split) - step_lo + KW - 1) / KW;
+  const int step_hi = min(steps, step_lo + per_split);
+
+  const float cs = p.scale * kLog2e;
+  float m[1] = {kLowest}, l[1] = {0.f}, vref = 0x1p-126f, down = 0x1p126f;  // down = 1 / vref
+  v4f acc[1][U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) acc[0][u] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  // entry lane % 32 of the wave's step in a round: its list entry, the table
+  // entry of the position it names, and the token
+  const int32_t* const list = p.indices + (int64_t)row * p.width;
+  const int32_t* const table = c.table + (int64_t)(row / p.R) * c.table_stride;
+  const int page_mask = (1 << c.page_shift) - 1;
+  auto listed = [&](int round) {
+    const int at = (step_lo + round * KW + kb) * 32 + (lane & 31);
+    const int x = list[min(at, p.width - 1)];
+    return at < min(step_hi * 32, p.width) && x >= 0 && x < e - s ? x : -1;
+  };
+  auto looked_up = [&](int x) { return table[(x < 0 ? 0 : min(s + x, c.cap - 1)) >> c.page_shift]; };
+  auto token_of = [&](int x, int entry) -> uint32_t {
+    const uint32_t page = (uint32_t)clamp_page(c, entry);
+    return x < 0 ? kNone : (page << c.page_shift) + (uint32_t)((s + x) & page_mask);
+  };
+  // what a lane loads: piece x = gt + GROUP r of the 32 keys, then values
+  auto token_row = [&](uint32_t tok) {
+    tok = tok == kNone ? 0u : tok;
+    return c.pages + (int64_t)(tok >> c.page_shift) * c.page_stride + (tok & page_mask) * (uint32_t)D;
+  };
+  const int k_at = code_at(c, 0, h, 0), v_at = code_at(c, 1, h, 0);
+  v4u reg[EACH];
+  float ks, vs;
+  auto load = [&](uint32_t tok) {
+#pragma unroll
+    for (int r = 0; r < EACH; ++r) {
+      const int x = gt + GROUP * r, key = x / PIECES % 32;
+      const uint8_t* at = token_row((uint32_t)__shfl((int)tok, key, 64));
+      reg[r] = *reinterpret_cast<const v4u*>(at + (x < 32 * PIECES ? k_at : v_at) +
+                                             16 * (x % PIECES));
+    }
+    const uint32_t mine = tok == kNone ? 0u : tok;
+    const uint8_t* page = c.pages + (int64_t)(mine >> c.page_shift) * c.page_stride;
+    ks = *reinterpret_cast<const float*>(page + scale_at(c, 0, h, mine & page_mask));
+    vs = *reinterpret_cast<const float*>(page + scale_at(c, 1, h, mine & page_mask));
+  };
+  // slot of piece x of a row in its LDS row
+  auto slot_of = [&](int key, int x) {
+    return x ^ (D == 128 ? (key >> 1) & 7 : (key >> 2) & 3);
+  };
+  auto stage = [&](int buf) {
+#pragma unroll
+    for (int r = 0; r < EACH; ++r) {
+      const int x = gt + GROUP * r;
+      *reinterpret_cast<v4u*>(&sh.step.rows[kb][buf][x / PIECES * D +
+                                                     16 * slot_of(x / PIECES, x % PIECES)]) = reg[r];
+    }
+  };
+  auto compute = [&](uint32_t valid, int buf) {
+    const bool clean = valid == ~0u;
+    const uint8_t* const rows = sh.step.rows[kb][buf];
+    v4f x[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      x[b] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+        const v4u w = *reinterpret_cast<const v4u*>(rows + (16 * b + n) * D +
+                                                    16 * slot_of(16 * b + n, g + 4 * k));
+        x[b] = mfma<T>(widen8<T, C>(w[0], w[1]), q[2 * k], x[b]);
+        x[b] = mfma<T>(widen8<T, C>(w[2], w[3]), q[2 * k + 1], x[b]);
+      }
+    }
+    const uint32_t sees = valid >> (4 * g);  // bit 16 b + i: entry 16 b + 4 g + i
+    float y[8], top = -__builtin_inff();
+    v4f vr[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const v4f f = *reinterpret_cast<const v4f*>(&sh.step.ks[wave][16 * b + 4 * g]);
+      vr[b] = *reinterpret_cast<const v4f*>(&sh.step.vs[wave][16 * b + 4 * g]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[4 * b + i] = x[b][i] * f[i];
+      }
+    }
+    if (!clean) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = or_lowest(y[j], bit(sees, 16 * (j >> 2) + (j & 3)));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = __builtin_fmaxf(top, y[j]);
+    if (__any(top > m[0] + kLag)) {
+      top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
+      top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
+      const float to = __builtin_fmaxf(m[0], __builtin_ceilf(top));
+      const float keep = __builtin_amdgcn_exp2f(m[0] - to);
+      m[0] = to;
+      l[0] *= keep;
+#pragma unroll
+      for (int u = 0; u < U; ++u) acc[0][u] *= keep;
+    }
+    float pr[8], sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      pr[j] = __builtin_amdgcn_exp2f(y[j] + (kBias - m[0]));
+      sum += pr[j];  // (exp2 of -infinity: 0)
+      pr[j] *= vr[j >> 2][j & 3];  // (0 where the entry names no position)
+    }
+    l[0] += sum;
+    v4u pf;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      pf[i] = __builtin_bit_cast(uint32_t, v2h{(_Float16)pr[2 * i], (_Float16)pr[2 * i + 1]});
+    uint32_t v[8][VW];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int key = 16 * (j >> 2) + 4 * g + (j & 3);
+      const uint8_t* at = rows + 32 * D + key * D +
+                          16 * slot_of(key, VW == 2 ? n >> 1 : n >> 2) +
+                          (VW == 2 ? 8 * (n & 1) : 4 * (n & 3));
+      if constexpr (VW == 2) {
+        const uint2 w = *reinterpret_cast<const uint2*>(at);
+        v[j][0] = w.x;
+        v[j][1] = w.y;
+      } else {
+        v[j][0] = *reinterpret_cast<const uint32_t*>(at);
+      }
+    }
+    if (!clean) {  // (what an entry that names no position was read from)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int w = 0; w < VW; ++w) v[j][w] &= bit(sees, 16 * (j >> 2) + (j & 3));
+    }
+#pragma unroll
+    for (int w = 0; w < VW; ++w) {
+      uint32_t in[4], a[4], b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) in[j] = v[j][w];
+      transpose4(in, a);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) in[j] = v[4 + j][w];
+      transpose4(in, b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[0][4 * w + i] = mfma<kFp16>(widen8<kFp16, C>(a[i], b[i]), pf, acc[0][4 * w + i]);
+    }
+  };
+
+  if (rounds > 0 && s < e) {
+    auto sync = [&]() {
+      if constexpr (HW > 1)
+        __syncthreads();
+      else
+        __builtin_amdgcn_wave_barrier();
+    };
+    // a round's scales and which of its entries name positions
+    uint32_t valid;
+    auto take_scales = [&](uint32_t tok) {
+      valid = (uint32_t)__ballot(tok != kNone);
+      const float k = tok != kNone ? ks * cs : 0.f, v = tok != kNone ? vs : 0.f;
+      const float finite = v < __builtin_inff() ? v : 0.f;
+      if (__any(finite > vref)) {
+        const float to = power_above(wave_max(finite)), keep = vref / to;
+        vref = uniform(to);
+        down = uniform(1.f / to);
+#pragma unroll
+        for (int u = 0; u < U; ++u) acc[0][u] *= keep;
+      }
+      sh.step.ks[wave][lane & 31] = k;
+      sh.step.vs[wave][lane & 31] = v * down;
+      __builtin_amdgcn_wave_barrier();
+    };
+    int x = listed(0), entry = looked_up(x);
+    uint32_t tok = token_of(x, entry), next;
+    load(tok);
+    x = listed(1);
+    entry = looked_up(x);
+    next = token_of(x, entry);
+    x = listed(2);
+    entry = looked_up(x);
+    for (int i = 0; i < rounds; ++i) {
+      const int buf = BUFS == 1 ? 0 : i & 1;
+      stage(buf);
+      take_scales(tok);
+      sync();
+      tok = next;
+      if (i + 1 < rounds) load(tok);
+      next = token_of(x, entry);
+      x = listed(i + 3);
+      entry = looked_up(x);
+      compute(valid, buf);
+      if constexpr (BUFS == 1) __builtin_amdgcn_wave_barrier();
+    }
+  }
+  __syncthreads();  // (the steps' memory becomes the sums')
+  finish<T>(p, sh.finish, block, row, p.group, tile, h, wave, m, l, vref, acc);
+}
+
+template <int T, int C, int D>
+void launch(const AttendParams& p, dim3 grid, hipStream_t s) {
+  if (p.cols == 16) attend_list_kernel<T, C, D, 1><<<grid, 256, 0, s>>>(p);
+  if (p.cols == 32) attend_list_kernel<T, C, D, 2><<<grid, 256, 0, s>>>(p);
+  if (p.cols == 64) attend_list_kernel<T, C, D, 4><<<grid, 256, 0, s>>>(p);
+}
+
+}  // namespace
+
+void attend_list(const AttendParams& p, dim3 grid, hipStream_t s) {
+  dispatch(p, [&](auto t, auto c, auto d) { launch<t.value, c.value, d.value>(p, grid, s); });
+}
+
+}  // namespace mqa

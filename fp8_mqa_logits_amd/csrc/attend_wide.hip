@@ -1,0 +1,502 @@
+// Attention over ranges for many columns (see attend_tiles.h for the sums).
+#include "attend_tiles.h"
+
+namespace mqa {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Many columns: 32 W columns of one request and key head per workgroup, 32 in
+// each of its W waves, every wave over all keys of the workgroup's part. Tiles
+// of 64 keys pass through LDS once for the workgroup, widened on the way in:
+// keys as [key][d], values transposed as [d][key] in the order in which a lane
+// holds its scores, both with rows padded by 16 bytes so that 16 lanes of a
+// read touch all banks.
+//   S^T = K Q^T   32 keys x 32 columns per v_mfma_f32_32x32x16, Q in registers
+//   O^T += V^T P^T   P straight from the scores' registers
+//
+// Half tiles j = 0, 1, .. run as a pipeline inside the wave: the products of
+// S(j + 1) and of P(j - 1) V are independent of the exponentials of S(j), so
+// that the matrix unit and the vector unit work at the same time. One barrier
+// a tile: between the halves of tile i, when the keys of tile i + 1 are in
+// LDS; its values follow during the second half and are first read after the
+// next barrier. m and vref only move by powers of two, so that the P in flight
+// can be rescaled exactly.
+template <int T, int C, int D, int W>
+__global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) {
+  constexpr int THREADS = 64 * W;
+  constexpr int KS = D / 16;          // products a half's scores take
+  constexpr int DT = D / 32;          // tiles of the output's columns
+  constexpr int PIECES = 4 * D;       // 16-byte pieces of a tile's keys; 4 x 4 pieces of its values
+  constexpr int EACH = (PIECES + THREADS - 1) / THREADS;  // of each, per thread
+  constexpr int COLS = 32 * W;
+  const KvCache& c = p.c;
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int hh = lane >> 5, n = lane & 31;
+  const int64_t block = p.block0 + blockIdx.x;
+  const int split = (int)(block % p.splits);
+  const int64_t item = block / p.splits;
+  const int h = (int)(item % c.kv_heads);
+  const int unit = (int)(item / c.kv_heads / p.tiles);
+  // the last rows see the most in a causal chunk: they start first
+  const int tile = p.tiles - 1 - (int)(item / c.kv_heads % p.tiles);
+  const int columns = p.R * p.group;
+
+  constexpr int KROW = 2 * D + 16, VROW = 2 * 64 + 16;  // bytes of a staged key, of a column
+  __shared__ __align__(16) uint8_t s_k[2][64 * KROW];
+  __shared__ __align__(16) uint8_t s_v[2][D * VROW];
+  __shared__ __align__(16) float s_scale[2][THREADS];  // 8 scales, over and over
+  __shared__ uint32_t s_poison[3][2];
+  __shared__ Span s_span[W];
+
+  const int row_lo = unit * p.R + tile * COLS / p.group;
+  const int last = tile * COLS + COLS < columns ? tile * COLS + COLS : columns;
+  const int row_hi = unit * p.R + (last - 1) / p.group;
+  Span span = row_span(p, row_lo, row_hi - row_lo + 1, t, THREADS);
+  if (lane == 0) s_span[wave] = span;
+  if (t < 6) s_poison[t >> 1][t & 1] = 0;
+  // the first half adds no values: P = 0 times what is staged "before" them
+  for (int x = t; x < D * VROW / 16; x += THREADS)
+    reinterpret_cast<v4u*>(s_v[1])[x] = v4u{0, 0, 0, 0};
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < W; ++w)
+    span = {min(span.lo, s_span[w].lo), max(span.hi, s_span[w].hi),
+            max(span.in_lo, s_span[w].in_lo), min(span.in_hi, s_span[w].in_hi)};
+  span = uniform(span);
+  const int lo = span.lo, hi = span.hi, in_lo = span.in_lo, in_hi = span.in_hi;
+
+  // this lane's column
+  int at_col = wave * 32 + n, col_s, col_e;
+  v4u q[KS];
+  {
+    const int col = tile * COLS + at_col;
+    const bool real = col < columns;
+    const int row = unit * p.R + (real ? col / p.group : 0);
+    const int head = h * p.group + (real ? col % p.group : 0);
+    row_range(p, row, col_s, col_e);
+    const uint16_t* src = static_cast<const uint16_t*>(p.q) + row * p.q_row + head * p.q_head;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      q[k] = *reinterpret_cast<const v4u*>(src + 16 * k + 8 * hh);
+      if (!real) q[k] = v4u{0, 0, 0, 0};
+    }
+  }
+
+  // the part of the keys that this workgroup takes, in tiles of 64 from a
+  // multiple of 16: each group of 16 keys lies in one block
+  const int first = lo & ~15;
+  const int all = hi > first ? (hi - first + 63) / 64 : 0;
+  const int per_split = (all + p.splits - 1) / p.splits;
+  const int tile_lo = split * per_split;
+  const int tiles = min(all - tile_lo, per_split);
+  const int base = first + tile_lo * 64;
+
+  // staging: piece x = t + THREADS r of the keys is 16 bytes of key x / (D /
+  // 16); of the values, columns 4 (x % (D / 4)) .. + 3 of keys 4 y .. 4 y + 3,
+  // y = x / (D / 4)
+  auto piece = [&](int r) { return t + THREADS * r; };
+  auto mine = [&](int r) { return PIECES % THREADS == 0 || piece(r) < PIECES; };
+  auto k_key = [&](int r) { return piece(r) / (D / 16); };
+  auto v_key = [&](int r) { return piece(r) / (D / 4) * 4; };
+  auto v_d = [&](int r) { return piece(r) % (D / 4) * 4; };
+  // A group of 16 keys that no row sees is read from the nearest one that some
+  // row sees (masked later; no branch in the loop). Its table entry is loaded a
+  // tile before its use, and only looked at then.
+  const int32_t* const table = c.table + (int64_t)unit * c.table_stride;
+  auto group_pos = [&](int i, int g) {
+    return min(max(base + i * 64 + 16 * g, lo), hi - 1) & ~15;
+  };
+  auto group_entry = [&](int i, int g) { return table[group_pos(i, g) >> c.page_shift]; };
+  auto page_at = [&](int entry) {
+    return c.pages + (int64_t)min(max(entry, 0), c.num_pages - 1) * c.page_stride;
+  };
+  auto slot_of = [&](int i, int key) {
+    return (group_pos(i, key >> 4) + (key & 15)) & ((1 << c.page_shift) - 1);
+  };
+  v4u kreg[EACH];
+  uint32_t vreg[EACH][4];
+  float sreg = 0.f;
+  int kentry[EACH], ventry[EACH], sentry;
+  // (of a workgroup with more threads than pieces, the others read piece 0 too)
+  auto k_of = [&](int r) { return mine(r) ? k_key(r) : 0; };
+  auto v_of = [&](int r) { return mine(r) ? v_key(r) : 0; };
+  auto find_k = [&](int i) {
+#pragma unroll
+    for (int r = 0; r < EACH; ++r) kentry[r] = group_entry(i, k_of(r) >> 4);
+    sentry = group_entry(i, t & 3);
+  };
+  auto find_v = [&](int i) {
+#pragma unroll
+    for (int r = 0; r < EACH; ++r) ventry[r] = group_entry(i, v_of(r) >> 4);
+  };
+  auto load_k = [&](int i) {
+#pragma unroll
+    for (int r = 0; r < EACH; ++r)
+      kreg[r] = *reinterpret_cast<const v4u*>(page_at(kentry[r]) +
+                                              code_at(c, 0, h, slot_of(i, k_of(r))) +
+                                              16 * (piece(r) % (D / 16)));
+    sreg = *reinterpret_cast<const float*>(page_at(sentry) +
+                                           scale_at(c, t >> 2 & 1, h, slot_of(i, 16 * (t & 3))));
+  };
+  auto load_v = [&](int i) {
+#pragma unroll
+    for (int r = 0; r < EACH; ++r) {
+      const uint8_t* at = page_at(ventry[r]) + code_at(c, 1, h, slot_of(i, v_of(r))) + v_d(r);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) vreg[r][j] = *reinterpret_cast<const uint32_t*>(at + j * D);
+    }
+  };
+  auto k_slot = [&](int key, int slot) { return key * KROW + 16 * slot; };
+  auto v_slot = [&](int d, int slot) { return d * VROW + 16 * slot; };
+  auto inside = [&](int i) {  // every row sees every key of tile i
+    return base + i * 64 >= in_lo && base + i * 64 + 64 <= in_hi;
+  };
+  auto stage_k = [&](int i) {
+    uint8_t* const to = s_k[i & 1];
+#pragma unroll
+    for (int r = 0; r < EACH; ++r) {
+      if (!mine(r)) continue;
+      const int x = piece(r) % (D / 16);
+      *reinterpret_cast<v4u*>(to + k_slot(k_key(r), 2 * x)) = widen8<T, C>(kreg[r][0], kreg[r][1]);
+      *reinterpret_cast<v4u*>(to + k_slot(k_key(r), 2 * x + 1)) =
+          widen8<T, C>(kreg[r][2], kreg[r][3]);
+    }
+    s_scale[i & 1][t] = sreg;
+  };
+  // values that no row sees become 0; a NaN code, which some rows may see and
+  // others not, becomes 0 too and is put back through the P of the rows that
+  // see it (0 * NaN would reach the others)
+  auto clean_v = [&](int i) {
+    if (t == 0) s_poison[(i + 1) % 3][0] = s_poison[(i + 1) % 3][1] = 0;
+    if (inside(i)) return;
+#pragma unroll
+    for (int r = 0; r < EACH; ++r) {
+      if (!mine(r)) continue;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int key = v_key(r) + j, pos = base + i * 64 + key;
+        if (i >= tiles || pos < lo || pos >= hi) vreg[r][j] = 0;
+        if constexpr (C == kE4m3) {
+          const uint32_t bad = nan_bytes(vreg[r][j]);
+          if (bad) {
+            vreg[r][j] &= ~bad;
+            atomicOr(&s_poison[i % 3][key >> 5], 1u << (key & 31));
+          }
+        }
+      }
+    }
+  };
+  // keys 16 g + {0..3, 8..11} share slot 2 g, {4..7, 12..15} slot 2 g + 1
+  auto stage_v = [&](int i) {
+#pragma unroll
+    for (int r = 0; r < EACH; ++r) {
+      if (!mine(r)) continue;
+      uint32_t a[4];
+      transpose4(vreg[r], a);
+      const int y = v_key(r) >> 2, slot = 2 * (y >> 2) + (y & 1), half = y >> 1 & 1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint2*>(s_v[i & 1] + v_slot(v_d(r) + j, slot) + 8 * half) =
+            widen4<kFp16, C>(a[j]);
+    }
+  };
+
+  const float cs = p.scale * kLog2e;
+  float m = kLowest, l = 0.f, vref = 0x1p-126f, down = 0x1p126f;  // down = 1 / vref
+  v16f acc[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) acc[d] = v16f{};
+  struct Prob {
+    v4u f[2];  // of the half's two groups of keys
+  };
+  // of the current tile, per group of 16 keys (the same in all lanes): the
+  // factor of the scores; vs / vref, its logarithm + kBias and its inverse
+  float fk[4], vr[4], lv[4], iv[4];
+  bool plain = false;  // every row sees every key, and the scales are ordinary
+
+  auto rescale_pending = [&](Prob& pr, float keep) {
+    const _Float16 k16 = (_Float16)keep;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      pr.f[k] = __builtin_bit_cast(v4u, __builtin_bit_cast(v8h, pr.f[k]) * k16);
+  };
+  float most = 0.f;
+  auto take_scales = [&](int i) {
+    const float* s = s_scale[i & 1];
+    float vs[4];
+    most = 0.f;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      fk[g] = uniform(s[g] * cs);
+      vs[g] = uniform(s[4 + g]);
+      most = vs[g] < __builtin_inff() ? __builtin_fmaxf(most, vs[g]) : most;
+    }
+    bool ordinary = true;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      vr[g] = uniform(vs[g] * down);
+      lv[g] = uniform(__builtin_amdgcn_logf(vr[g]) + kBias);
+      iv[g] = uniform(__builtin_amdgcn_rcpf(vr[g]));
+      ordinary = ordinary && vr[g] >= 0x1p-60f && vr[g] <= 1.f;
+    }
+    plain = __builtin_amdgcn_readfirstlane((int)(ordinary && inside(i)));
+  };
+  // moves vref where a scale of tile i passes it
+  auto settle_scales = [&](int i, Prob& pending) {
+    if (most <= vref) return;
+    const float to = power_above(most);
+    const float keep = vref / to;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) acc[d] *= keep;
+    rescale_pending(pending, keep);
+    vref = uniform(to);
+    down = uniform(1.f / to);
+    take_scales(i);
+  };
+  auto scores = [&](v16f& s, int i, int half) {
+    const uint8_t* const from = s_k[i & 1] + k_slot(n, hh);
+    s = v16f{};
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+      s = mfma32<T>(*reinterpret_cast<const v4u*>(from + k_slot(32 * half, 2 * k)), q[k], s);
+  };
+  auto values = [&](const Prob& pr, int i, int half) {
+    const uint8_t* const from = s_v[i & 1] + v_slot(n, hh);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+        acc[d] = mfma32<kFp16>(
+            *reinterpret_cast<const v4u*>(from + v_slot(32 * d, 2 * (2 * half + k))), pr.f[k],
+            acc[d]);
+  };
+  // bit key_at(e): whether the column sees the key of its score e
+  auto seen_keys = [&](int i, int half) {
+    return seen_bits(base + i * 64 + 32 * half, col_s, col_e) >> (4 * hh);
+  };
+  auto key_at = [](int e) { return 8 * (e >> 2) + (e & 3); };
+  auto pack = [&](const float* e) {
+    v4u f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      f[j] = __builtin_bit_cast(uint32_t, v2h{(_Float16)e[2 * j], (_Float16)e[2 * j + 1]});
+    return f;
+  };
+  // scores -> probabilities of one half
+  auto soft = [&](auto is_plain, const v16f& s, Prob& pr, int i, int half) {
+    if constexpr (is_plain.value) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int g = 2 * half + k;
+        const float off = lv[g] - m;
+        float e[8], sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * k + j], fk[g], off));
+          sum += e[j];
+        }
+        l = __builtin_fmaf(sum, iv[g], l);
+        pr.f[k] = pack(e);
+      }
+    } else {
+      const uint32_t sees = seen_keys(i, half);
+      const uint32_t ill = sees & (s_poison[i % 3][half] >> (4 * hh));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int g = 2 * half + k;
+        float e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t see = bit(sees, key_at(8 * k + j));
+          const float x = or_zero(
+              __builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * k + j], fk[g], kBias - m)), see);
+          l += x;
+          e[j] = __uint_as_float(__float_as_uint(or_zero(x * vr[g], see)) |
+                                 (bit(ill, key_at(8 * k + j)) & 0x7FC00000u));
+        }
+        pr.f[k] = pack(e);
+      }
+    }
+  };
+  // a half's largest score in this lane
+  auto largest = [&](auto is_plain, const v16f& s, int i, int half) {
+    if constexpr (is_plain.value) {
+      float x = s[0], y = s[8];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) {
+        x = __builtin_fmaxf(x, s[j]);
+        y = __builtin_fmaxf(y, s[8 + j]);
+      }
+      return __builtin_fmaxf(x * fk[2 * half], y * fk[2 * half + 1]);
+    } else {
+      const uint32_t sees = seen_keys(i, half);
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        top = __builtin_fmaxf(
+            top, or_lowest(s[e] * fk[2 * half + (e >> 3)], bit(sees, key_at(e))));
+      return top;
+    }
+  };
+  // moves m where a score passes it by more than kLag; `pending`: the P not
+  // yet in the sums
+  auto passes = [&](float top) { return __any(top > m + kLag); };
+  auto settle = [&](float top, Prob& pending) {
+    if (!passes(top)) return;
+    const float x = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
+    const float to = __builtin_fmaxf(m, __builtin_ceilf(x));
+    const float keep = __builtin_amdgcn_exp2f(m - to);
+    m = to;
+    l *= keep;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) acc[d] *= keep;
+    rescale_pending(pending, keep);
+  };
+
+  if (tiles > 0) {
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    v16f s0, s1;
+    Prob p0, p1;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) p0.f[k] = p1.f[k] = v4u{0, 0, 0, 0};
+    find_k(0);
+    find_v(0);
+    load_k(0);
+    load_v(0);
+    find_k(1);
+    find_v(1);
+    stage_k(0);
+    clean_v(0);
+    stage_v(0);
+    load_k(1);
+    load_v(1);
+    find_k(2);
+    find_v(2);
+    __syncthreads();
+    // holds the exponentials next to the products (they are used after a branch
+    // only, and would be moved behind it)
+    auto keep_here = [](Prob& pr, float& x) {
+      asm volatile("" : "+v"(pr.f[0]), "+v"(pr.f[1]), "+v"(x));
+    };
+    // first half: s0 -> p0, scores of the second, values of the last tile's
+    // second; keys of the next tile into LDS. The largest of the scores.
+    auto half0 = [&](auto is_plain, int i) {
+      scores(s1, i, 1);
+      soft(is_plain, s0, p0, i, 0);
+      values(p1, i - 1, 1);
+      stage_k(i + 1);
+      load_k(i + 2);
+      const float top = largest(is_plain, s1, i, 1);
+      keep_here(p0, l);
+      clean_v(i + 1);
+      find_k(i + 3);
+      __syncthreads();
+      return top;
+    };
+    // second half: s1 -> p1, scores of the next tile's first, values of this
+    // tile's first; values of the next tile into LDS
+    auto half1 = [&](auto is_plain, int i) {
+      scores(s0, i + 1, 0);
+      soft(is_plain, s1, p1, i, 1);
+      values(p0, i, 0);
+      stage_v(i + 1);
+      load_v(i + 2);
+      keep_here(p1, l);
+      find_v(i + 3);
+    };
+    // The tiles that need nothing but the pipeline run in a loop of their own,
+    // whose sums stay in place; it is left where a reference point has to move
+    // or a tile needs masks.
+    int i = 0;
+    take_scales(0);
+    settle_scales(0, p0);
+    scores(s0, 0, 0);
+    settle(largest(no, s0, 0, 0), p0);
+    while (true) {
+      float top;
+      if (plain) {
+        bool within = false;
+        while (true) {
+          top = half0(yes, i);
+          if (passes(top)) {
+            within = true;
+            break;
+          }
+          half1(yes, i);
+          if (++i >= tiles) break;
+          take_scales(i);
+          if (!plain || most > vref || passes(largest(yes, s0, i, 0))) break;
+        }
+        if (i >= tiles) break;
+        if (!within) {
+          settle_scales(i, p1);
+          settle(largest(no, s0, i, 0), p1);
+          continue;
+        }
+      } else {
+        top = half0(no, i);
+      }
+      settle(top, p0);
+      half1(no, i);
+      if (++i >= tiles) break;
+      take_scales(i);
+      settle_scales(i, p1);
+      settle(largest(no, s0, i, 0), p1);
+    }
+    values(p1, tiles - 1, 1);
+  }
+
+  const bool direct = p.splits == 1;
+  const float both = l + __shfl_xor(l, 32, 64);
+  const float sum = col_s >= col_e ? 0.f : both;  // (sums of a row that sees nothing)
+  const int64_t slot = (((int64_t)unit * p.tiles + tile) * c.kv_heads + h) * p.splits * COLS +
+                       (int64_t)split * COLS + at_col;
+  asm("" : "+v"(at_col));  // (the row and head are computed anew, not kept in the loop)
+  const int col = tile * COLS + at_col;
+  if (col >= columns) return;
+  const int row = unit * p.R + col / p.group, head = h * p.group + col % p.group;
+  if (hh == 0) {
+    if (!direct) {
+      p.part_ml[2 * slot] = m;
+      p.part_ml[2 * slot + 1] = sum;
+    } else if (p.lse) {
+      p.lse[(int64_t)row * p.heads + head] =
+          sum == 0.f ? -__builtin_inff() : (m - kBias) * kLn2 + __builtin_logf(sum);
+    }
+  }
+  const float by = direct ? vref / sum : vref;
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int at = 32 * d + 8 * e + 4 * hh;
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = sum == 0.f ? 0.f : acc[d][4 * e + j] * by;
+      if (direct) {
+        const uint32_t x = to_type(v[0], T) | (uint32_t)to_type(v[1], T) << 16;
+        const uint32_t y = to_type(v[2], T) | (uint32_t)to_type(v[3], T) << 16;
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) +
+                                  ((int64_t)row * p.heads + head) * D + at) = uint2{x, y};
+      } else {
+        *reinterpret_cast<float4*>(p.part_o + slot * D + at) = float4{v[0], v[1], v[2], v[3]};
+      }
+    }
+}
+
+template <int T, int C, int D>
+void launch(const AttendParams& p, dim3 grid, hipStream_t s) {
+  if (p.cols == 128)
+    attend_wide_kernel<T, C, D, 4><<<grid, 256, 0, s>>>(p);
+  else
+    attend_wide_kernel<T, C, D, 8><<<grid, 512, 0, s>>>(p);
+}
+
+}  // namespace
+
+void attend_wide(const AttendParams& p, dim3 grid, hipStream_t s) {
+  dispatch(p, [&](auto t, auto c, auto d) { launch<t.value, c.value, d.value>(p, grid, s); });
+}
+
+}  // namespace mqa

@@ -32,14 +32,15 @@ DeviceInfo g_dev[64];
 
 // Compute-unit count and persistent-grid occupancy of a gfx950 device.
 const DeviceInfo* device_info(int device) {
-  int ndev = 0;
-  if (hipGetDeviceCount(&ndev) != hipSuccess || device < 0 || device >= ndev || device >= 64) {
-    (void)hipGetLastError();
-    return nullptr;
-  }
+  if (device < 0 || device >= 64) return nullptr;
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceInfo& d = g_dev[device];
   if (!d.probed) {
+    int ndev = 0;
+    if (hipGetDeviceCount(&ndev) != hipSuccess || device >= ndev) {
+      (void)hipGetLastError();
+      return nullptr;
+    }
     d.probed = true;
     hipDeviceProp_t prop;
     if (hipGetDeviceProperties(&prop, device) == hipSuccess &&

@@ -119,10 +119,10 @@ int attend(const mqa_kv_cache* cache, const void* q, int64_t q_row, int64_t q_he
       q_head < 0 || !(scale >= 0.f) || scale > 3.4e38f ||
       (indices && (width < 1 || width > MQA_MAX_LIST)))
     return MQA_ERR_SHAPE;
-  int device = -1;
-  if (!mqa::current_device_cus() || hipGetDevice(&device) != hipSuccess) return MQA_ERR_DEVICE;
+  const int cus = mqa::current_device_cus();
+  if (!cus) return MQA_ERR_DEVICE;
   const Plan a = plan(requests, R, heads, cache->kv_heads, cache->head_dim, positions,
-                      indices != nullptr, mqa::device_cus(device));
+                      indices != nullptr, cus);
   if (workspace_bytes < a.total)
     return mqa::workspace_failed("the workspace is smaller than workspace_size_attend()");
   AttendParams p{};

@@ -186,7 +186,10 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
       }
     }
   };
-  // keys 16 g + {0..3, 8..11} share slot 2 g, {4..7, 12..15} slot 2 g + 1
+  // keys 16 g + {0..3, 8..11} share slot 2 g, {4..7, 12..15} slot 2 g + 1;
+  // column d is row D / 4 (d % 4) + d / 4, so that the lanes of a write, four
+  // columns apart, go to neighbouring rows (next to each other in the banks;
+  // as rows d they met in four of them, 43% of all LDS cycles)
   auto stage_v = [&](int i) {
 #pragma unroll
     for (int r = 0; r < EACH; ++r) {
@@ -196,7 +199,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
       const int y = v_key(r) >> 2, slot = 2 * (y >> 2) + (y & 1), half = y >> 1 & 1;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint2*>(s_v[i & 1] + v_slot(v_d(r) + j, slot) + 8 * half) =
+        *reinterpret_cast<uint2*>(s_v[i & 1] + v_slot(D / 4 * j + v_d(r) / 4, slot) + 8 * half) =
             widen4<kFp16, C>(a[j]);
     }
   };
@@ -465,24 +468,25 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
           sum == 0.f ? -__builtin_inff() : (m - kBias) * kLn2 + __builtin_logf(sum);
     }
   }
+  // score row x of product d's sums is row 32 d + x of the staged values: four
+  // neighbouring columns are in DT products (and halves of them)
   const float by = direct ? vref / sum : vref;
 #pragma unroll
-  for (int d = 0; d < DT; ++d)
+  for (int e = 0; e < 4 * DT; ++e) {
+    float v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int at = 32 * d + 8 * e + 4 * hh;
-      float v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = sum == 0.f ? 0.f : acc[d][4 * e + j] * by;
-      if (direct) {
-        const uint32_t x = to_type(v[0], T) | (uint32_t)to_type(v[1], T) << 16;
-        const uint32_t y = to_type(v[2], T) | (uint32_t)to_type(v[3], T) << 16;
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) +
-                                  ((int64_t)row * p.heads + head) * D + at) = uint2{x, y};
-      } else {
-        *reinterpret_cast<float4*>(p.part_o + slot * D + at) = float4{v[0], v[1], v[2], v[3]};
-      }
+    for (int j = 0; j < 4; ++j)
+      v[j] = sum == 0.f ? 0.f : (DT == 4 ? acc[j][e] : acc[j >> 1][e + 8 * (j & 1)]) * by;
+    const int at = 4 * (8 * (e >> 2) + 4 * hh + (e & 3));
+    if (direct) {
+      const uint32_t x = to_type(v[0], T) | (uint32_t)to_type(v[1], T) << 16;
+      const uint32_t y = to_type(v[2], T) | (uint32_t)to_type(v[3], T) << 16;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) +
+                                ((int64_t)row * p.heads + head) * D + at) = uint2{x, y};
+    } else {
+      *reinterpret_cast<float4*>(p.part_o + slot * D + at) = float4{v[0], v[1], v[2], v[3]};
     }
+  }
 }
 
 template <int T, int C, int D>

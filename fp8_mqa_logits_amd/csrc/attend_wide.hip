@@ -77,7 +77,9 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     const uint16_t* src = static_cast<const uint16_t*>(p.q) + row * p.q_row + head * p.q_head;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
-      q[k] = *reinterpret_cast<const v4u*>(src + 16 * k + 8 * hh);
+      // slot 2 k + hh of a staged key: see stage_k
+      const int slot = 2 * k + hh;
+      q[k] = *reinterpret_cast<const v4u*>(src + 16 * (slot % (D / 16)) + 8 * (slot / (D / 16)));
       if (!real) q[k] = v4u{0, 0, 0, 0};
     }
   }
@@ -157,8 +159,9 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     for (int r = 0; r < EACH; ++r) {
       if (!mine(r)) continue;
       const int x = piece(r) % (D / 16);
-      *reinterpret_cast<v4u*>(to + k_slot(k_key(r), 2 * x)) = widen8<T, C>(kreg[r][0], kreg[r][1]);
-      *reinterpret_cast<v4u*>(to + k_slot(k_key(r), 2 * x + 1)) =
+      // (the halves of a piece half a row apart: eight lanes write 128 bytes)
+      *reinterpret_cast<v4u*>(to + k_slot(k_key(r), x)) = widen8<T, C>(kreg[r][0], kreg[r][1]);
+      *reinterpret_cast<v4u*>(to + k_slot(k_key(r), D / 16 + x)) =
           widen8<T, C>(kreg[r][2], kreg[r][3]);
     }
     s_scale[i & 1][t] = sreg;

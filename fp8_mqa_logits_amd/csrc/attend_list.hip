@@ -6,21 +6,21 @@ namespace {
 
 constexpr uint32_t kNone = ~0u;  // token of an entry that names no position
 
-// A workgroup takes one row and 16 HW of the query heads of one key head, and
-// one of p.splits parts of the row's list, 32 entries and KW = 4 / HW waves at
-// a time. HW waves share 32 entries: each loads its part of their rows (16
+// A workgroup takes one row and 16 NT HW of the query heads of one key head,
+// and one of p.splits parts of the row's list, 32 entries and KW = 4 / HW waves
+// at a time. HW waves share 32 entries: each loads its part of their rows (16
 // bytes a lane, whole rows next to each other), a step ahead, into registers
-// and then into LDS, and every one of them reads all of it for its own 16
-// heads, with the products of attend_narrow.hip. (One wave for all heads would
-// widen each code once, not HW times, but its sums leave room for one wave per
-// SIMD only, and a gather's latency shows: 1.14 ms for 4096 rows of 64 heads
-// and 2048 positions.) The rows' 16-byte slots are exchanged so that the lanes
-// of a read touch all banks.
+// and then into LDS, and every one of them reads all of it for its own 16 NT
+// heads, with the products of attend_narrow.hip. For 64 heads two waves take 32
+// each: with one wave for all, its sums leave room for one wave per SIMD only
+// and a gather's latency shows (4096 rows of 64 heads and 2048 positions: 1.14
+// ms); with four of 16, every code is widened and read from LDS four times (666
+// us).
 //
 // A step's tokens (slots in the pool) are found by lanes 0 .. 31, an entry
 // each, two steps ahead, and go to the other lanes by permutation; scales go
 // through LDS, a wave for itself.
-template <int T, int C, int D, int HW>
+template <int T, int C, int D, int NT, int HW>
 __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
   constexpr int KW = 4 / HW;
   constexpr int KC = D / 64;       // 16-byte pieces of a key per lane and product
@@ -29,7 +29,7 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
   constexpr int PIECES = D / 16;   // 16-byte pieces of a row
   constexpr int GROUP = 64 * HW;   // threads that share 32 entries
   constexpr int EACH = 64 * PIECES / GROUP;  // pieces of 32 keys and 32 values per thread
-  constexpr int COLS = 16 * HW, BUFS = HW == 1 ? 1 : 2;
+  constexpr int COLS = 16 * NT * HW, BUFS = HW == 1 ? 1 : 2;
   const KvCache& c = p.c;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, n = lane & 15;
@@ -45,21 +45,22 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
       uint8_t rows[KW][BUFS][64 * D];  // 32 keys, 32 values
       float ks[4][32], vs[4][32];
     } step;
-    Finish<D, 1, HW, KW> finish;
+    Finish<D, NT, HW, KW> finish;
   } sh;
 
   int s, e;
   row_range(p, row, s, e);
-  v4u q[2 * KC];
-  {
-    const int col = tile * COLS + 16 * hw + n;
+  v4u q[NT][2 * KC];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int col = tile * COLS + 16 * (NT * hw + t) + n;
     const bool real = col < p.group;
     const uint16_t* src = static_cast<const uint16_t*>(p.q) + row * p.q_row +
                           (h * p.group + (real ? col : 0)) * p.q_head;
 #pragma unroll
     for (int k = 0; k < 2 * KC; ++k) {
-      q[k] = *reinterpret_cast<const v4u*>(src + 64 * (k >> 1) + 16 * g + 8 * (k & 1));
-      if (!real) q[k] = v4u{0, 0, 0, 0};
+      q[t][k] = *reinterpret_cast<const v4u*>(src + 64 * (k >> 1) + 16 * g + 8 * (k & 1));
+      if (!real) q[t][k] = v4u{0, 0, 0, 0};
     }
   }
   const int steps = (p.width + 31) / 32;
@@ -69,10 +70,15 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
   const int step_hi = min(steps, step_lo + per_split);
 
   const float cs = p.scale * kLog2e;
-  float m[1] = {kLowest}, l[1] = {0.f}, vref = 0x1p-126f, down = 0x1p126f;  // down = 1 / vref
-  v4f acc[1][U];
+  float m[NT], l[NT], vref = 0x1p-126f, down = 0x1p126f;  // down = 1 / vref
+  v4f acc[NT][U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) acc[0][u] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < NT; ++t) {
+    m[t] = kLowest;
+    l[t] = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) acc[t][u] = v4f{0.f, 0.f, 0.f, 0.f};
+  }
 
   // entry lane % 32 of the wave's step in a round: its list entry, the table
   // entry of the position it names, and the token
@@ -110,79 +116,94 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
     ks = *reinterpret_cast<const float*>(page + scale_at(c, 0, h, mine & page_mask));
     vs = *reinterpret_cast<const float*>(page + scale_at(c, 1, h, mine & page_mask));
   };
-  // slot of piece x of a row in its LDS row
-  auto slot_of = [&](int key, int x) {
-    return x ^ (D == 128 ? (key >> 1) & 7 : (key >> 2) & 3);
+  // byte of piece x of a row in LDS (of 32 rows, 16-byte pieces exchanged so
+  // that the lanes of every read here touch all banks: 16 rows and one piece,
+  // or whole rows four apart)
+  auto place = [&](int key, int x) {
+    if constexpr (D == 128)
+      return (key ^ (key >> 2 & 1)) * D + 16 * (x ^ (key >> 1 & 7));
+    else
+      return key * D + 16 * (x ^ (key >> 2 & 3));
   };
   auto stage = [&](int buf) {
 #pragma unroll
     for (int r = 0; r < EACH; ++r) {
-      const int x = gt + GROUP * r;
-      *reinterpret_cast<v4u*>(&sh.step.rows[kb][buf][x / PIECES * D +
-                                                     16 * slot_of(x / PIECES, x % PIECES)]) = reg[r];
+      const int x = gt + GROUP * r, key = x / PIECES;  // values: rows 32 ..
+      *reinterpret_cast<v4u*>(
+          &sh.step.rows[kb][buf][(key & 32) * D + place(key & 31, x % PIECES)]) = reg[r];
     }
   };
   auto compute = [&](uint32_t valid, int buf) {
     const bool clean = valid == ~0u;
     const uint8_t* const rows = sh.step.rows[kb][buf];
-    v4f x[2];
+    v4f x[NT][2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      x[b] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int t = 0; t < NT; ++t) x[t][b] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < KC; ++k) {
-        const v4u w = *reinterpret_cast<const v4u*>(rows + (16 * b + n) * D +
-                                                    16 * slot_of(16 * b + n, g + 4 * k));
-        x[b] = mfma<T>(widen8<T, C>(w[0], w[1]), q[2 * k], x[b]);
-        x[b] = mfma<T>(widen8<T, C>(w[2], w[3]), q[2 * k + 1], x[b]);
+        const v4u w = *reinterpret_cast<const v4u*>(rows + place(16 * b + n, g + 4 * k));
+        const v4u lo = widen8<T, C>(w[0], w[1]), hi = widen8<T, C>(w[2], w[3]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          x[t][b] = mfma<T>(lo, q[t][2 * k], x[t][b]);
+          x[t][b] = mfma<T>(hi, q[t][2 * k + 1], x[t][b]);
+        }
       }
     }
     const uint32_t sees = valid >> (4 * g);  // bit 16 b + i: entry 16 b + 4 g + i
-    float y[8], top = -__builtin_inff();
     v4f vr[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const v4f f = *reinterpret_cast<const v4f*>(&sh.step.ks[wave][16 * b + 4 * g]);
       vr[b] = *reinterpret_cast<const v4f*>(&sh.step.vs[wave][16 * b + 4 * g]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        y[4 * b + i] = x[b][i] * f[i];
-      }
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[t][b][i] *= f[i];
     }
     if (!clean) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = or_lowest(y[j], bit(sees, 16 * (j >> 2) + (j & 3)));
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          x[t][j >> 2][j & 3] = or_lowest(x[t][j >> 2][j & 3], bit(sees, 16 * (j >> 2) + (j & 3)));
     }
+    v4u pf[NT];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top = __builtin_fmaxf(top, y[j]);
-    if (__any(top > m[0] + kLag)) {
-      top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
-      top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
-      const float to = __builtin_fmaxf(m[0], __builtin_ceilf(top));
-      const float keep = __builtin_amdgcn_exp2f(m[0] - to);
-      m[0] = to;
-      l[0] *= keep;
+    for (int t = 0; t < NT; ++t) {
+      float top = x[t][0][0];
 #pragma unroll
-      for (int u = 0; u < U; ++u) acc[0][u] *= keep;
+      for (int j = 1; j < 8; ++j) top = __builtin_fmaxf(top, x[t][j >> 2][j & 3]);
+      if (__any(top > m[t] + kLag)) {
+        top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
+        top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
+        const float to = __builtin_fmaxf(m[t], __builtin_ceilf(top));
+        const float keep = __builtin_amdgcn_exp2f(m[t] - to);
+        m[t] = to;
+        l[t] *= keep;
+#pragma unroll
+        for (int u = 0; u < U; ++u) acc[t][u] *= keep;
+      }
+      const float off = kBias - m[t];
+      float e[8], sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        e[j] = __builtin_amdgcn_exp2f(x[t][j >> 2][j & 3] + off);
+        sum += e[j];  // (exp2 of -infinity: 0)
+        e[j] *= vr[j >> 2][j & 3];  // (0 where the entry names no position)
+      }
+      l[t] += sum;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        pf[t][i] = __builtin_bit_cast(uint32_t, v2h{(_Float16)e[2 * i], (_Float16)e[2 * i + 1]});
     }
-    float pr[8], sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      pr[j] = __builtin_amdgcn_exp2f(y[j] + (kBias - m[0]));
-      sum += pr[j];  // (exp2 of -infinity: 0)
-      pr[j] *= vr[j >> 2][j & 3];  // (0 where the entry names no position)
-    }
-    l[0] += sum;
-    v4u pf;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      pf[i] = __builtin_bit_cast(uint32_t, v2h{(_Float16)pr[2 * i], (_Float16)pr[2 * i + 1]});
     uint32_t v[8][VW];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int key = 16 * (j >> 2) + 4 * g + (j & 3);
-      const uint8_t* at = rows + 32 * D + key * D +
-                          16 * slot_of(key, VW == 2 ? n >> 1 : n >> 2) +
+      const uint8_t* at = rows + 32 * D + place(key, VW == 2 ? n >> 1 : n >> 2) +
                           (VW == 2 ? 8 * (n & 1) : 4 * (n & 3));
       if constexpr (VW == 2) {
         const uint2 w = *reinterpret_cast<const uint2*>(at);
@@ -208,8 +229,11 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
       for (int j = 0; j < 4; ++j) in[j] = v[4 + j][w];
       transpose4(in, b);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        acc[0][4 * w + i] = mfma<kFp16>(widen8<kFp16, C>(a[i], b[i]), pf, acc[0][4 * w + i]);
+      for (int i = 0; i < 4; ++i) {
+        const v4u vf = widen8<kFp16, C>(a[i], b[i]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[t][4 * w + i] = mfma<kFp16>(vf, pf[t], acc[t][4 * w + i]);
+      }
     }
   };
 
@@ -231,7 +255,9 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
         vref = uniform(to);
         down = uniform(1.f / to);
 #pragma unroll
-        for (int u = 0; u < U; ++u) acc[0][u] *= keep;
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int u = 0; u < U; ++u) acc[t][u] *= keep;
       }
       sh.step.ks[wave][lane & 31] = k;
       sh.step.vs[wave][lane & 31] = v * down;
@@ -265,9 +291,9 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
 
 template <int T, int C, int D>
 void launch(const AttendParams& p, dim3 grid, hipStream_t s) {
-  if (p.cols == 16) attend_list_kernel<T, C, D, 1><<<grid, 256, 0, s>>>(p);
-  if (p.cols == 32) attend_list_kernel<T, C, D, 2><<<grid, 256, 0, s>>>(p);
-  if (p.cols == 64) attend_list_kernel<T, C, D, 4><<<grid, 256, 0, s>>>(p);
+  if (p.cols == 16) attend_list_kernel<T, C, D, 1, 1><<<grid, 256, 0, s>>>(p);
+  if (p.cols == 32) attend_list_kernel<T, C, D, 2, 1><<<grid, 256, 0, s>>>(p);
+  if (p.cols == 64) attend_list_kernel<T, C, D, 2, 2><<<grid, 256, 0, s>>>(p);
 }
 
 }  // namespace

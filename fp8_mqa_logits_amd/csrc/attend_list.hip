@@ -80,17 +80,17 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
     for (int u = 0; u < U; ++u) acc[t][u] = v4f{0.f, 0.f, 0.f, 0.f};
   }
 
-  // entry lane % 32 of the wave's step in a round: its list entry, the table
-  // entry of the position it names, and the token
+  // entry lane % 32 of the wave's step in a round: its list entry as it is,
+  // what it names (-1: nothing), the table entry of that position, the token
   const int32_t* const list = p.indices + (int64_t)row * p.width;
   const int32_t* const table = c.table + (int64_t)(row / p.R) * c.table_stride;
   const int page_mask = (1 << c.page_shift) - 1;
-  auto listed = [&](int round) {
-    const int at = (step_lo + round * KW + kb) * 32 + (lane & 31);
-    const int x = list[min(at, p.width - 1)];
-    return at < min(step_hi * 32, p.width) && x >= 0 && x < e - s ? x : -1;
+  auto at_of = [&](int round) { return (step_lo + round * KW + kb) * 32 + (lane & 31); };
+  auto listed = [&](int round) { return list[min(at_of(round), p.width - 1)]; };
+  auto named = [&](int x, int round) {
+    return at_of(round) < min(step_hi * 32, p.width) && x >= 0 && x < e - s ? x : -1;
   };
-  auto looked_up = [&](int x) { return table[(x < 0 ? 0 : min(s + x, c.cap - 1)) >> c.page_shift]; };
+  auto looked_up = [&](int x) { return table[(x < 0 ? 0 : s + x) >> c.page_shift]; };
   auto token_of = [&](int x, int entry) -> uint32_t {
     const uint32_t page = (uint32_t)clamp_page(c, entry);
     return x < 0 ? kNone : (page << c.page_shift) + (uint32_t)((s + x) & page_mask);
@@ -101,20 +101,24 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
     return c.pages + (int64_t)(tok >> c.page_shift) * c.page_stride + (tok & page_mask) * (uint32_t)D;
   };
   const int k_at = code_at(c, 0, h, 0), v_at = code_at(c, 1, h, 0);
-  v4u reg[EACH];
-  float ks, vs;
-  auto load = [&](uint32_t tok) {
+  struct Codes {
+    v4u reg[EACH];
+    float ks, vs;
+    uint32_t tok;
+  };
+  auto load = [&](Codes& f, uint32_t tok) {
+    f.tok = tok;
 #pragma unroll
     for (int r = 0; r < EACH; ++r) {
       const int x = gt + GROUP * r, key = x / PIECES % 32;
       const uint8_t* at = token_row((uint32_t)__shfl((int)tok, key, 64));
-      reg[r] = *reinterpret_cast<const v4u*>(at + (x < 32 * PIECES ? k_at : v_at) +
+      f.reg[r] = *reinterpret_cast<const v4u*>(at + (x < 32 * PIECES ? k_at : v_at) +
                                              16 * (x % PIECES));
     }
     const uint32_t mine = tok == kNone ? 0u : tok;
     const uint8_t* page = c.pages + (int64_t)(mine >> c.page_shift) * c.page_stride;
-    ks = *reinterpret_cast<const float*>(page + scale_at(c, 0, h, mine & page_mask));
-    vs = *reinterpret_cast<const float*>(page + scale_at(c, 1, h, mine & page_mask));
+    f.ks = *reinterpret_cast<const float*>(page + scale_at(c, 0, h, mine & page_mask));
+    f.vs = *reinterpret_cast<const float*>(page + scale_at(c, 1, h, mine & page_mask));
   };
   // byte of piece x of a row in LDS (of 32 rows, 16-byte pieces exchanged so
   // that the lanes of every read here touch all banks: 16 rows and one piece,
@@ -125,12 +129,12 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
     else
       return key * D + 16 * (x ^ (key >> 2 & 3));
   };
-  auto stage = [&](int buf) {
+  auto stage = [&](const Codes& f, int buf) {
 #pragma unroll
     for (int r = 0; r < EACH; ++r) {
       const int x = gt + GROUP * r, key = x / PIECES;  // values: rows 32 ..
       *reinterpret_cast<v4u*>(
-          &sh.step.rows[kb][buf][(key & 32) * D + place(key & 31, x % PIECES)]) = reg[r];
+          &sh.step.rows[kb][buf][(key & 32) * D + place(key & 31, x % PIECES)]) = f.reg[r];
     }
   };
   auto compute = [&](uint32_t valid, int buf) {
@@ -246,9 +250,9 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
     };
     // a round's scales and which of its entries name positions
     uint32_t valid;
-    auto take_scales = [&](uint32_t tok) {
-      valid = (uint32_t)__ballot(tok != kNone);
-      const float k = tok != kNone ? ks * cs : 0.f, v = tok != kNone ? vs : 0.f;
+    auto take_scales = [&](const Codes& f) {
+      valid = (uint32_t)__ballot(f.tok != kNone);
+      const float k = f.tok != kNone ? f.ks * cs : 0.f, v = f.tok != kNone ? f.vs : 0.f;
       const float finite = v < __builtin_inff() ? v : 0.f;
       if (__any(finite > vref)) {
         const float to = power_above(wave_max(finite)), keep = vref / to;
@@ -263,24 +267,27 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
       sh.step.vs[wave][lane & 31] = v * down;
       __builtin_amdgcn_wave_barrier();
     };
-    int x = listed(0), entry = looked_up(x);
-    uint32_t tok = token_of(x, entry), next;
-    load(tok);
-    x = listed(1);
-    entry = looked_up(x);
-    next = token_of(x, entry);
-    x = listed(2);
-    entry = looked_up(x);
+    // Loads come back in order: what a later round's addresses wait for is asked
+    // for before the next round's codes, so that no one waits for these before
+    // they are used (as the compiler placed them otherwise: 149 us, not 123, for
+    // 64 x 2 rows of 2048 positions and 8 heads; codes two rounds ahead added
+    // nothing to that).
+    Codes codes;
+    int x = named(listed(0), 0), entry = looked_up(x), x_raw = listed(1);
+    auto ahead = [&](int round) {  // token of `round`; entry of the next, list of the one after
+      const uint32_t tok = token_of(x, entry);
+      x = named(x_raw, round + 1);
+      entry = looked_up(x);
+      x_raw = listed(round + 2);
+      return tok;
+    };
+    load(codes, ahead(0));
     for (int i = 0; i < rounds; ++i) {
       const int buf = BUFS == 1 ? 0 : i & 1;
-      stage(buf);
-      take_scales(tok);
+      stage(codes, buf);
+      take_scales(codes);
       sync();
-      tok = next;
-      if (i + 1 < rounds) load(tok);
-      next = token_of(x, entry);
-      x = listed(i + 3);
-      entry = looked_up(x);
+      load(codes, ahead(i + 1));
       compute(valid, buf);
       if constexpr (BUFS == 1) __builtin_amdgcn_wave_barrier();
     }

@@ -40,7 +40,8 @@ def store(pool, k, v, table, starts, counts=None):
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
 @pytest.mark.parametrize("starts,R,Hkv,D,P,B", [
     ([0], 1, 1, 64, 16, 16), ([7, 15, 16, 31], 1, 2, 128, 16, 16), ([0, 33], 64, 2, 64, 32, 32),
-    ([5, 64, 127], 70, 3, 128, 64, 64), ([100], 200, 1, 128, 128, 32), ([3, 9], 2, 2, 64, 256, 128)])
+    ([5, 64, 127], 70, 3, 128, 64, 64), ([100], 200, 1, 128, 128, 32), ([3, 9], 2, 2, 64, 256, 128),
+    ([5], 300, 1, 128, 512, 256)])
 def test_append(starts, R, Hkv, D, P, B, dtype, codes):
     say(f"case: append {starts} {R} {Hkv} {D} {P} {B} {dtype} {codes}")
     table, pages = ref.make_table([s + R for s in starts], P, 2)

@@ -71,23 +71,40 @@ struct Plan {
   size_t ml, o, total;  // workspace offsets
 };
 
-// The widest tile whose workgroups, each with 512 keys at least, give every
-// compute unit one; the narrowest where none does (window_333: 20 -> us).
+// Tiles: the widest whose workgroups, with 512 keys each at least, give every
+// compute unit one, else the narrowest (333 rows of 12 heads, each its own key
+// head, over a window of 83: 6 us on 16 columns, 20 on 256 with the keys split).
+// Parts of a tile's keys: every round of resident workgroups takes the time of
+// its keys and of a start and an end that 512 keys' time stands for (1024 for
+// the wide tiles, whose sums are larger); the join takes twice that. One round
+// comes out where the keys allow it: 32 x 131072 positions of 2 heads 373 us in
+// 16 parts, 384 in 24, 425 in 64; 48 uneven requests of 4 heads 123.5 us in 5,
+// 124.5 in 8; one request of 777 positions 10 us in one, 13 in two.
 Plan plan(int requests, int R, int heads, int kv_heads, int head_dim, int positions, bool list,
           int cus) {
   Plan a{};
   const int group = heads / kv_heads, columns = list ? group : R * group;
   const int64_t units = (int64_t)(list ? requests * R : requests) * kv_heads;
-  const int64_t most = positions < 1024 ? 1 : positions / 512;
   a.cols = 16;
   while (a.cols < columns && a.cols < (list ? 64 : 256)) a.cols *= 2;
   auto items = [&]() { return units * ((columns + a.cols - 1) / a.cols); };
+  const int64_t most = positions < 1024 ? 1 : positions / 512;
   while (!list && a.cols > 16 && items() * most < cus) a.cols /= 2;
   a.tiles = (columns + a.cols - 1) / a.cols;
-  // splits: enough workgroups for the device
-  const int64_t want = ((int64_t)(a.cols > 64 ? 1 : 6) * cus + items() - 1) / items();
-  a.splits = (int)(want < most ? want : most);
-  a.splits = a.splits < 1 ? 1 : (a.splits > mqa::kMaxSplits ? mqa::kMaxSplits : a.splits);
+  // workgroups that a compute unit holds at once, by their registers
+  const bool wide = a.cols > 64;
+  const int held = list ? 2 : a.cols == 16 ? 4 : a.cols == 32 ? (head_dim == 64 ? 4 : 2)
+                                               : a.cols == 128 ? 2 : 1;
+  const int64_t resident = (int64_t)held * cus, n = items(), ends = wide ? 1024 : 512;
+  int64_t best = 0;
+  for (int s = 1; s <= mqa::kMaxSplits && (s == 1 || s * 256 <= positions); ++s) {
+    const int64_t rounds = (n * s + resident - 1) / resident;
+    const int64_t cost = rounds * ((positions + s - 1) / s + ends) + (s > 1 ? 2 * ends : 0);
+    if (s > 1 && rounds > 4) break;
+    if (s > 1 && cost >= best) continue;
+    best = cost;
+    a.splits = s;
+  }
   const int64_t slots = a.splits > 1 ? items() * a.splits * a.cols : 0;
   a.ml = 0;
   a.o = (size_t)((slots * 8 + 255) / 256 * 256);

@@ -279,12 +279,13 @@ __device__ __forceinline__ void finish(const AttendParams& p, Finish<D, NT, HW, 
         for (int w = 0; w < KW; ++w) v[u] += sh.part[w][u * 16 + r][col];
       }
       const int d = U * r + u0;
+      if (!real) continue;
       if (!direct) {
         float* const o = p.part_o + slot * D + d;
 #pragma unroll
         for (int u = 0; u < US; u += 2)
           *reinterpret_cast<float2*>(o + u) = float2{v[u], v[u + 1]};
-      } else if (real) {
+      } else {
 #pragma unroll
         for (int u = 0; u < US; u += 2) {
           const float x = sum == 0.f ? 0.f : v[u] * inv, y = sum == 0.f ? 0.f : v[u + 1] * inv;

@@ -16,6 +16,7 @@ import torch
 CODES = {"e4m3": 0, "int8": 1}
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 MAX_LIST = 1 << 16
+NO_WORKSPACE = 256  # workspace_size_attend of a call that needs none
 
 EXPORTS = ("mqa_kv_page_bytes", "mqa_kv_append", "mqa_kv_read", "workspace_size_attend",
            "mqa_attend_paged", "mqa_attend_topk")
@@ -281,16 +282,15 @@ def _attend(layout, q, cache, page_table, indices, starts, ends, scale, out, lse
             raise ValueError("indices must be a tensor [rows, width]")
         positions = indices.shape[1]
         _dense(indices, "indices", torch.int32, (rows, positions), dev)
-    shape = (rows, heads, layout.head_dim)
     if scale is None:
         scale = 1.0 / math.sqrt(layout.head_dim)
     lib = _load()
     with _launch(dev, stream):
         s = _stream(dev, stream)
         if out is None:
-            out = torch.empty(shape, dtype=q.dtype, device=dev)
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
         else:
-            _dense(out, "out", q.dtype, shape, dev)
+            _dense(out, "out", q.dtype, (rows, heads, layout.head_dim), dev)
         if lse is not None:
             _dense(lse, "lse", torch.float32, (rows, heads), dev)
         elif return_lse:
@@ -298,7 +298,8 @@ def _attend(layout, q, cache, page_table, indices, starts, ends, scale, out, lse
         if workspace is None:
             n = lib.workspace_size_attend(requests, R, heads, layout.kv_heads, layout.head_dim,
                                           positions, dev.index)
-            workspace = torch.empty(n or 256, dtype=torch.uint8, device=dev)
+            if n > NO_WORKSPACE:
+                workspace = torch.empty(n, dtype=torch.uint8, device=dev)
         else:
             _on(workspace, "workspace", torch.uint8, dev)
             if not workspace.is_contiguous():
@@ -306,7 +307,8 @@ def _attend(layout, q, cache, page_table, indices, starts, ends, scale, out, lse
         head = (c, q.data_ptr(), q_row, q_head, DTYPES[q.dtype])
         tail = (starts.data_ptr(), ends.data_ptr(), out.data_ptr(),
                 None if lse is None else lse.data_ptr(), requests, R, heads, float(scale),
-                workspace.data_ptr(), workspace.numel(), s)
+                None if workspace is None else workspace.data_ptr(),
+                0 if workspace is None else workspace.numel(), s)
         if indices is None:
             rc = lib.mqa_attend_paged(*head, *tail)
         else:

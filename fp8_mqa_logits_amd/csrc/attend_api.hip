@@ -65,6 +65,8 @@ bool rows_ok(int requests, int R) {
   return requests >= 1 && R >= 1 && (int64_t)requests * R <= MQA_MAX_ROWS;
 }
 
+constexpr size_t kNoWorkspace = 256;  // what is asked for where nothing is needed
+
 // How an attention call is cut (AttendParams), from what the host knows.
 struct Plan {
   int cols, tiles, splits;
@@ -109,7 +111,7 @@ Plan plan(int requests, int R, int heads, int kv_heads, int head_dim, int positi
   a.ml = 0;
   a.o = (size_t)((slots * 8 + 255) / 256 * 256);
   a.total = a.o + (size_t)slots * head_dim * 4;
-  if (a.total == 0) a.total = 256;
+  if (a.total == 0) a.total = kNoWorkspace;
   return a;
 }
 
@@ -125,7 +127,7 @@ int attend(const mqa_kv_cache* cache, const void* q, int64_t q_row, int64_t q_he
            const int32_t* indices, int width, const int32_t* starts, const int32_t* ends,
            void* out, float* lse, int requests, int R, int heads, float scale, void* workspace,
            size_t workspace_bytes, int positions, void* stream) {
-  if (!cache || !q || !starts || !ends || !out || !workspace) return MQA_ERR_NULL;
+  if (!cache || !q || !starts || !ends || !out) return MQA_ERR_NULL;
   const int rc = cache_pointers(cache);
   if (rc != MQA_OK) return rc;
   if (!aligned(q, 16) || q_row % 8 != 0 || q_head % 8 != 0 || !aligned(starts, 4) ||
@@ -140,7 +142,8 @@ int attend(const mqa_kv_cache* cache, const void* q, int64_t q_row, int64_t q_he
   if (!cus) return MQA_ERR_DEVICE;
   const Plan a = plan(requests, R, heads, cache->kv_heads, cache->head_dim, positions,
                       indices != nullptr, cus);
-  if (workspace_bytes < a.total)
+  if (!workspace && a.total > kNoWorkspace) return MQA_ERR_NULL;
+  if (workspace && workspace_bytes < a.total)
     return mqa::workspace_failed("the workspace is smaller than workspace_size_attend()");
   AttendParams p{};
   p.c = kernel_cache(cache);

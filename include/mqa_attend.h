@@ -101,8 +101,8 @@ int mqa_kv_read(const mqa_kv_cache* cache, void* k, void* v, int dtype, const in
  * Bytes of workspace an attention call needs on `device`: requests * R rows
  * of `heads` query heads; `positions` the most that a row may see
  * (mqa_attend_paged: table_stride * page_size; mqa_attend_topk: the list's
- * width). May be 256 where a call needs none to speak of; 0 for sizes out of
- * range or a device that is not gfx950.
+ * width). 256 where the call needs none (its workspace may then be NULL); 0 for
+ * sizes out of range or a device that is not gfx950.
  */
 size_t workspace_size_attend(int requests, int R, int heads, int kv_heads, int head_dim,
                              int positions, int device);

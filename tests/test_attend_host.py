@@ -92,7 +92,7 @@ def test_page_bytes():
 
 
 def test_attend_errors():
-    for name in ("q", "starts", "ends", "out", "ws"):
+    for name in ("q", "starts", "ends", "out"):
         assert paged(**{name: 0}) == 1, name
     assert paged(cache(pages=0)) == 1
     assert paged(cache(table=0)) == 1

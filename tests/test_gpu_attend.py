@@ -360,9 +360,14 @@ def test_binding_refusals():
     with pytest.raises(mqa.MQAError) as e:
         call(L, q, cache, table, starts, ends, scale=-1.0)
     assert e.value.code == 3
-    with pytest.raises(mqa.MQAError) as e:
-        call(L, q, cache, table, starts, ends, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
-    assert e.value.code in (1, 4)
+    many = torch.zeros(1, 2000, dtype=torch.int32, device="cuda")  # keys in parts
+    size = mqa.workspace_size_attend(1, 2, 8, L, 2000 * 32)
+    assert size > 256
+    for n, code in ((0, 1), (512, 4)):
+        with pytest.raises(mqa.MQAError) as e:
+            call(L, q, cache, many, starts, ends,
+                 workspace=torch.empty(n, dtype=torch.uint8, device="cuda"))
+        assert e.value.code == code
     wide = torch.zeros(2, 8, 132, dtype=BF16, device="cuda")
     with pytest.raises(mqa.MQAError) as e:
         call(L, wide[:, :, 4:], cache, table, starts, ends)

@@ -11,7 +11,7 @@ namespace mqa {
 
 enum { kE4m3 = 0, kInt8 = 1 };
 enum { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
-constexpr int kMaxSplits = 64;  // parts of a tile's keys
+constexpr int kMaxSplits = 256;  // parts of a tile's keys, a multiple of 64
 
 struct KvCache {
   uint8_t* pages;

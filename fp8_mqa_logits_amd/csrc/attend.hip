@@ -4,40 +4,65 @@
 namespace mqa {
 namespace {
 
-// Joins the splits of a (row, query head), in order, a wave each: a lane a
-// split for the weights, then D / 64 columns of the output. A split that saw
-// nothing has l = 0.
-template <int T, int D>
+// Joins the splits of a (row, query head), in order, with WAYS waves each: a
+// lane every 64th split for the weights, then D / 64 columns of the output of
+// every WAYS-th split. A split that saw nothing has l = 0. (Few splits: one
+// wave, many rows a workgroup; many: their reads in parallel.)
+template <int T, int D, int WAYS>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
-  constexpr int EACH = D / 64;
-  const int lane = threadIdx.x & 63;
-  const int64_t pair = (p.block0 + blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (pair >= (int64_t)p.rows * p.heads) return;
-  const int row = (int)(pair / p.heads), head = (int)(pair % p.heads), h = head / p.group;
+  constexpr int EACH = D / 64, MANY = kMaxSplits / 64;
+  __shared__ float s_v[4][D];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, way = wave % WAYS;
+  const int64_t pair = (p.block0 + blockIdx.x) * (4 / WAYS) + wave / WAYS;
+  const bool real = pair < (int64_t)p.rows * p.heads;
+  if (WAYS == 1 && !real) return;
+  const int row = (int)(real ? pair / p.heads : 0), head = (int)(real ? pair % p.heads : 0);
+  const int h = head / p.group;
   const int per_unit = p.indices ? 1 : p.R;
   const int column = row % per_unit * p.group + head % p.group;
   const int64_t item = ((int64_t)(row / per_unit) * p.tiles + column / p.cols) * p.c.kv_heads + h;
   const int64_t first = item * p.splits * p.cols + column % p.cols;
-  static_assert(kMaxSplits == 64, "a lane a split");
-  const bool mine = lane < p.splits;
-  const float* ml = p.part_ml + 2 * (first + (int64_t)(mine ? lane : 0) * p.cols);
-  const float ls = mine ? ml[1] : 0.f;
-  const float ms = ls != 0.f ? ml[0] : kLowest;
-  const float top = wave_max(ms);
-  const float w = ls != 0.f ? __builtin_amdgcn_exp2f(ms - top) : 0.f;
-  float sum = ls * w;
+  float ms[MANY], ls[MANY], w[MANY], top = kLowest, sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < MANY; ++k) {
+    const int s = lane + 64 * k;
+    const float* ml = p.part_ml + 2 * (first + (int64_t)(s < p.splits ? s : 0) * p.cols);
+    ls[k] = s < p.splits ? ml[1] : 0.f;
+    ms[k] = ls[k] != 0.f ? ml[0] : kLowest;
+    top = __builtin_fmaxf(top, ms[k]);
+  }
+  top = wave_max(top);
+#pragma unroll
+  for (int k = 0; k < MANY; ++k) {
+    w[k] = ls[k] != 0.f ? __builtin_amdgcn_exp2f(ms[k] - top) : 0.f;
+    sum = __builtin_fmaf(ls[k], w[k], sum);
+  }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o, 64);
   const float* o = p.part_o + first * D + EACH * lane;
   float v[EACH] = {};
-#pragma unroll 8
-  for (int s = 0; s < p.splits; ++s) {
-    const float ws = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), s));
 #pragma unroll
-    for (int e = 0; e < EACH; ++e) {
-      const float x = o[(int64_t)s * p.cols * D + e];
-      v[e] = ws == 0.f ? v[e] : __builtin_fmaf(x, ws, v[e]);
+  for (int k = 0; k < MANY; ++k) {
+    const int end = min(p.splits - 64 * k, 64);
+#pragma unroll 8
+    for (int s = way; s < end; s += WAYS) {
+      const float ws = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w[k]), s));
+#pragma unroll
+      for (int e = 0; e < EACH; ++e) {
+        const float x = o[(int64_t)(64 * k + s) * p.cols * D + e];
+        v[e] = ws == 0.f ? v[e] : __builtin_fmaf(x, ws, v[e]);
+      }
     }
+  }
+  if constexpr (WAYS > 1) {
+#pragma unroll
+    for (int e = 0; e < EACH; ++e) s_v[wave][EACH * lane + e] = v[e];
+    __syncthreads();
+    if (way != 0 || !real) return;
+#pragma unroll
+    for (int k = 1; k < WAYS; ++k)
+#pragma unroll
+      for (int e = 0; e < EACH; ++e) v[e] += s_v[wave + k][EACH * lane + e];
   }
   uint16_t* const out = static_cast<uint16_t*>(p.out) + pair * D + EACH * lane;
 #pragma unroll
@@ -69,11 +94,17 @@ extern "C" int mqa_attend_launch(const mqa::AttendParams* all, hipStream_t s) {
               else
                 attend_wide(p, grid, s);
             });
-  if (all->splits > 1)
-    in_pieces(*all, ((int64_t)all->rows * all->heads + 3) / 4, [&](const AttendParams& p, dim3 grid) {
+  if (all->splits > 1) {
+    const int64_t pairs = (int64_t)all->rows * all->heads;
+    const bool many = all->splits > 16;
+    in_pieces(*all, many ? pairs : (pairs + 3) / 4, [&](const AttendParams& p, dim3 grid) {
       dispatch(p, [&](auto t, auto, auto d) {
-        attend_join_kernel<t.value, d.value><<<grid, 256, 0, s>>>(p);
+        if (many)
+          attend_join_kernel<t.value, d.value, 4><<<grid, 256, 0, s>>>(p);
+        else
+          attend_join_kernel<t.value, d.value, 1><<<grid, 256, 0, s>>>(p);
       });
     });
+  }
   return (int)hipGetLastError();
 }

@@ -46,6 +46,7 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
       float ks[4][32], vs[4][32];
     } step;
     Finish<D, NT, HW, KW> finish;
+    int used[4];
   } sh;
 
   int s, e;
@@ -63,7 +64,25 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
       if (!real) q[t][k] = v4u{0, 0, 0, 0};
     }
   }
-  const int steps = (p.width + 31) / 32;
+  // A row that cannot fill its list (its valid entries come first, but for
+  // what a caller wrote himself) ends it at the last entry that names a position.
+  int used = p.width;
+  if (e - s < p.width) {
+    used = 0;
+    const int32_t* const list = p.indices + (int64_t)row * p.width;
+    for (int i = threadIdx.x; i < p.width; i += 256) {
+      const int x = list[i];
+      if (x >= 0 && x < e - s) used = i + 1;
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) used = max(used, __shfl_xor(used, o, 64));
+    if (lane == 0) sh.used[wave] = used;
+    __syncthreads();
+    used = max(max(sh.used[0], sh.used[1]), max(sh.used[2], sh.used[3]));
+    used = __builtin_amdgcn_readfirstlane(used);
+    __syncthreads();
+  }
+  const int steps = (used + 31) / 32;
   const int per_split = ((steps + p.splits - 1) / p.splits + KW - 1) / KW * KW;
   const int step_lo = split * per_split;
   const int rounds = (min(steps, step_lo + per_split) - step_lo + KW - 1) / KW;
@@ -88,7 +107,7 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
   auto at_of = [&](int round) { return (step_lo + round * KW + kb) * 32 + (lane & 31); };
   auto listed = [&](int round) { return list[min(at_of(round), p.width - 1)]; };
   auto named = [&](int x, int round) {
-    return at_of(round) < min(step_hi * 32, p.width) && x >= 0 && x < e - s ? x : -1;
+    return at_of(round) < min(step_hi * 32, used) && x >= 0 && x < e - s ? x : -1;
   };
   auto looked_up = [&](int x) { return table[(x < 0 ? 0 : s + x) >> c.page_shift]; };
   auto token_of = [&](int x, int entry) -> uint32_t {

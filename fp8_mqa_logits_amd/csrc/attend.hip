@@ -39,18 +39,27 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
   }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o, 64);
-  const float* o = p.part_o + first * D + EACH * lane;
-  float v[EACH] = {};
+  typedef float Cols __attribute__((ext_vector_type(EACH)));
+  const float* const o = p.part_o + first * D + EACH * lane;
+  const int64_t stride = (int64_t)p.cols * D;
+  Cols v = 0.f;
 #pragma unroll
   for (int k = 0; k < MANY; ++k) {
+    constexpr int AHEAD = 8;  // reads on their way
     const int end = min(p.splits - 64 * k, 64);
-#pragma unroll 8
-    for (int s = way; s < end; s += WAYS) {
-      const float ws = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w[k]), s));
+    for (int s0 = way; s0 < end; s0 += WAYS * AHEAD) {
+      Cols x[AHEAD];
 #pragma unroll
-      for (int e = 0; e < EACH; ++e) {
-        const float x = o[(int64_t)(64 * k + s) * p.cols * D + e];
-        v[e] = ws == 0.f ? v[e] : __builtin_fmaf(x, ws, v[e]);
+      for (int a = 0; a < AHEAD; ++a)
+        x[a] = *reinterpret_cast<const Cols*>(o + (64 * k + min(s0 + WAYS * a, end - 1)) * stride);
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a) {
+        const int s = s0 + WAYS * a;
+        const float ws = s < end ? __int_as_float(__builtin_amdgcn_readlane(
+                                       __float_as_int(w[k]), s & 63)) : 0.f;
+        // (not times 0: a part that saw nothing may hold anything)
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) v[e] = ws == 0.f ? v[e] : __builtin_fmaf(x[a][e], ws, v[e]);
       }
     }
   }

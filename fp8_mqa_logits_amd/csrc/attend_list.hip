@@ -40,10 +40,10 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
   const int h = (int)(item % c.kv_heads), tile = (int)(item / c.kv_heads % p.tiles);
   const int row = (int)(item / c.kv_heads / p.tiles);
 
-  __shared__ union {
+  __shared__ __align__(16) union {
     struct {
-      uint8_t rows[KW][BUFS][64 * D];  // 32 keys, 32 values
-      float ks[4][32], vs[4][32];
+      __align__(16) uint8_t rows[KW][BUFS][64 * D];  // 32 keys, 32 values
+      __align__(16) float ks[4][32], vs[4][32];
     } step;
     Finish<D, NT, HW, KW> finish;
     int used[4];
@@ -176,30 +176,36 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
       }
     }
     const uint32_t sees = valid >> (4 * g);  // bit 16 b + i: entry 16 b + 4 g + i
-    v4f vr[2];
+    v4f f[2], vr[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const v4f f = *reinterpret_cast<const v4f*>(&sh.step.ks[wave][16 * b + 4 * g]);
+      f[b] = *reinterpret_cast<const v4f*>(&sh.step.ks[wave][16 * b + 4 * g]);
       vr[b] = *reinterpret_cast<const v4f*>(&sh.step.vs[wave][16 * b + 4 * g]);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[t][b][i] *= f[i];
-    }
-    if (!clean) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          x[t][j >> 2][j & 3] = or_lowest(x[t][j >> 2][j & 3], bit(sees, 16 * (j >> 2) + (j & 3)));
     }
     v4u pf[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float top = x[t][0][0];
+      float e[8], sum;
+      auto exponentials = [&]() {
+        const float off = kBias - m[t];
 #pragma unroll
-      for (int j = 1; j < 8; ++j) top = __builtin_fmaxf(top, x[t][j >> 2][j & 3]);
-      if (__any(top > m[t] + kLag)) {
+        for (int j = 0; j < 8; ++j)
+          e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][j >> 2][j & 3], f[j >> 2][j & 3], off));
+        if (!clean) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) e[j] = or_zero(e[j], bit(sees, 16 * (j >> 2) + (j & 3)));
+        }
+        sum = e[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) sum += e[j];
+      };
+      exponentials();
+      if (__any(!(sum <= kMost))) {  // m moves
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          top = __builtin_fmaxf(top, or_lowest(x[t][j >> 2][j & 3] * f[j >> 2][j & 3],
+                                               bit(sees, 16 * (j >> 2) + (j & 3))));
         top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
         top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
         const float to = __builtin_fmaxf(m[t], __builtin_ceilf(top));
@@ -208,16 +214,11 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
         l[t] *= keep;
 #pragma unroll
         for (int u = 0; u < U; ++u) acc[t][u] *= keep;
-      }
-      const float off = kBias - m[t];
-      float e[8], sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        e[j] = __builtin_amdgcn_exp2f(x[t][j >> 2][j & 3] + off);
-        sum += e[j];  // (exp2 of -infinity: 0)
-        e[j] *= vr[j >> 2][j & 3];  // (0 where the entry names no position)
+        exponentials();
       }
       l[t] += sum;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] *= vr[j >> 2][j & 3];  // (0 where nothing is named)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         pf[t][i] = __builtin_bit_cast(uint32_t, v2h{(_Float16)e[2 * i], (_Float16)e[2 * i + 1]});

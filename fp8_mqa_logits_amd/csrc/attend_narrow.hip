@@ -27,7 +27,7 @@ namespace {
 // earlier; a single set of registers leaves room for three or four waves per
 // SIMD, which hide what that does not.
 template <int T, int C, int D, int NT>
-__global__ __launch_bounds__(256, NT == 4 ? 1 : NT == 2 ? 2 : 4) void attend_narrow_kernel(AttendParams p) {
+__global__ __launch_bounds__(256, NT == 4 ? 1 : NT == 2 && D == 128 ? 2 : 4) void attend_narrow_kernel(AttendParams p) {
   constexpr int KC = D / 64;       // 16-byte pieces of a key per lane
   constexpr int U = D / 16;        // products per step and column tile
   constexpr int VW = D / 64;       // dwords of a value per lane
@@ -176,18 +176,10 @@ __global__ __launch_bounds__(256, NT == 4 ? 1 : NT == 2 ? 2 : 4) void attend_nar
     const bool clean = pos0 >= span.in_lo && pos0 + 32 <= span.in_hi;  // all rows see all keys
     uint32_t sees[NT], ill = 0;  // bit 16 b + i: key 16 b + 4 g + i
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[t][j >> 2][j & 3] *= f[j >> 2];
+    for (int t = 0; t < NT; ++t) sees[t] = ~0u;
     if (!clean) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        sees[t] = seen_bits(pos0, col_s[t], col_e[t]) >> (4 * g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          x[t][j >> 2][j & 3] =
-              or_lowest(x[t][j >> 2][j & 3], bit(sees[t], 16 * (j >> 2) + (j & 3)));
-      }
+      for (int t = 0; t < NT; ++t) sees[t] = seen_bits(pos0, col_s[t], col_e[t]) >> (4 * g);
       // values that no row sees become 0; a NaN code, which some rows may
       // see and others not, becomes 0 too and is put back through the P of
       // the rows that see it (0 * NaN would reach the others)
@@ -211,10 +203,27 @@ __global__ __launch_bounds__(256, NT == 4 ? 1 : NT == 2 ? 2 : 4) void attend_nar
     v4u pf[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float top = x[t][0][0];
+      float e[8], sum;
+      auto exponentials = [&]() {
+        const float off = kBias - m[t];
 #pragma unroll
-      for (int j = 1; j < 8; ++j) top = __builtin_fmaxf(top, x[t][j >> 2][j & 3]);
-      if (__any(top > m[t] + kLag)) {
+        for (int j = 0; j < 8; ++j)
+          e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][j >> 2][j & 3], f[j >> 2], off));
+        if (!clean) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) e[j] = or_zero(e[j], bit(sees[t], 16 * (j >> 2) + (j & 3)));
+        }
+        sum = e[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) sum += e[j];
+      };
+      exponentials();
+      if (__any(!(sum <= kMost))) {  // m moves
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          top = __builtin_fmaxf(top, or_lowest(x[t][j >> 2][j & 3] * f[j >> 2],
+                                               bit(sees[t], 16 * (j >> 2) + (j & 3))));
         top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
         top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
         const float to = __builtin_fmaxf(m[t], __builtin_ceilf(top));
@@ -223,16 +232,11 @@ __global__ __launch_bounds__(256, NT == 4 ? 1 : NT == 2 ? 2 : 4) void attend_nar
         l[t] *= keep;
 #pragma unroll
         for (int u = 0; u < U; ++u) acc[t][u] *= keep;
-      }
-      const float off = kBias - m[t];
-      float e[8], sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        e[j] = __builtin_amdgcn_exp2f(x[t][j >> 2][j & 3] + off);
-        sum += e[j];  // (what is unseen: exp2 of -infinity)
-        e[j] *= vr[j >> 2];
+        exponentials();
       }
       l[t] += sum;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] *= vr[j >> 2];
       if (!clean) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {

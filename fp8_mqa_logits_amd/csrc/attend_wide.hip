@@ -19,8 +19,8 @@ namespace {
 // that the matrix unit and the vector unit work at the same time. One barrier
 // a tile: between the halves of tile i, when the keys of tile i + 1 are in
 // LDS; its values follow during the second half and are first read after the
-// next barrier. m and vref only move by powers of two, so that the P in flight
-// can be rescaled exactly.
+// next barrier. m and vref only move by powers of two, so that a P in flight can
+// be rescaled exactly.
 template <int T, int C, int D, int W>
 __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) {
   constexpr int THREADS = 64 * W;
@@ -288,8 +288,10 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
       f[j] = __builtin_bit_cast(uint32_t, v2h{(_Float16)e[2 * j], (_Float16)e[2 * j + 1]});
     return f;
   };
-  // scores -> probabilities of one half
+  // scores -> probabilities of one half; of a plain tile's, the largest sum of
+  // eight of them: over kMost, m has to move and they are to be formed again
   auto soft = [&](auto is_plain, const v16f& s, Prob& pr, int i, int half) {
+    float over = 0.f;
     if constexpr (is_plain.value) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -302,6 +304,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
           sum += e[j];
         }
         l = __builtin_fmaf(sum, iv[g], l);
+        over += sum;
         pr.f[k] = pack(e);
       }
     } else {
@@ -323,40 +326,24 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
         pr.f[k] = pack(e);
       }
     }
+    return over;
   };
-  // a half's largest score in this lane
-  auto largest = [&](auto is_plain, const v16f& s, int i, int half) {
-    if constexpr (is_plain.value) {
-      float x = s[0], y = s[8];
+  // moves m to a half's largest score, where that is above it
+  auto settle = [&](const v16f& s, int i, int half) {
+    const uint32_t sees = seen_keys(i, half);
+    float top = -__builtin_inff();
 #pragma unroll
-      for (int j = 1; j < 8; ++j) {
-        x = __builtin_fmaxf(x, s[j]);
-        y = __builtin_fmaxf(y, s[8 + j]);
-      }
-      return __builtin_fmaxf(x * fk[2 * half], y * fk[2 * half + 1]);
-    } else {
-      const uint32_t sees = seen_keys(i, half);
-      float top = -__builtin_inff();
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        top = __builtin_fmaxf(
-            top, or_lowest(s[e] * fk[2 * half + (e >> 3)], bit(sees, key_at(e))));
-      return top;
-    }
-  };
-  // moves m where a score passes it by more than kLag; `pending`: the P not
-  // yet in the sums
-  auto passes = [&](float top) { return __any(top > m + kLag); };
-  auto settle = [&](float top, Prob& pending) {
-    if (!passes(top)) return;
-    const float x = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
-    const float to = __builtin_fmaxf(m, __builtin_ceilf(x));
+    for (int e = 0; e < 16; ++e)
+      top = __builtin_fmaxf(top,
+                            or_lowest(s[e] * fk[2 * half + (e >> 3)], bit(sees, key_at(e))));
+    top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
+    if (!__any(top > m)) return;
+    const float to = __builtin_fmaxf(m, __builtin_ceilf(top));
     const float keep = __builtin_amdgcn_exp2f(m - to);
     m = to;
     l *= keep;
 #pragma unroll
     for (int d = 0; d < DT; ++d) acc[d] *= keep;
-    rescale_pending(pending, keep);
   };
 
   if (tiles > 0) {
@@ -386,69 +373,102 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
       asm volatile("" : "+v"(pr.f[0]), "+v"(pr.f[1]), "+v"(x));
     };
     // first half: s0 -> p0, scores of the second, values of the last tile's
-    // second; keys of the next tile into LDS. The largest of the scores.
+    // second; keys of the next tile into LDS. Whether p0 is to be formed again.
     auto half0 = [&](auto is_plain, int i) {
+      const float before = l;
       scores(s1, i, 1);
-      soft(is_plain, s0, p0, i, 0);
-      values(p1, i - 1, 1);
-      stage_k(i + 1);
-      load_k(i + 2);
-      const float top = largest(is_plain, s1, i, 1);
-      keep_here(p0, l);
-      clean_v(i + 1);
-      find_k(i + 3);
-      __syncthreads();
-      return top;
+      if constexpr (is_plain.value) {
+        const float over = soft(is_plain, s0, p0, i, 0);
+        values(p1, i - 1, 1);
+        stage_k(i + 1);
+        load_k(i + 2);
+        keep_here(p0, l);
+        clean_v(i + 1);
+        find_k(i + 3);
+        __syncthreads();
+        const bool again = __any(!(over <= kMost));
+        if (again) l = before;
+        return again;
+      } else {
+        values(p1, i - 1, 1);
+        settle(s0, i, 0);
+        soft(is_plain, s0, p0, i, 0);
+        stage_k(i + 1);
+        load_k(i + 2);
+        clean_v(i + 1);
+        find_k(i + 3);
+        __syncthreads();
+        return false;
+      }
     };
     // second half: s1 -> p1, scores of the next tile's first, values of this
     // tile's first; values of the next tile into LDS
     auto half1 = [&](auto is_plain, int i) {
+      const float before = l;
       scores(s0, i + 1, 0);
-      soft(is_plain, s1, p1, i, 1);
-      values(p0, i, 0);
-      stage_v(i + 1);
-      load_v(i + 2);
-      keep_here(p1, l);
-      find_v(i + 3);
+      if constexpr (is_plain.value) {
+        const float over = soft(is_plain, s1, p1, i, 1);
+        values(p0, i, 0);
+        stage_v(i + 1);
+        load_v(i + 2);
+        keep_here(p1, l);
+        find_v(i + 3);
+        const bool again = __any(!(over <= kMost));
+        if (again) l = before;
+        return again;
+      } else {
+        values(p0, i, 0);
+        settle(s1, i, 1);
+        soft(is_plain, s1, p1, i, 1);
+        stage_v(i + 1);
+        load_v(i + 2);
+        find_v(i + 3);
+        return false;
+      }
     };
     // The tiles that need nothing but the pipeline run in a loop of their own,
     // whose sums stay in place; it is left where a reference point has to move
     // or a tile needs masks.
     int i = 0;
     take_scales(0);
-    settle_scales(0, p0);
+    settle_scales(0, p1);
     scores(s0, 0, 0);
-    settle(largest(no, s0, 0, 0), p0);
     while (true) {
-      float top;
       if (plain) {
-        bool within = false;
+        enum { kFirst, kSecond, kTile } left = kTile;
         while (true) {
-          top = half0(yes, i);
-          if (passes(top)) {
-            within = true;
+          if (half0(yes, i)) {
+            left = kFirst;
             break;
           }
-          half1(yes, i);
+          if (half1(yes, i)) {
+            left = kSecond;
+            break;
+          }
           if (++i >= tiles) break;
           take_scales(i);
-          if (!plain || most > vref || passes(largest(yes, s0, i, 0))) break;
+          if (!plain || most > vref) break;
         }
         if (i >= tiles) break;
-        if (!within) {
+        if (left == kTile) {
           settle_scales(i, p1);
-          settle(largest(no, s0, i, 0), p1);
           continue;
         }
+        if (left == kFirst) {
+          settle(s0, i, 0);
+          soft(no, s0, p0, i, 0);
+          half1(no, i);
+        } else {
+          settle(s1, i, 1);
+          soft(no, s1, p1, i, 1);
+        }
       } else {
-        top = half0(no, i);
+        half0(no, i);
+        half1(no, i);
       }
-      settle(top, p0);
-      half1(no, i);
       if (++i >= tiles) break;
       take_scales(i);
       settle_scales(i, p1);
-      settle(largest(no, s0, i, 0), p1);
     }
     values(p1, tiles - 1, 1);
   }

@@ -6,8 +6,9 @@ namespace {
 
 // Joins the splits of a (row, query head), in order, with WAYS waves each: a
 // lane every 64th split for the weights, then D / 64 columns of the output of
-// every WAYS-th split. A split that saw nothing has l = 0. (Few splits: one
-// wave, many rows a workgroup; many: their reads in parallel.)
+// every WAYS-th split. A split that saw nothing has l = 0 and sums of 0 (but for a
+// row that sees nothing at all, whose output is 0 whatever they are). Few
+// splits: one wave, many rows a workgroup; many: their reads in parallel.
 template <int T, int D, int WAYS>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
   constexpr int EACH = D / 64, MANY = kMaxSplits / 64;
@@ -57,9 +58,9 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendParams p) {
         const int s = s0 + WAYS * a;
         const float ws = s < end ? __int_as_float(__builtin_amdgcn_readlane(
                                        __float_as_int(w[k]), s & 63)) : 0.f;
-        // (not times 0: a part that saw nothing may hold anything)
+        // (also where a part's weight is 0: what it holds may be NaN)
 #pragma unroll
-        for (int e = 0; e < EACH; ++e) v[e] = ws == 0.f ? v[e] : __builtin_fmaf(x[a][e], ws, v[e]);
+        for (int e = 0; e < EACH; ++e) v[e] = __builtin_fmaf(x[a][e], ws, v[e]);
       }
     }
   }

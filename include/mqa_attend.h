@@ -128,8 +128,8 @@ size_t workspace_size_attend(int requests, int R, int heads, int kv_heads, int h
  * Scores, softmax sums and the output's sums are held in fp32. Positions that
  * no row sees may hold anything (also NaN codes and NaN or infinite scales); a
  * table entry outside [0, num_pages) is clamped into it. Scales of seen
- * positions must be >= 0. A row that sees a NaN code becomes NaN, and no
- * other row does.
+ * positions must be >= 0. A row that sees a NaN code becomes NaN (of a value's,
+ * at least in its column), and no other row does.
  */
 int mqa_attend_paged(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
                      int64_t q_head_stride, int dtype, const int32_t* starts, const int32_t* ends,

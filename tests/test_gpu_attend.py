@@ -198,6 +198,25 @@ def test_nan_reaches_only_the_rows_that_see_it(R, Hq, where):
     assert ref.differs(out[~sees], want[~sees], tol[~sees]) == 0
 
 
+@pytest.mark.parametrize("R", [1, 12, 70])
+def test_nan_of_a_position_without_weight(R):
+    # the first half of the keys, scored 5000 below the others, holds a NaN value
+    say(f"case: NaN without weight, {R} rows")
+    pool, table, q, starts, ends = problem([20000], R, 8, 1, 128, 64, 64, BF16, "e4m3", "full")
+    first = table[0, :156].long()
+    pool.codes[first, 0] = 0xFE
+    pool.scales[first, 0] = 1.0
+    pool.codes[first[7], 1, 0, 9, 5] = 0x7F
+    q = torch.ones_like(q)
+    starts[1::2] = 12000  # does not see it
+    for idx in (None, torch.arange(20000).int().repeat(R, 1)):
+        args = [layout(pool), q.cuda(), pool.bytes().cuda(), table.cuda()]
+        args += [] if idx is None else [idx.cuda()]
+        call = mqa.mqa_attend_paged if idx is None else mqa.mqa_attend_topk
+        out = call(*args, starts.cuda(), ends.cuda()).float().cpu()
+        assert bool(torch.isnan(out[0::2, :, 5]).all()) and bool(torch.isfinite(out[1::2]).all())
+
+
 @pytest.mark.parametrize("R", [1, 40, 100])
 def test_scales_of_very_different_size(R):
     # value scales that fall and rise by 2^40 along the context, zero blocks

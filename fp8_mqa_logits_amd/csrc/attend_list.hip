@@ -13,9 +13,14 @@ constexpr uint32_t kNone = ~0u;  // token of an entry that names no position
 // and then into LDS, and every one of them reads all of it for its own 16 NT
 // heads, with the products of attend_narrow.hip. For 64 heads two waves take 32
 // each: with one wave for all, its sums leave room for one wave per SIMD only
-// and a gather's latency shows (4096 rows of 64 heads and 2048 positions: 1.14
-// ms); with four of 16, every code is widened and read from LDS four times (666
-// us).
+// and a gather's latency shows; with four of 16, every code is widened and read
+// from LDS four times (4096 rows of 64 heads and 2048 positions, when they were
+// compared: 1.14 ms, 666 us, and 594 us for this).
+//
+// Bound by the gathered bytes where heads are few: 64 x 2 rows of 2048 positions,
+// 8 heads a key head, take 100 us, 5.4 TB/s. With 64 heads a key head by vector
+// instructions (the widening, done by both waves, and the exponentials): 4096
+// rows of 2048 positions of one key head 463 us, 594 TFLOP/s.
 //
 // A step's tokens (slots in the pool) are found by lanes 0 .. 31, an entry
 // each, two steps ahead, and go to the other lanes by permutation; scales go

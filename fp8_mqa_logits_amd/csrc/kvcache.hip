@@ -149,7 +149,8 @@ __device__ __forceinline__ void widen(const Raw<T>& r, float* x) {
 // HELD: its tokens stay in registers between the search for the largest and
 // the rounding (blocks of up to kHold pieces of 8 elements a thread: 128 tokens
 // of 128); larger blocks are read twice. Kept tokens are read only where the
-// scale grows.
+// scale grows. Bound by the bytes of long inputs: 16384 tokens of 8 heads of 128
+// in bf16 take 21.6 us, 4.7 TB/s in and out.
 constexpr int kHold = 8;
 
 template <int T, int C, int D, bool HELD>
@@ -243,7 +244,9 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(KvMoveParams p, int
 // A thread reads kRows times 8 codes and writes as many values: consecutive
 // threads go along a token, then to the next ones of the same head (contiguous
 // in its page); its rows are kThreads / PER apart, each with its own chain of
-// lookups under way.
+// lookups under way (16384 tokens of 8 heads of 128 to bf16: 20.8 us, 4.8 TB/s;
+// append and read together 54.6 us with one row a thread here and two looks at
+// the tokens there, 47.6 us now).
 constexpr int kRows = 4;
 
 template <int T, int C, int D>

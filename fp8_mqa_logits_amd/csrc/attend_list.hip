@@ -4,8 +4,6 @@
 namespace mqa {
 namespace {
 
-constexpr uint32_t kNone = ~0u;  // token of an entry that names no position
-
 // A workgroup takes one row and 16 NT HW of the query heads of one key head,
 // and one of p.splits parts of the row's list, 32 entries and KW = 4 / HW waves
 // at a time. HW waves share 32 entries: each loads its part of their rows (16
@@ -30,10 +28,9 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
   constexpr int KW = 4 / HW;
   constexpr int KC = D / 64;       // 16-byte pieces of a key per lane and product
   constexpr int U = D / 16;        // products per step
-  constexpr int VW = D / 64;       // dwords of a value per lane
   constexpr int PIECES = D / 16;   // 16-byte pieces of a row
   constexpr int GROUP = 64 * HW;   // threads that share 32 entries
-  constexpr int EACH = 64 * PIECES / GROUP;  // pieces of 32 keys and 32 values per thread
+  constexpr int EACH = 32 * PIECES / GROUP;  // pieces of 32 keys, and of 32 values, per thread
   constexpr int COLS = 16 * NT * HW, BUFS = HW == 1 ? 1 : 2;
   const KvCache& c = p.c;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -105,7 +102,7 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
   }
 
   // entry lane % 32 of the wave's step in a round: its list entry as it is,
-  // what it names (-1: nothing), the table entry of that position, the token
+  // what it names (-1: nothing), the table entry of that position
   const int32_t* const list = p.indices + (int64_t)row * p.width;
   const int32_t* const table = c.table + (int64_t)(row / p.R) * c.table_stride;
   const int page_mask = (1 << c.page_shift) - 1;
@@ -115,50 +112,53 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
     return at_of(round) < min(step_hi * 32, used) && x >= 0 && x < e - s ? x : -1;
   };
   auto looked_up = [&](int x) { return table[(x < 0 ? 0 : s + x) >> c.page_shift]; };
-  auto token_of = [&](int x, int entry) -> uint32_t {
-    const uint32_t page = (uint32_t)clamp_page(c, entry);
-    return x < 0 ? kNone : (page << c.page_shift) + (uint32_t)((s + x) & page_mask);
-  };
-  // what a lane loads: piece x = gt + GROUP r of the 32 keys, then values
-  auto token_row = [&](uint32_t tok) {
-    tok = tok == kNone ? 0u : tok;
-    return c.pages + (int64_t)(tok >> c.page_shift) * c.page_stride + (tok & page_mask) * (uint32_t)D;
-  };
-  const int k_at = code_at(c, 0, h, 0), v_at = code_at(c, 1, h, 0);
+  // what a lane loads: piece x = gt + GROUP r of the 32 keys, and of the values
+  const int lane_at = 16 * (gt % PIECES);
+  const int k_at = code_at(c, 0, h, 0) + lane_at, v_at = code_at(c, 1, h, 0) + lane_at;
   struct Codes {
-    v4u reg[EACH];
+    v4u k[EACH], v[EACH];
     float ks, vs;
-    uint32_t tok;
+    bool named;
   };
-  auto load = [&](Codes& f, uint32_t tok) {
-    f.tok = tok;
+  auto load = [&](Codes& f, int x, int entry) {
+    f.named = x >= 0;
+    const uint8_t* const page = c.pages + (int64_t)clamp_page(c, entry) * c.page_stride;
+    const int slot = x < 0 ? 0 : (s + x) & page_mask;
+    const uint64_t token = (uint64_t)(page + slot * D);
 #pragma unroll
     for (int r = 0; r < EACH; ++r) {
-      const int x = gt + GROUP * r, key = x / PIECES % 32;
-      const uint8_t* at = token_row((uint32_t)__shfl((int)tok, key, 64));
-      f.reg[r] = *reinterpret_cast<const v4u*>(at + (x < 32 * PIECES ? k_at : v_at) +
-                                             16 * (x % PIECES));
+      const int key = (gt + GROUP * r) / PIECES;
+      const uint64_t lo = (uint32_t)__shfl((int)token, key, 64);
+      const uint64_t hi = (uint32_t)__shfl((int)(token >> 32), key, 64);
+      const uint8_t* const at = (const uint8_t*)(hi << 32 | lo);
+      f.k[r] = *reinterpret_cast<const v4u*>(at + k_at);
+      f.v[r] = *reinterpret_cast<const v4u*>(at + v_at);
     }
-    const uint32_t mine = tok == kNone ? 0u : tok;
-    const uint8_t* page = c.pages + (int64_t)(mine >> c.page_shift) * c.page_stride;
-    f.ks = *reinterpret_cast<const float*>(page + scale_at(c, 0, h, mine & page_mask));
-    f.vs = *reinterpret_cast<const float*>(page + scale_at(c, 1, h, mine & page_mask));
+    f.ks = *reinterpret_cast<const float*>(page + scale_at(c, 0, h, slot));
+    f.vs = *reinterpret_cast<const float*>(page + scale_at(c, 1, h, slot));
   };
-  // byte of piece x of a row in LDS (of 32 rows, 16-byte pieces exchanged so
-  // that the lanes of every read here touch all banks: 16 rows and one piece,
-  // or whole rows four apart)
-  auto place = [&](int key, int x) {
+  // byte of piece x of a row in LDS (of 32 rows), 16-byte pieces exchanged so
+  // that the lanes of every read touch all banks: 16 rows and one piece of the
+  // keys, rows 4 g .. 4 g + 3 of both halves and one piece of the values
+  auto k_place = [&](int key, int x) {
     if constexpr (D == 128)
       return (key ^ (key >> 2 & 1)) * D + 16 * (x ^ (key >> 1 & 7));
     else
       return key * D + 16 * (x ^ (key >> 2 & 3));
   };
+  auto v_place = [&](int key, int x) {
+    if constexpr (D == 128)
+      return key * D + 16 * (x ^ ((key >> 1 & 3) | (key >> 2 & 4)));
+    else
+      return key * D + 16 * (x ^ ((key >> 2 & 1) | (key >> 3 & 2)));
+  };
   auto stage = [&](const Codes& f, int buf) {
+    uint8_t* const to = sh.step.rows[kb][buf];
 #pragma unroll
     for (int r = 0; r < EACH; ++r) {
-      const int x = gt + GROUP * r, key = x / PIECES;  // values: rows 32 ..
-      *reinterpret_cast<v4u*>(
-          &sh.step.rows[kb][buf][(key & 32) * D + place(key & 31, x % PIECES)]) = f.reg[r];
+      const int key = (gt + GROUP * r) / PIECES, x = gt % PIECES;
+      *reinterpret_cast<v4u*>(to + k_place(key, x)) = f.k[r];
+      *reinterpret_cast<v4u*>(to + 32 * D + v_place(key, x)) = f.v[r];
     }
   };
   auto compute = [&](uint32_t valid, int buf) {
@@ -171,7 +171,7 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
       for (int t = 0; t < NT; ++t) x[t][b] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < KC; ++k) {
-        const v4u w = *reinterpret_cast<const v4u*>(rows + place(16 * b + n, g + 4 * k));
+        const v4u w = *reinterpret_cast<const v4u*>(rows + k_place(16 * b + n, g + 4 * k));
         const v4u lo = widen8<T, C>(w[0], w[1]), hi = widen8<T, C>(w[2], w[3]);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -228,41 +228,28 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
       for (int i = 0; i < 4; ++i)
         pf[t][i] = __builtin_bit_cast(uint32_t, v2h{(_Float16)e[2 * i], (_Float16)e[2 * i + 1]});
     }
-    uint32_t v[8][VW];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int key = 16 * (j >> 2) + 4 * g + (j & 3);
-      const uint8_t* at = rows + 32 * D + place(key, VW == 2 ? n >> 1 : n >> 2) +
-                          (VW == 2 ? 8 * (n & 1) : 4 * (n & 3));
-      if constexpr (VW == 2) {
-        const uint2 w = *reinterpret_cast<const uint2*>(at);
-        v[j][0] = w.x;
-        v[j][1] = w.y;
-      } else {
-        v[j][0] = *reinterpret_cast<const uint32_t*>(at);
-      }
-    }
+    // A transposing read gives lane n of 16 the bytes n of the eight rows that
+    // lanes 2 j and 2 j + 1 point at: the codes of one column and the eight
+    // keys whose P the lane holds.
+    uint32_t some[2] = {~0u, ~0u};
     if (!clean) {  // (what an entry that names no position was read from)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int b = 0; b < 2; ++b) {
+        some[b] = 0;
 #pragma unroll
-        for (int w = 0; w < VW; ++w) v[j][w] &= bit(sees, 16 * (j >> 2) + (j & 3));
-    }
-#pragma unroll
-    for (int w = 0; w < VW; ++w) {
-      uint32_t in[4], a[4], b[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) in[j] = v[j][w];
-      transpose4(in, a);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) in[j] = v[4 + j][w];
-      transpose4(in, b);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const v4u vf = widen8<kFp16, C>(a[i], b[i]);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[t][4 * w + i] = mfma<kFp16>(vf, pf[t], acc[t][4 * w + i]);
+        for (int i = 0; i < 4; ++i) some[b] |= bit(sees, 16 * b + i) & 0xFFu << (8 * i);
       }
+    }
+    const int key = 4 * g + (n >> 1 & 3) + 16 * (n >> 3);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      typedef int v2i __attribute__((ext_vector_type(2)));
+      v2i w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+          (__attribute__((address_space(3))) v2i*)(rows + 32 * D + v_place(key, u) + 8 * (n & 1)));
+      if (!clean) w = v2i{(int)(w.x & some[0]), (int)(w.y & some[1])};
+      const v4u vf = widen8<kFp16, C>(w.x, w.y);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[t][u] = mfma<kFp16>(vf, pf[t], acc[t][u]);
     }
   };
 
@@ -276,8 +263,8 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
     // a round's scales and which of its entries name positions
     uint32_t valid;
     auto take_scales = [&](const Codes& f) {
-      valid = (uint32_t)__ballot(f.tok != kNone);
-      const float k = f.tok != kNone ? f.ks * cs : 0.f, v = f.tok != kNone ? f.vs : 0.f;
+      valid = (uint32_t)__ballot(f.named);
+      const float k = f.named ? f.ks * cs : 0.f, v = f.named ? f.vs : 0.f;
       const float finite = v < __builtin_inff() ? v : 0.f;
       if (__any(finite > vref)) {
         const float to = power_above(wave_max(finite)), keep = vref / to;
@@ -299,26 +286,26 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
     // nothing to that).
     Codes codes;
     int x = named(listed(0), 0), entry = looked_up(x), x_raw = listed(1);
-    auto ahead = [&](int round) {  // token of `round`; entry of the next, list of the one after
-      const uint32_t tok = token_of(x, entry);
+    auto load_next = [&](int round) {  // codes of `round`; entry of the next, list of the one after
+      const int x0 = x, entry0 = entry;
       x = named(x_raw, round + 1);
       entry = looked_up(x);
       x_raw = listed(round + 2);
-      return tok;
+      load(codes, x0, entry0);
     };
-    load(codes, ahead(0));
+    load_next(0);
     for (int i = 0; i < rounds; ++i) {
       const int buf = BUFS == 1 ? 0 : i & 1;
       stage(codes, buf);
       take_scales(codes);
       sync();
-      load(codes, ahead(i + 1));
+      load_next(i + 1);
       compute(valid, buf);
       if constexpr (BUFS == 1) __builtin_amdgcn_wave_barrier();
     }
   }
   __syncthreads();  // (the steps' memory becomes the sums')
-  finish<T>(p, sh.finish, block, row, p.group, tile, h, wave, m, l, vref, acc);
+  finish<T, true>(p, sh.finish, block, row, p.group, tile, h, wave, m, l, vref, acc);
 }
 
 template <int T, int C, int D>

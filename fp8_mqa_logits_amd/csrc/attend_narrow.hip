@@ -280,7 +280,7 @@ void attend_narrow_kernel(AttendParams p) {
 #pragma unroll
   for (int t = 0; t < NT; ++t)
     if (col_s[t] >= col_e[t]) l[t] = 0.f;  // sums of a row that sees nothing
-  finish<T>(p, s_finish, block, unit * p.R, columns, tile, h, wave, m, l, vref, acc);
+  finish<T, false>(p, s_finish, block, unit * p.R, columns, tile, h, wave, m, l, vref, acc);
 }
 
 template <int T, int C, int D>

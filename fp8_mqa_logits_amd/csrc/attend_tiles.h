@@ -199,8 +199,8 @@ __device__ __forceinline__ Span uniform(Span a) {
 
 // The end of a workgroup whose waves hold O^T sums in v_mfma_f32_16x16x32's
 // layout: wave kb * HW + hw has 16 NT columns from 16 NT hw, over part kb of the
-// keys; lane (g, n) holds columns d = D / 16 * (4 g + i) + u of column n's
-// output in acc[t][u][i]. The KW waves of a column are brought to one reference
+// keys; lane (g, n) holds element d of column n's output in acc[t][u][i], d =
+// 16 u + 4 g + i (INLINE) or D / 16 * (4 g + i) + u. The KW waves of a column are brought to one reference
 // point and added, US products a round, through LDS; then the rows are written,
 // or the parts when the keys are split over workgroups.
 template <int D, int NT, int HW, int KW>
@@ -211,7 +211,7 @@ struct Finish {
   float m[KW][COLS], l[KW][COLS];
 };
 
-template <int T, int D, int NT, int HW, int KW>
+template <int T, bool INLINE, int D, int NT, int HW, int KW>
 __device__ __forceinline__ void finish(const AttendParams& p, Finish<D, NT, HW, KW>& sh,
                                        int64_t block, int first_row, int columns, int tile, int h,
                                        int wave, const float (&m)[NT], const float (&l_in)[NT],
@@ -279,9 +279,9 @@ __device__ __forceinline__ void finish(const AttendParams& p, Finish<D, NT, HW, 
       for (int u = 0; u < US; ++u) {
         v[u] = 0.f;
 #pragma unroll
-        for (int w = 0; w < KW; ++w) v[u] += sh.part[w][u * 16 + r][col];
+        for (int w = 0; w < KW; ++w) v[u] += sh.part[w][INLINE ? US * r + u : u * 16 + r][col];
       }
-      const int d = U * r + u0;
+      const int d = INLINE ? 16 * u0 + US * r : U * r + u0;
       if (!real) continue;
       if (!direct) {
         float* const o = p.part_o + slot * D + d;

@@ -15,10 +15,12 @@ namespace {
 // from LDS four times (4096 rows of 64 heads and 2048 positions, when they were
 // compared: 1.14 ms, 666 us, and 594 us for this).
 //
-// Bound by the gathered bytes where heads are few: 64 x 2 rows of 2048 positions,
-// 8 heads a key head, take 100 us, 5.4 TB/s. With 64 heads a key head by vector
-// instructions (the widening, done by both waves, and the exponentials): 4096
-// rows of 2048 positions of one key head 463 us, 594 TFLOP/s.
+// Bound by the gathered bytes: 64 x 2 rows of 2048 positions, 8 key heads of 4
+// query heads, take 93 us, 5.8 TB/s. So nearly with 64 query heads on one key
+// head, where each row gathers what others gather too, but from a cache larger
+// than an L2, and the vector unit (widening, exponentials) is busy most of the
+// time: 4096 rows of 2048 of 65536 positions 409 us, 5.2 TB/s of gathered codes,
+// 672 TFLOP/s.
 //
 // A step's tokens (slots in the pool) are found by lanes 0 .. 31, an entry
 // each, two steps ahead, and go to the other lanes by permutation; scales go
@@ -152,8 +154,14 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
     else
       return key * D + 16 * (x ^ ((key >> 2 & 1) | (key >> 3 & 2)));
   };
-  auto stage = [&](const Codes& f, int buf) {
+  // (an entry that names no position was read from somewhere: its values become 0)
+  auto stage = [&](Codes& f, uint32_t valid, int buf) {
     uint8_t* const to = sh.step.rows[kb][buf];
+    if (valid != ~0u) {
+#pragma unroll
+      for (int r = 0; r < EACH; ++r)
+        if (!(valid >> (gt + GROUP * r) / PIECES & 1)) f.v[r] = v4u{0, 0, 0, 0};
+    }
 #pragma unroll
     for (int r = 0; r < EACH; ++r) {
       const int key = (gt + GROUP * r) / PIECES, x = gt % PIECES;
@@ -231,22 +239,12 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
     // A transposing read gives lane n of 16 the bytes n of the eight rows that
     // lanes 2 j and 2 j + 1 point at: the codes of one column and the eight
     // keys whose P the lane holds.
-    uint32_t some[2] = {~0u, ~0u};
-    if (!clean) {  // (what an entry that names no position was read from)
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        some[b] = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) some[b] |= bit(sees, 16 * b + i) & 0xFFu << (8 * i);
-      }
-    }
     const int key = 4 * g + (n >> 1 & 3) + 16 * (n >> 3);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       typedef int v2i __attribute__((ext_vector_type(2)));
-      v2i w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+      const v2i w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
           (__attribute__((address_space(3))) v2i*)(rows + 32 * D + v_place(key, u) + 8 * (n & 1)));
-      if (!clean) w = v2i{(int)(w.x & some[0]), (int)(w.y & some[1])};
       const v4u vf = widen8<kFp16, C>(w.x, w.y);
 #pragma unroll
       for (int t = 0; t < NT; ++t) acc[t][u] = mfma<kFp16>(vf, pf[t], acc[t][u]);
@@ -261,9 +259,7 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
         __builtin_amdgcn_wave_barrier();
     };
     // a round's scales and which of its entries name positions
-    uint32_t valid;
     auto take_scales = [&](const Codes& f) {
-      valid = (uint32_t)__ballot(f.named);
       const float k = f.named ? f.ks * cs : 0.f, v = f.named ? f.vs : 0.f;
       const float finite = v < __builtin_inff() ? v : 0.f;
       if (__any(finite > vref)) {
@@ -294,15 +290,22 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
       load(codes, x0, entry0);
     };
     load_next(0);
-    for (int i = 0; i < rounds; ++i) {
-      const int buf = BUFS == 1 ? 0 : i & 1;
-      stage(codes, buf);
+    auto round = [&](int i, int buf) {
+      const uint32_t valid = (uint32_t)__ballot(codes.named);
+      stage(codes, valid, buf);
       take_scales(codes);
       sync();
       load_next(i + 1);
       compute(valid, buf);
       if constexpr (BUFS == 1) __builtin_amdgcn_wave_barrier();
-    }
+    };
+    int i = 0;
+    if constexpr (BUFS == 2)  // (two at a time: what LDS addresses add is known)
+      for (; i + 1 < rounds; i += 2) {
+        round(i, 0);
+        round(i + 1, 1);
+      }
+    for (; i < rounds; ++i) round(i, 0);
   }
   __syncthreads();  // (the steps' memory becomes the sums')
   finish<T, true>(p, sh.finish, block, row, p.group, tile, h, wave, m, l, vref, acc);

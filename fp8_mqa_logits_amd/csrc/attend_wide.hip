@@ -35,8 +35,11 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   constexpr int THREADS = 64 * W;
   constexpr int KS = D / 16;          // products a half's scores take
   constexpr int DT = D / 32;          // tiles of the output's columns
-  constexpr int PIECES = 4 * D;       // 16-byte pieces of a tile's keys; 4 x 4 pieces of its values
-  constexpr int EACH = (PIECES + THREADS - 1) / THREADS;  // of each, per thread
+  // pieces of a tile, EACH of either kind per thread: KB bytes of a key, and VK
+  // values' codes of four columns (all threads take the same part, so that the
+  // loop has no branch)
+  constexpr int KB = 4 * D < THREADS ? 8 : 16, VK = KB / 4;
+  constexpr int EACH = 64 * D / KB / THREADS;
   constexpr int COLS = 32 * W;
   const KvCache& c = p.c;
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -102,13 +105,12 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   const int tiles = min(all - tile_lo, per_split);
   const int base = first + tile_lo * 64;
 
-  // staging: piece x = t + THREADS r of the keys is 16 bytes of key x / (D /
-  // 16); of the values, columns 4 (x % (D / 4)) .. + 3 of keys 4 y .. 4 y + 3,
-  // y = x / (D / 4)
+  // staging: piece x = t + THREADS r of the keys is KB bytes of key x / (D /
+  // KB); of the values, columns 4 (x % (D / 4)) .. + 3 of VK keys from
+  // VK (x / (D / 4))
   auto piece = [&](int r) { return t + THREADS * r; };
-  auto mine = [&](int r) { return PIECES % THREADS == 0 || piece(r) < PIECES; };
-  auto k_key = [&](int r) { return piece(r) / (D / 16); };
-  auto v_key = [&](int r) { return piece(r) / (D / 4) * 4; };
+  auto k_key = [&](int r) { return piece(r) / (D / KB); };
+  auto v_key = [&](int r) { return piece(r) / (D / 4) * VK; };
   auto v_d = [&](int r) { return piece(r) % (D / 4) * 4; };
   // A group of 16 keys that no row sees is read from the nearest one that some
   // row sees (masked later; no branch in the loop). Its table entry is loaded a
@@ -124,37 +126,37 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   auto slot_of = [&](int i, int key) {
     return (group_pos(i, key >> 4) + (key & 15)) & ((1 << c.page_shift) - 1);
   };
-  v4u kreg[EACH];
-  uint32_t vreg[EACH][4];
+  uint32_t kreg[EACH][KB / 4], vreg[EACH][VK];
   float sreg = 0.f;
   int kentry[EACH], ventry[EACH], sentry;
-  // (of a workgroup with more threads than pieces, the others read piece 0 too)
-  auto k_of = [&](int r) { return mine(r) ? k_key(r) : 0; };
-  auto v_of = [&](int r) { return mine(r) ? v_key(r) : 0; };
   auto find_k = [&](int i) {
 #pragma unroll
-    for (int r = 0; r < EACH; ++r) kentry[r] = group_entry(i, k_of(r) >> 4);
+    for (int r = 0; r < EACH; ++r) kentry[r] = group_entry(i, k_key(r) >> 4);
     sentry = group_entry(i, t & 3);
   };
   auto find_v = [&](int i) {
 #pragma unroll
-    for (int r = 0; r < EACH; ++r) ventry[r] = group_entry(i, v_of(r) >> 4);
+    for (int r = 0; r < EACH; ++r) ventry[r] = group_entry(i, v_key(r) >> 4);
   };
   auto load_k = [&](int i) {
 #pragma unroll
-    for (int r = 0; r < EACH; ++r)
-      kreg[r] = *reinterpret_cast<const v4u*>(page_at(kentry[r]) +
-                                              code_at(c, 0, h, slot_of(i, k_of(r))) +
-                                              16 * (piece(r) % (D / 16)));
+    for (int r = 0; r < EACH; ++r) {
+      typedef uint32_t Piece __attribute__((ext_vector_type(KB / 4)));
+      const Piece x = *reinterpret_cast<const Piece*>(page_at(kentry[r]) +
+                                                      code_at(c, 0, h, slot_of(i, k_key(r))) +
+                                                      KB * (piece(r) % (D / KB)));
+#pragma unroll
+      for (int j = 0; j < KB / 4; ++j) kreg[r][j] = x[j];
+    }
     sreg = *reinterpret_cast<const float*>(page_at(sentry) +
                                            scale_at(c, t >> 2 & 1, h, slot_of(i, 16 * (t & 3))));
   };
   auto load_v = [&](int i) {
 #pragma unroll
     for (int r = 0; r < EACH; ++r) {
-      const uint8_t* at = page_at(ventry[r]) + code_at(c, 1, h, slot_of(i, v_of(r))) + v_d(r);
+      const uint8_t* at = page_at(ventry[r]) + code_at(c, 1, h, slot_of(i, v_key(r))) + v_d(r);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) vreg[r][j] = *reinterpret_cast<const uint32_t*>(at + j * D);
+      for (int j = 0; j < VK; ++j) vreg[r][j] = *reinterpret_cast<const uint32_t*>(at + j * D);
     }
   };
   auto k_slot = [&](int key, int slot) { return key * KROW + 16 * slot; };
@@ -166,12 +168,13 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     uint8_t* const to = s_k[i & 1];
 #pragma unroll
     for (int r = 0; r < EACH; ++r) {
-      if (!mine(r)) continue;
-      const int x = piece(r) % (D / 16);
-      // (the halves of a piece half a row apart: eight lanes write 128 bytes)
-      *reinterpret_cast<v4u*>(to + k_slot(k_key(r), x)) = widen8<T, C>(kreg[r][0], kreg[r][1]);
-      *reinterpret_cast<v4u*>(to + k_slot(k_key(r), D / 16 + x)) =
-          widen8<T, C>(kreg[r][2], kreg[r][3]);
+      // (the halves of 16 bytes half a row apart: eight lanes write 128 bytes)
+#pragma unroll
+      for (int j = 0; j < KB / 8; ++j) {
+        const int x = piece(r) % (D / KB) * (KB / 8) + j;  // 8 codes
+        *reinterpret_cast<v4u*>(to + k_slot(k_key(r), (x & 1) * (D / 16) + (x >> 1))) =
+            widen8<T, C>(kreg[r][2 * j], kreg[r][2 * j + 1]);
+      }
     }
     s_scale[i & 1][t] = sreg;
   };
@@ -183,9 +186,8 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     if (inside(i)) return;
 #pragma unroll
     for (int r = 0; r < EACH; ++r) {
-      if (!mine(r)) continue;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < VK; ++j) {
         const int key = v_key(r) + j, pos = base + i * 64 + key;
         if (i >= tiles || pos < lo || pos >= hi) vreg[r][j] = 0;
         if constexpr (C == kE4m3) {
@@ -205,14 +207,25 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   auto stage_v = [&](int i) {
 #pragma unroll
     for (int r = 0; r < EACH; ++r) {
-      if (!mine(r)) continue;
-      uint32_t a[4];
-      transpose4(vreg[r], a);
       const int y = v_key(r) >> 2, slot = 2 * (y >> 2) + (y & 1), half = y >> 1 & 1;
+      auto to = [&](int j) {
+        return s_v[i & 1] + v_slot(D / 4 * j + v_d(r) / 4, slot) + 8 * half + 2 * (v_key(r) & 3);
+      };
+      if constexpr (VK == 4) {
+        uint32_t a[4];
+        transpose4(vreg[r], a);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint2*>(s_v[i & 1] + v_slot(D / 4 * j + v_d(r) / 4, slot) + 8 * half) =
-            widen4<kFp16, C>(a[j]);
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint2*>(to(j)) = widen4<kFp16, C>(a[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {  // columns j and j + 1 of both keys
+          const uint2 w = widen4<kFp16, C>(
+              __builtin_amdgcn_perm(vreg[r][1], vreg[r][0], j ? 0x07030602u : 0x05010400u));
+          *reinterpret_cast<uint32_t*>(to(j)) = w.x;
+          *reinterpret_cast<uint32_t*>(to(j + 1)) = w.y;
+        }
+      }
     }
   };
 

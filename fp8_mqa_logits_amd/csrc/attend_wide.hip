@@ -56,7 +56,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   constexpr int KROW = 2 * D + 16, VROW = 2 * 64 + 16;  // bytes of a staged key, of a column
   __shared__ __align__(16) uint8_t s_k[2][64 * KROW];
   __shared__ __align__(16) uint8_t s_v[2][D * VROW];
-  __shared__ __align__(16) float s_scale[2][THREADS];  // 8 scales, over and over
+  __shared__ __align__(16) float s_scale[2][256];  // 8 scales, over and over
   __shared__ uint32_t s_poison[3][2];
   __shared__ Span s_span[W];
 
@@ -112,51 +112,52 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   auto k_key = [&](int r) { return piece(r) / (D / KB); };
   auto v_key = [&](int r) { return piece(r) / (D / 4) * VK; };
   auto v_d = [&](int r) { return piece(r) % (D / 4) * 4; };
-  // A group of 16 keys that no row sees is read from the nearest one that some
-  // row sees (masked later; no branch in the loop). Its table entry is loaded a
-  // tile before its use, and only looked at then.
-  const int32_t* const table = c.table + (int64_t)unit * c.table_stride;
-  auto group_pos = [&](int i, int g) {
-    return min(max(base + i * 64 + 16 * g, lo), hi - 1) & ~15;
+  // What a wave takes lies in one group of 16 keys, so that its page, its
+  // addresses (but for an offset that each lane keeps) and its scales are the
+  // wave's. A group that no row sees is read from the nearest one that some row
+  // sees (masked later; no branch in the loop). Its table entry is loaded a tile
+  // before its use, and only looked at then, by a vector load: a scalar one would
+  // have every LDS read in flight waited for.
+  static_assert(64 / (D / KB) == 64 / (D / 4) * VK && 64 / (D / KB) <= 16);
+  auto group = [&](int r) { return (wave * 64 + THREADS * r) / (D / KB) >> 4; };
+  const int* const table = c.table + (int64_t)unit * c.table_stride;
+  int zero = 0;
+  asm("" : "+v"(zero));
+  auto group_pos = [&](int i, int r) {
+    return min(max(base + i * 64 + 16 * group(r), lo), hi - 1) & ~15;
   };
-  auto group_entry = [&](int i, int g) { return table[group_pos(i, g) >> c.page_shift]; };
-  auto page_at = [&](int entry) {
-    return c.pages + (int64_t)min(max(entry, 0), c.num_pages - 1) * c.page_stride;
-  };
-  auto slot_of = [&](int i, int key) {
-    return (group_pos(i, key >> 4) + (key & 15)) & ((1 << c.page_shift) - 1);
-  };
+  const uint32_t k_lane = (k_key(0) & 15) * D + KB * (t % (D / KB));
+  const uint32_t v_lane = (v_key(0) & 15) * D + v_d(0);
+  const uint32_t s_lane = (lane & 1) * (scale_at(c, 1, h, 0) - scale_at(c, 0, h, 0));
   uint32_t kreg[EACH][KB / 4], vreg[EACH][VK];
-  float sreg = 0.f;
-  int kentry[EACH], ventry[EACH], sentry;
-  auto find_k = [&](int i) {
+  float sreg[EACH];
+  int entry[EACH];
+  const uint8_t* page[EACH];
+  auto find = [&](int i) {
 #pragma unroll
-    for (int r = 0; r < EACH; ++r) kentry[r] = group_entry(i, k_key(r) >> 4);
-    sentry = group_entry(i, t & 3);
-  };
-  auto find_v = [&](int i) {
-#pragma unroll
-    for (int r = 0; r < EACH; ++r) ventry[r] = group_entry(i, v_key(r) >> 4);
+    for (int r = 0; r < EACH; ++r) entry[r] = table[(group_pos(i, r) >> c.page_shift) + zero];
   };
   auto load_k = [&](int i) {
 #pragma unroll
     for (int r = 0; r < EACH; ++r) {
+      page[r] = c.pages + (int64_t)clamp_page(c, __builtin_amdgcn_readfirstlane(entry[r])) *
+                              c.page_stride;
+      const int slot = group_pos(i, r) & ((1 << c.page_shift) - 1);
       typedef uint32_t Piece __attribute__((ext_vector_type(KB / 4)));
-      const Piece x = *reinterpret_cast<const Piece*>(page_at(kentry[r]) +
-                                                      code_at(c, 0, h, slot_of(i, k_key(r))) +
-                                                      KB * (piece(r) % (D / KB)));
+      const Piece x = *reinterpret_cast<const Piece*>(page[r] + code_at(c, 0, h, slot) + k_lane);
 #pragma unroll
       for (int j = 0; j < KB / 4; ++j) kreg[r][j] = x[j];
+      sreg[r] = *reinterpret_cast<const float*>(page[r] + scale_at(c, 0, h, slot) + s_lane);
     }
-    sreg = *reinterpret_cast<const float*>(page_at(sentry) +
-                                           scale_at(c, t >> 2 & 1, h, slot_of(i, 16 * (t & 3))));
   };
   auto load_v = [&](int i) {
 #pragma unroll
     for (int r = 0; r < EACH; ++r) {
-      const uint8_t* at = page_at(ventry[r]) + code_at(c, 1, h, slot_of(i, v_key(r))) + v_d(r);
+      const int slot = group_pos(i, r) & ((1 << c.page_shift) - 1);
+      const uint8_t* const at = page[r] + code_at(c, 1, h, slot);
 #pragma unroll
-      for (int j = 0; j < VK; ++j) vreg[r][j] = *reinterpret_cast<const uint32_t*>(at + j * D);
+      for (int j = 0; j < VK; ++j)
+        vreg[r][j] = *reinterpret_cast<const uint32_t*>(at + (v_lane + j * D));
     }
   };
   auto k_slot = [&](int key, int slot) { return key * KROW + 16 * slot; };
@@ -175,8 +176,8 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
         *reinterpret_cast<v4u*>(to + k_slot(k_key(r), (x & 1) * (D / 16) + (x >> 1))) =
             widen8<T, C>(kreg[r][2 * j], kreg[r][2 * j + 1]);
       }
+      s_scale[i & 1][4 * lane + group(r)] = sreg[r];
     }
-    s_scale[i & 1][t] = sreg;
   };
   // values that no row sees become 0; a NaN code, which some rows may see and
   // others not, becomes 0 too and is put back through the P of the rows that
@@ -375,19 +376,16 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     Prob p0, p1;
 #pragma unroll
     for (int k = 0; k < 2; ++k) p0.f[k] = p1.f[k] = v4u{0, 0, 0, 0};
-    find_k(0);
-    find_v(0);
+    find(0);
     load_k(0);
     load_v(0);
-    find_k(1);
-    find_v(1);
+    find(1);
     stage_k(0);
     clean_v(0);
     stage_v(0);
     load_k(1);
     load_v(1);
-    find_k(2);
-    find_v(2);
+    find(2);
     __syncthreads();
     // holds the exponentials next to the products (they are used after a branch
     // only, and would be moved behind it)
@@ -406,7 +404,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
         load_k(i + 2);
         keep_here(p0, l);
         clean_v(i + 1);
-        find_k(i + 3);
+        find(i + 3);
         __syncthreads();
         const bool again = __any(!(over <= kMost));
         if (again) l = before;
@@ -418,7 +416,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
         stage_k(i + 1);
         load_k(i + 2);
         clean_v(i + 1);
-        find_k(i + 3);
+        find(i + 3);
         __syncthreads();
         return false;
       }
@@ -434,7 +432,6 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
         stage_v(i + 1);
         load_v(i + 2);
         keep_here(p1, l);
-        find_v(i + 3);
         const bool again = __any(!(over <= kMost));
         if (again) l = before;
         return again;
@@ -444,7 +441,6 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
         soft(is_plain, s1, p1, i, 1);
         stage_v(i + 1);
         load_v(i + 2);
-        find_v(i + 3);
         return false;
       }
     };

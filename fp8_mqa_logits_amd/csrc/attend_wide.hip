@@ -239,8 +239,8 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     v4u f[2];  // of the half's two groups of keys
   };
   // of the current tile, per group of 16 keys (the same in all lanes): the
-  // factor of the scores; vs / vref, its logarithm + kBias and its inverse
-  float fk[4], vr[4], lv[4], iv[4];
+  // factor of the scores; the logarithm + kBias and the inverse of vs / vref
+  float fk[4], lv[4], iv[4];
   bool plain = false;  // every row sees every key, and the scales are ordinary
 
   auto rescale_pending = [&](Prob& pr, float keep) {
@@ -249,36 +249,33 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     for (int k = 0; k < 2; ++k)
       pr.f[k] = __builtin_bit_cast(v4u, __builtin_bit_cast(v8h, pr.f[k]) * k16);
   };
-  float most = 0.f;
-  auto take_scales = [&](int i) {
-    const float* s = s_scale[i & 1];
-    float vs[4];
-    most = 0.f;
+  uint64_t above = 0;  // scales of values that pass vref
+  auto take_scales = [&](int i) {  // lanes 0 .. 3 the groups' keys, 4 .. 7 their values
+    const float x = s_scale[i & 1][lane & 7], to_value = x * down;
+    const float key = x * cs, lg = __builtin_amdgcn_logf(to_value) + kBias;
+    const float inv = __builtin_amdgcn_rcpf(to_value);
+    auto of = [&](float y, int from) {
+      return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(y), from));
+    };
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      fk[g] = uniform(s[g] * cs);
-      vs[g] = uniform(s[4 + g]);
-      most = vs[g] < __builtin_inff() ? __builtin_fmaxf(most, vs[g]) : most;
+      fk[g] = of(key, g);
+      lv[g] = of(lg, 4 + g);
+      iv[g] = of(inv, 4 + g);
     }
-    bool ordinary = true;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      vr[g] = uniform(vs[g] * down);
-      lv[g] = uniform(__builtin_amdgcn_logf(vr[g]) + kBias);
-      iv[g] = uniform(__builtin_amdgcn_rcpf(vr[g]));
-      ordinary = ordinary && vr[g] >= 0x1p-60f && vr[g] <= 1.f;
-    }
-    plain = __builtin_amdgcn_readfirstlane((int)(ordinary && inside(i)));
+    above = __ballot(x > vref && x < __builtin_inff()) & 0xF0;
+    plain = (__ballot(to_value >= 0x1p-60f && to_value <= 1.f) & 0xF0) == 0xF0 && inside(i);
   };
   // moves vref where a scale of tile i passes it
   auto settle_scales = [&](int i, Prob& pending) {
-    if (most <= vref) return;
-    const float to = power_above(most);
+    if (!above) return;
+    const float x = s_scale[i & 1][4 + (lane & 3)];
+    const float to = uniform(power_above(wave_max(x < __builtin_inff() ? x : 0.f)));
     const float keep = vref / to;
 #pragma unroll
     for (int d = 0; d < DT; ++d) acc[d] *= keep;
     rescale_pending(pending, keep);
-    vref = uniform(to);
+    vref = to;
     down = uniform(1.f / to);
     take_scales(i);
   };
@@ -336,6 +333,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int g = 2 * half + k;
+        const float vr = s_scale[i & 1][4 + g] * down;
         float e[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -343,7 +341,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
           const float x = or_zero(
               __builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * k + j], fk[g], kBias - m)), see);
           l += x;
-          e[j] = __uint_as_float(__float_as_uint(or_zero(x * vr[g], see)) |
+          e[j] = __uint_as_float(__float_as_uint(or_zero(x * vr, see)) |
                                  (bit(ill, key_at(8 * k + j)) & 0x7FC00000u));
         }
         pr.f[k] = pack(e);
@@ -465,7 +463,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
           }
           if (++i >= tiles) break;
           take_scales(i);
-          if (!plain || most > vref) break;
+          if (!plain) break;
         }
         if (i >= tiles) break;
         if (left == kTile) {

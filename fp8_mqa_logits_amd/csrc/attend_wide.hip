@@ -103,7 +103,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   const int per_split = (all + p.splits - 1) / p.splits;
   const int tile_lo = split * per_split;
   const int tiles = min(all - tile_lo, per_split);
-  const int base = first + tile_lo * 64;
+  const int base = __builtin_amdgcn_readfirstlane(first + tile_lo * 64);
 
   // staging: piece x = t + THREADS r of the keys is KB bytes of key x / (D /
   // KB); of the values, columns 4 (x % (D / 4)) .. + 3 of VK keys from
@@ -183,6 +183,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   // others not, becomes 0 too and is put back through the P of the rows that
   // see it (0 * NaN would reach the others)
   auto clean_v = [&](int i) {
+    if (inside(i) && inside(i + 1)) return;
     if (t == 0) s_poison[(i + 1) % 3][0] = s_poison[(i + 1) % 3][1] = 0;
     if (inside(i)) return;
 #pragma unroll
@@ -317,19 +318,19 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
       for (int k = 0; k < 2; ++k) {
         const int g = 2 * half + k;
         const float off = lv[g] - m;
-        float e[8], sum = 0.f;
+        float e[8], sum;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * k + j], fk[g], off));
-          sum += e[j];
+          sum = j ? sum + e[j] : e[j];
         }
         l = __builtin_fmaf(sum, iv[g], l);
-        over += sum;
+        over = k ? over + sum : sum;
         pr.f[k] = pack(e);
       }
     } else {
       const uint32_t sees = seen_keys(i, half);
-      const uint32_t ill = sees & (s_poison[i % 3][half] >> (4 * hh));
+      const uint32_t ill = inside(i) ? 0 : sees & (s_poison[i % 3][half] >> (4 * hh));
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int g = 2 * half + k;
@@ -381,9 +382,9 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     stage_k(0);
     clean_v(0);
     stage_v(0);
-    load_k(1);
-    load_v(1);
+    load_k(1);  // (in the loop's order: what is waited for there is counted)
     find(2);
+    load_v(1);
     __syncthreads();
     // holds the exponentials next to the products (they are used after a branch
     // only, and would be moved behind it)

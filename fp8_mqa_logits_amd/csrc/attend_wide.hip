@@ -131,17 +131,20 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   const uint32_t s_lane = (lane & 1) * (scale_at(c, 1, h, 0) - scale_at(c, 0, h, 0));
   uint32_t kreg[EACH][KB / 4], vreg[EACH][VK];
   float sreg[EACH];
-  int entry[EACH];
+  int found[EACH], entry[EACH];
   const uint8_t* page[EACH];
   auto find = [&](int i) {
 #pragma unroll
-    for (int r = 0; r < EACH; ++r) entry[r] = table[(group_pos(i, r) >> c.page_shift) + zero];
+    for (int r = 0; r < EACH; ++r) found[r] = table[(group_pos(i, r) >> c.page_shift) + zero];
+  };
+  auto look = [&]() {  // (after the loads that may be in flight behind find's)
+#pragma unroll
+    for (int r = 0; r < EACH; ++r) entry[r] = __builtin_amdgcn_readfirstlane(found[r]);
   };
   auto load_k = [&](int i) {
 #pragma unroll
     for (int r = 0; r < EACH; ++r) {
-      page[r] = c.pages + (int64_t)clamp_page(c, __builtin_amdgcn_readfirstlane(entry[r])) *
-                              c.page_stride;
+      page[r] = c.pages + (int64_t)clamp_page(c, entry[r]) * c.page_stride;
       const int slot = group_pos(i, r) & ((1 << c.page_shift) - 1);
       typedef uint32_t Piece __attribute__((ext_vector_type(KB / 4)));
       const Piece x = *reinterpret_cast<const Piece*>(page[r] + code_at(c, 0, h, slot) + k_lane);
@@ -376,15 +379,18 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
 #pragma unroll
     for (int k = 0; k < 2; ++k) p0.f[k] = p1.f[k] = v4u{0, 0, 0, 0};
     find(0);
+    look();
     load_k(0);
-    load_v(0);
     find(1);
+    load_v(0);
+    look();
     stage_k(0);
     clean_v(0);
     stage_v(0);
-    load_k(1);  // (in the loop's order: what is waited for there is counted)
+    load_k(1);
     find(2);
     load_v(1);
+    look();
     __syncthreads();
     // holds the exponentials next to the products (they are used after a branch
     // only, and would be moved behind it)
@@ -430,6 +436,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
         values(p0, i, 0);
         stage_v(i + 1);
         load_v(i + 2);
+        look();
         keep_here(p1, l);
         const bool again = __any(!(over <= kMost));
         if (again) l = before;
@@ -440,6 +447,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
         soft(is_plain, s1, p1, i, 1);
         stage_v(i + 1);
         load_v(i + 2);
+        look();
         return false;
       }
     };

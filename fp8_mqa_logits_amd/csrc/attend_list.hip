@@ -93,7 +93,7 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
   const int step_hi = min(steps, step_lo + per_split);
 
   const float cs = p.scale * kLog2e;
-  float m[NT], l[NT], vref = 0x1p-126f, down = 0x1p126f;  // down = 1 / vref
+  float m[NT], l[NT], vref = kVref, down = kUp / kVref;  // down = kUp / vref
   v4f acc[NT][U];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -265,7 +265,7 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
       if (__any(finite > vref)) {
         const float to = power_above(wave_max(finite)), keep = vref / to;
         vref = uniform(to);
-        down = uniform(1.f / to);
+        down = uniform(kUp / to);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll

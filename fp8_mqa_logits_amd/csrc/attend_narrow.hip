@@ -85,7 +85,7 @@ void attend_narrow_kernel(AttendParams p) {
   const int step_hi = min(steps, (split + 1) * per_split);
 
   const float cs = p.scale * kLog2e;
-  float m[NT], l[NT], vref = 0x1p-126f, down = 0x1p126f;  // down = 1 / vref
+  float m[NT], l[NT], vref = kVref, down = kUp / kVref;  // down = kUp / vref
   v4f acc[NT][U];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -175,7 +175,7 @@ void attend_narrow_kernel(AttendParams p) {
     if (most > vref) {
       const float to = power_above(most), keep = vref / to;
       vref = uniform(to);
-      down = uniform(1.f / to);
+      down = uniform(kUp / to);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll

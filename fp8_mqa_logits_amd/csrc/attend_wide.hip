@@ -56,8 +56,11 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   constexpr int KROW = 2 * D + 16, VROW = 2 * 64 + 16;  // bytes of a staged key, of a column
   __shared__ __align__(16) uint8_t s_k[2][64 * KROW];
   __shared__ __align__(16) uint8_t s_v[2][D * VROW];
-  __shared__ __align__(16) float s_scale[2][256];  // 8 scales, over and over
-  __shared__ uint32_t s_poison[3][2];
+  // of a tile: 8 scales, over and over; keys whose values hold a NaN code. A wave
+  // behind the others reads them until the next tile's barrier, one ahead writes
+  // two tiles further meanwhile and clears a third: four buffers.
+  __shared__ __align__(16) float s_scale[4][256];
+  __shared__ uint32_t s_poison[4][2];
   __shared__ Span s_span[W];
 
   const int row_lo = unit * p.R + tile * COLS / p.group;
@@ -65,7 +68,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   const int row_hi = unit * p.R + (last - 1) / p.group;
   Span span = row_span(p, row_lo, row_hi - row_lo + 1, t, THREADS);
   if (lane == 0) s_span[wave] = span;
-  if (t < 6) s_poison[t >> 1][t & 1] = 0;
+  if (t < 8) s_poison[t >> 1][t & 1] = 0;
   // the first half adds no values: P = 0 times what is staged "before" them
   for (int x = t; x < D * VROW / 16; x += THREADS)
     reinterpret_cast<v4u*>(s_v[1])[x] = v4u{0, 0, 0, 0};
@@ -179,7 +182,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
         *reinterpret_cast<v4u*>(to + k_slot(k_key(r), (x & 1) * (D / 16) + (x >> 1))) =
             widen8<T, C>(kreg[r][2 * j], kreg[r][2 * j + 1]);
       }
-      s_scale[i & 1][4 * lane + group(r)] = sreg[r];
+      s_scale[i & 3][4 * lane + group(r)] = sreg[r];
     }
   };
   // values that no row sees become 0; a NaN code, which some rows may see and
@@ -187,7 +190,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   // see it (0 * NaN would reach the others)
   auto clean_v = [&](int i) {
     if (inside(i) && inside(i + 1)) return;
-    if (t == 0) s_poison[(i + 1) % 3][0] = s_poison[(i + 1) % 3][1] = 0;
+    if (t == 0) s_poison[(i + 1) & 3][0] = s_poison[(i + 1) & 3][1] = 0;
     if (inside(i)) return;
 #pragma unroll
     for (int r = 0; r < EACH; ++r) {
@@ -199,7 +202,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
           const uint32_t bad = nan_bytes(vreg[r][j]);
           if (bad) {
             vreg[r][j] &= ~bad;
-            atomicOr(&s_poison[i % 3][key >> 5], 1u << (key & 31));
+            atomicOr(&s_poison[i & 3][key >> 5], 1u << (key & 31));
           }
         }
       }
@@ -235,7 +238,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   };
 
   const float cs = p.scale * kLog2e;
-  float m = kLowest, l = 0.f, vref = 0x1p-126f, down = 0x1p126f;  // down = 1 / vref
+  float m = kLowest, l = 0.f, vref = kVref, down = kUp / kVref;  // down = kUp / vref
   v16f acc[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d) acc[d] = v16f{};
@@ -243,7 +246,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     v4u f[2];  // of the half's two groups of keys
   };
   // of the current tile, per group of 16 keys (the same in all lanes): the
-  // factor of the scores; the logarithm + kBias and the inverse of vs / vref
+  // factor of the scores; the logarithm + kBias and the inverse of kUp vs / vref
   float fk[4], lv[4], iv[4];
   bool plain = false;  // every row sees every key, and the scales are ordinary
 
@@ -255,7 +258,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   };
   uint64_t above = 0;  // scales of values that pass vref
   auto take_scales = [&](int i) {  // lanes 0 .. 3 the groups' keys, 4 .. 7 their values
-    const float x = s_scale[i & 1][lane & 7], to_value = x * down;
+    const float x = s_scale[i & 3][lane & 7], to_value = x * down;
     const float key = x * cs, lg = __builtin_amdgcn_logf(to_value) + kBias;
     const float inv = __builtin_amdgcn_rcpf(to_value);
     auto of = [&](float y, int from) {
@@ -268,19 +271,19 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
       iv[g] = of(inv, 4 + g);
     }
     above = __ballot(x > vref && x < __builtin_inff()) & 0xF0;
-    plain = (__ballot(to_value >= 0x1p-60f && to_value <= 1.f) & 0xF0) == 0xF0 && inside(i);
+    plain = (__ballot(to_value >= 0x1p-60f && to_value <= kUp) & 0xF0) == 0xF0 && inside(i);
   };
   // moves vref where a scale of tile i passes it
   auto settle_scales = [&](int i, Prob& pending) {
     if (!above) return;
-    const float x = s_scale[i & 1][4 + (lane & 3)];
+    const float x = s_scale[i & 3][4 + (lane & 3)];
     const float to = uniform(power_above(wave_max(x < __builtin_inff() ? x : 0.f)));
     const float keep = vref / to;
 #pragma unroll
     for (int d = 0; d < DT; ++d) acc[d] *= keep;
     rescale_pending(pending, keep);
     vref = to;
-    down = uniform(1.f / to);
+    down = uniform(kUp / to);
     take_scales(i);
   };
   auto scores = [&](v16f& s, int i, int half) {
@@ -313,7 +316,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     return f;
   };
   // scores -> probabilities of one half; of a plain tile's, the largest sum of
-  // eight of them: over kMost, m has to move and they are to be formed again
+  // eight of them: over kUp kMost, m has to move and they are to be formed again
   auto soft = [&](auto is_plain, const v16f& s, Prob& pr, int i, int half) {
     float over = 0.f;
     if constexpr (is_plain.value) {
@@ -333,11 +336,11 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
       }
     } else {
       const uint32_t sees = seen_keys(i, half);
-      const uint32_t ill = inside(i) ? 0 : sees & (s_poison[i % 3][half] >> (4 * hh));
+      const uint32_t ill = inside(i) ? 0 : sees & (s_poison[i & 3][half] >> (4 * hh));
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int g = 2 * half + k;
-        const float vr = s_scale[i & 1][4 + g] * down;
+        const float vr = s_scale[i & 3][4 + g] * down;
         float e[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -411,7 +414,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
         clean_v(i + 1);
         find(i + 3);
         __syncthreads();
-        const bool again = __any(!(over <= kMost));
+        const bool again = __any(!(over <= kUp * kMost));
         if (again) l = before;
         return again;
       } else {
@@ -438,7 +441,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
         load_v(i + 2);
         look();
         keep_here(p1, l);
-        const bool again = __any(!(over <= kMost));
+        const bool again = __any(!(over <= kUp * kMost));
         if (again) l = before;
         return again;
       } else {
@@ -518,7 +521,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   }
   // score row x of product d's sums is row 32 d + x of the staged values: four
   // neighbouring columns are in DT products (and halves of them)
-  const float by = direct ? vref / sum : vref;
+  const float by = direct ? vref / kUp / sum : vref / kUp;
 #pragma unroll
   for (int e = 0; e < 4 * DT; ++e) {
     float v[4];

@@ -41,8 +41,14 @@ def layout(pool):
     return mqa.KVLayout(Hkv, D, P, B, pool.kind)
 
 
+def reached(pool, table, ends):
+    """The table without the pages past every row's end."""
+    return table[:, :max(1, -(-int(ends.max()) // pool.dims[2]))]
+
+
 def check(pool, table, q, starts, ends, indices=None, scale=None):
-    want, lse, tol, tol_lse = ref.attend(pool, q, table, starts, ends, scale, indices)
+    want, lse, tol, tol_lse = ref.attend(pool, q, reached(pool, table, ends), starts, ends, scale,
+                                         indices)
     args = [layout(pool), q.cuda(), pool.bytes().cuda(), table.cuda()]
     if indices is not None:
         args.append(indices.cuda())
@@ -94,6 +100,44 @@ def test_rows_of_any_range(shape, see):
     if see == "mixed":
         assert bool((out[0::6] == 0).all()) and bool((lse[0::6] == -math.inf).all())
         assert bool((out[3::6] == 0).all()) and bool((lse[3::6] == -math.inf).all())
+
+
+# calls whose tables have room for 131072 positions run on tiles of 128 and 256
+# columns however short their contexts are
+CHUNKS = [s for s in SHAPES if s[1] in (40, 70, 130, 333)] + [
+    ([700, 90], 20, 8, 2, 128, 64, 64),
+    ([70], 17, 8, 2, 64, 16, 16),
+    ([3000], 70, 4, 1, 64, 64, 32),
+]
+
+
+@pytest.mark.parametrize("dtype,codes", [(BF16, "e4m3"), (FP16, "int8"), (FP16, "e4m3"),
+                                         (BF16, "int8")])
+@pytest.mark.parametrize("shape", CHUNKS, ids=lambda s: "x".join(map(str, s[1:])))
+def test_wide_tiles(shape, dtype, codes):
+    for see in ("causal", "window", "full", "mixed"):
+        say(f"case: wide tiles {shape} {dtype} {codes} {see}")
+        check(*problem(*shape, dtype, codes, see, extra=131072 // shape[5]))
+
+
+@pytest.mark.parametrize("dtype,codes,D", [(BF16, "e4m3", 128), (FP16, "int8", 128),
+                                           (FP16, "e4m3", 64), (BF16, "int8", 64)])
+@pytest.mark.parametrize("R", [20, 45])
+@pytest.mark.parametrize("loud", [1.0, 6.0])
+def test_wide_tiles_over_many_keys(R, loud, dtype, codes, D):
+    # requests enough for one part each, so that every workgroup goes through
+    # dozens of tiles; with loud scores the rows' largest ones are met all along
+    say(f"case: many keys {R} {loud} {dtype} {codes} {D}")
+    lens, times = [2300, 1111, 1984], 44
+    pool, table, q, starts, ends = problem(lens, R, 8, 2, D, 64, 32, dtype, codes)
+    q = (q.float() * loud).to(dtype)
+    want, lse, tol, tol_lse = ref.attend(pool, q, table, starts, ends)
+    out, got_lse = mqa.mqa_attend_paged(
+        layout(pool), q.cuda().repeat(times, 1, 1), pool.bytes().cuda(),
+        table.cuda().repeat(times, 1), starts.cuda().repeat(times), ends.cuda().repeat(times),
+        return_lse=True)
+    assert ref.differs(out, want.repeat(times, 1, 1), tol.repeat(times, 1, 1)) == 0
+    assert ref.differs(got_lse, lse.repeat(times, 1), tol_lse.repeat(times, 1)) == 0
 
 
 @pytest.mark.parametrize("split", [97, 128])
@@ -149,13 +193,15 @@ def test_list_of_everything_is_the_range():
     assert torch.allclose(la, lb, atol=1e-5)
 
 
+@pytest.mark.parametrize("room", [1, 4096])  # (pages past the contexts: wider tiles)
 @pytest.mark.parametrize("R,Hq", [(1, 8), (5, 8), (90, 8), (3, 64), (200, 32)])
 @pytest.mark.parametrize("codes", ["e4m3", "int8"])
-def test_unseen_positions_may_hold_anything(R, Hq, codes):
+def test_unseen_positions_may_hold_anything(R, Hq, codes, room):
     # NaN codes and NaN, infinite and negative scales in slots no row sees
     say(f"case: garbage {R} {Hq} {codes}")
     lens = [411, 250]
-    pool, table, q, starts, ends = problem(lens, R, Hq, 2, 128, 32, 16, BF16, codes, "causal")
+    pool, table, q, starts, ends = problem(lens, R, Hq, 2, 128, 32, 16, BF16, codes, "causal",
+                                           extra=room)
     starts += 100
     clean = pool.bytes()
     args = (starts.cuda(), ends.cuda())
@@ -179,11 +225,13 @@ def test_unseen_positions_may_hold_anything(R, Hq, codes):
     assert torch.equal(clean_out, out)
 
 
+@pytest.mark.parametrize("room", [1, 4096])  # (pages past the contexts: wider tiles)
 @pytest.mark.parametrize("where", ["k", "v"])
 @pytest.mark.parametrize("R,Hq", [(4, 8), (40, 8), (150, 16)])
-def test_nan_reaches_only_the_rows_that_see_it(R, Hq, where):
+def test_nan_reaches_only_the_rows_that_see_it(R, Hq, where, room):
     say(f"case: NaN in {where}, {R} rows")
-    pool, table, q, starts, ends = problem([400], R, Hq, 2, 128, 32, 32, BF16, "e4m3", "causal")
+    pool, table, q, starts, ends = problem([400], R, Hq, 2, 128, 32, 32, BF16, "e4m3", "causal",
+                                           extra=room)
     at = 400 - R // 2  # the later rows see it
     pool.codes[table[0, at // 32].long(), 0 if where == "k" else 1, 1, at % 32, 5] = 0x7F
     out = mqa.mqa_attend_paged(layout(pool), q.cuda(), pool.bytes().cuda(), table.cuda(),
@@ -194,7 +242,7 @@ def test_nan_reaches_only_the_rows_that_see_it(R, Hq, where):
     assert bool(torch.isfinite(out[~sees]).all()) and bool(torch.isfinite(out[:, ~heads]).all())
     hit = torch.isnan(out[sees][:, heads])
     assert bool(hit.all()) if where == "k" else bool(hit[..., 5].all())
-    want, _, tol, _ = ref.attend(pool, q, table, starts, ends)
+    want, _, tol, _ = ref.attend(pool, q, reached(pool, table, ends), starts, ends)
     assert ref.differs(out[~sees], want[~sees], tol[~sees]) == 0
 
 
@@ -217,12 +265,13 @@ def test_nan_of_a_position_without_weight(R):
         assert bool(torch.isnan(out[0::2, :, 5]).all()) and bool(torch.isfinite(out[1::2]).all())
 
 
-@pytest.mark.parametrize("R", [1, 40, 100])
-def test_scales_of_very_different_size(R):
+@pytest.mark.parametrize("R,room", [(1, 1), (40, 1), (100, 1), (40, 8192), (100, 8192)])
+def test_scales_of_very_different_size(R, room):
     # value scales that fall and rise by 2^40 along the context, zero blocks
     # among them; the softmax sees all of them
     say(f"case: uneven scales, {R} rows")
-    pool, table, q, starts, ends = problem([640], R, 8, 2, 128, 32, 16, BF16, "e4m3", "causal")
+    pool, table, q, starts, ends = problem([640], R, 8, 2, 128, 32, 16, BF16, "e4m3", "causal",
+                                           extra=room)
     for j in range(40):
         page, b = int(table[0, j * 16 // 32]), j * 16 % 32 // 16
         pool.scales[page, 1, :, b] = [2.0 ** -20, 1.0, 0.0, 2.0 ** 20, 2.0 ** -8][j % 5]

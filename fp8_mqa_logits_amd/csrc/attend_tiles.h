@@ -9,17 +9,20 @@
 // on the matrix unit in q's own type with fp32 sums, and the scales come in
 // afterwards, in fp32. The probabilities go to the second product in fp16
 // whatever q's type (11 bits; bf16's 8 would add an error as large as the
-// rounding of a bf16 output), as P = 2^11 exp2(S' - m) vs / vref with S' in
+// rounding of a bf16 output), as P = 2^10 exp2(S' - m) vs / vref with S' in
 // units of ln 2 and vref the power of two above the largest value scale met so
-// far: at most 2^15, and full precision down to 2^-25 of the row's largest. (Of
+// far: at most 65504, and full precision down to 2^-24 of the row's largest. (Of
 // the exponentials l sums 2^7 exp2(S' - m): a larger power would cost bits of lse
 // where it is near 0.)
 // Reference points move lazily: m, to the next integer above the largest score,
-// only when the P that a lane forms at once (eight or sixteen of them) could add
-// up to more than 2^15 (no search for a largest score in the
-// common step: 374 -> 367 us for 32 rows of 16 heads over 131072 positions, 3.28
-// -> 3.26 ms for 4096 rows of 32 heads over 49152); vref when a larger scale is met. Both times the sums
-// are rescaled, by powers of two. l sums the fp32 P before its rounding.
+// only when eight P that a lane forms could add up to more than 65504 (no search
+// for a largest score in the common step: 374 -> 367 us for 32 rows of 16 heads
+// over 131072 positions); vref when a larger scale is met. Both times the sums
+// are rescaled, by powers of two. l sums the fp32 exponentials before P's rounding.
+// (2^10 is a choice between the two ends of fp16: at 2^7 outputs near 2^-20, made
+// up of values of such weights, were off by up to twice an fp16 output's own
+// rounding; the higher P starts the more often m moves, and 4096 rows of 32 heads
+// over 49152 positions take 5% longer than at 2^7, and 10% at 2^11.)
 
 #pragma once
 
@@ -42,8 +45,8 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.4028234e38f;  // m of a column that has seen nothing
 constexpr float kBias = 7.f;               // exponentials are 2^kBias at a score of m
-constexpr float kMost = 2048.f;            // most that those formed at once may add up to
-constexpr float kUp = 16.f;                // P = kUp times them, times vs / vref
+constexpr float kUp = 8.f;                 // P = kUp times them, times vs / vref
+constexpr float kMost = 65504.f / kUp;     // most that eight of them may add up to
 constexpr float kVref = 0x1p-122f;         // vref at first
 
 // 4 codes of one dword -> 4 values of the matrix unit's type.

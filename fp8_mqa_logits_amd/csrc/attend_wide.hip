@@ -22,9 +22,9 @@ namespace {
 // next barrier. m and vref only move by powers of two, so that a P in flight can
 // be rescaled exactly.
 //
-// 4096 rows of 32 heads over 49152 positions of 4 key heads: 3.26 ms, 970 TFLOP/s,
-// 82% of what a large matrix product reaches here; two requests of 1024 rows
-// packed into 32768 positions of 8 key heads 577 us, 923 TFLOP/s. Bound by LDS reads (every wave
+// 4096 rows of 32 heads over 49152 positions of 4 key heads: 3.04 ms, 1.04 PFLOP/s,
+// 88% of what a large matrix product reaches here; two requests of 1024 rows
+// packed into 32768 positions of 8 key heads 555 us, 960 TFLOP/s. Bound by LDS reads (every wave
 // reads all keys and values for its 32 columns: 2048 clocks a tile of 64 keys at
 // 128 bytes a clock, two thirds of its time or more) next to the exponentials; 64 columns a wave would halve
 // the reads but leave one wave per SIMD (3.97 ms), two groups of waves in turn
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   auto v_d = [&](int r) { return piece(r) % (D / 4) * 4; };
   // What a wave takes lies in one group of 16 keys, so that its page, its
   // addresses (but for an offset that each lane keeps) and its scales are the
-  // wave's. A group that no row sees is read from the nearest one that some row
+  // wave's (3.08 ms, not 3.24, for those 4096 rows on one card). A group that no row sees is read from the nearest one that some row
   // sees (masked later; no branch in the loop). Its table entry is loaded a tile
   // before its use, and only looked at then, by a vector load: a scalar one would
   // have every LDS read in flight waited for.
@@ -257,7 +257,9 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
       pr.f[k] = __builtin_bit_cast(v4u, __builtin_bit_cast(v8h, pr.f[k]) * k16);
   };
   uint64_t above = 0;  // scales of values that pass vref
-  auto take_scales = [&](int i) {  // lanes 0 .. 3 the groups' keys, 4 .. 7 their values
+  // lanes 0 .. 3 the groups' keys, 4 .. 7 their values (all at once: 3.18 ms, not
+  // 3.34, on one card)
+  auto take_scales = [&](int i) {
     const float x = s_scale[i & 3][lane & 7], to_value = x * down;
     const float key = x * cs, lg = __builtin_amdgcn_logf(to_value) + kBias;
     const float inv = __builtin_amdgcn_rcpf(to_value);
@@ -331,7 +333,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
           sum = j ? sum + e[j] : e[j];
         }
         l = __builtin_fmaf(sum, iv[g], l);
-        over = k ? over + sum : sum;
+        over = k ? __builtin_fmaxf(over, sum) : sum;
         pr.f[k] = pack(e);
       }
     } else {
@@ -357,13 +359,14 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     return over;
   };
   // moves m to a half's largest score, where that is above it
-  auto settle = [&](const v16f& s, int i, int half) {
-    const uint32_t sees = seen_keys(i, half);
+  auto settle = [&](auto is_plain, const v16f& s, int i, int half) {
+    const uint32_t sees = is_plain.value ? 0 : seen_keys(i, half);
     float top = -__builtin_inff();
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      top = __builtin_fmaxf(top,
-                            or_lowest(s[e] * fk[2 * half + (e >> 3)], bit(sees, key_at(e))));
+    for (int e = 0; e < 16; ++e) {
+      const float x = s[e] * fk[2 * half + (e >> 3)];
+      top = __builtin_fmaxf(top, is_plain.value ? x : or_lowest(x, bit(sees, key_at(e))));
+    }
     top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
     if (!__any(top > m)) return;
     const float to = __builtin_fmaxf(m, __builtin_ceilf(top));
@@ -419,7 +422,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
         return again;
       } else {
         values(p1, i - 1, 1);
-        settle(s0, i, 0);
+        settle(is_plain, s0, i, 0);
         soft(is_plain, s0, p0, i, 0);
         stage_k(i + 1);
         load_k(i + 2);
@@ -446,7 +449,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
         return again;
       } else {
         values(p0, i, 0);
-        settle(s1, i, 1);
+        settle(is_plain, s1, i, 1);
         soft(is_plain, s1, p1, i, 1);
         stage_v(i + 1);
         load_v(i + 2);
@@ -483,12 +486,13 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
           continue;
         }
         if (left == kFirst) {
-          settle(s0, i, 0);
-          soft(no, s0, p0, i, 0);
-          half1(no, i);
-        } else {
-          settle(s1, i, 1);
-          soft(no, s1, p1, i, 1);
+          settle(yes, s0, i, 0);
+          soft(yes, s0, p0, i, 0);
+          if (half1(yes, i)) left = kSecond;
+        }
+        if (left == kSecond) {
+          settle(yes, s1, i, 1);
+          soft(yes, s1, p1, i, 1);
         }
       } else {
         half0(no, i);

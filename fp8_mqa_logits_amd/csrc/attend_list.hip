@@ -18,9 +18,9 @@ namespace {
 // Bound by the gathered bytes: 64 x 2 rows of 2048 positions, 8 key heads of 4
 // query heads, take 93 us, 5.8 TB/s. So nearly with 64 query heads on one key
 // head, where each row gathers what others gather too, but from a cache larger
-// than an L2, and the vector unit (widening, exponentials) is busy most of the
-// time: 4096 rows of 2048 of 65536 positions 409 us, 5.2 TB/s of gathered codes,
-// 672 TFLOP/s.
+// than an L2, and vector instructions (widening, exponentials) take 59% of the
+// cycles or more: 4096 rows of 2048 of 65536 positions 405 to 418 us, 5.1 to 5.3
+// TB/s of gathered codes, 660 to 680 TFLOP/s.
 //
 // A step's tokens (slots in the pool) are found by lanes 0 .. 31, an entry
 // each, two steps ahead, and go to the other lanes by permutation; scales go

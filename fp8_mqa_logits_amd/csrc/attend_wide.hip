@@ -22,14 +22,16 @@ namespace {
 // next barrier. m and vref only move by powers of two, so that a P in flight can
 // be rescaled exactly.
 //
-// 4096 rows of 32 heads over 49152 positions of 4 key heads: 3.04 ms, 1.04 PFLOP/s,
-// 88% of what a large matrix product reaches here; two requests of 1024 rows
-// packed into 32768 positions of 8 key heads 555 us, 960 TFLOP/s. Bound by LDS reads (every wave
-// reads all keys and values for its 32 columns: 2048 clocks a tile of 64 keys at
-// 128 bytes a clock, two thirds of its time or more) next to the exponentials; 64 columns a wave would halve
-// the reads but leave one wave per SIMD (3.97 ms), two groups of waves in turn
-// on the matrix and the vector unit met at too many barriers (4.46 ms). What
-// the two waves per SIMD spill lies outside the plain tiles' loop.
+// 4096 rows of 32 heads over 49152 positions of 4 key heads: 3.04 to 3.09 ms, 1.02
+// to 1.04 PFLOP/s, 86 to 88% of what a large matrix product reaches here; two
+// requests of 1024 rows packed into 32768 positions of 8 key heads 570 us, 934
+// TFLOP/s. By the counters the matrix unit is busy 46% of the cycles, vector
+// instructions take 40% or more at four cycles each (exponentials need more), LDS
+// is active a third: two waves per SIMD overlap the first two only in part. 64
+// columns a wave would halve the LDS reads but leave one wave per SIMD (3.97 ms);
+// two groups of waves in turn on the matrix and the vector unit met at too many
+// barriers (4.46 ms). What the two waves per SIMD spill lies outside the plain
+// tiles' loop.
 template <int T, int C, int D, int W>
 __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) {
   constexpr int THREADS = 64 * W;

@@ -236,7 +236,7 @@ void attend_narrow_kernel(AttendParams p) {
                                                bit(sees[t], 16 * (j >> 2) + (j & 3))));
         top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
         top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
-        const float to = __builtin_fmaxf(m[t], __builtin_ceilf(top));
+        const float to = __builtin_fmaxf(m[t], top);
         const float keep = __builtin_amdgcn_exp2f(m[t] - to);
         m[t] = to;
         l[t] *= keep;

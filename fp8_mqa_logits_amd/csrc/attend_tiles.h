@@ -14,11 +14,13 @@
 // far: at most 65504, and full precision down to 2^-24 of the row's largest. (Of
 // the exponentials l sums 2^7 exp2(S' - m): a larger power would cost bits of lse
 // where it is near 0.)
-// Reference points move lazily: m, to the next integer above the largest score,
-// only when eight P that a lane forms could add up to more than 65504 (no search
-// for a largest score in the common step: 374 -> 367 us for 32 rows of 16 heads
-// over 131072 positions); vref when a larger scale is met. Both times the sums
-// are rescaled, by powers of two. l sums the fp32 exponentials before P's rounding.
+// Reference points move lazily: m, to the largest score, only when eight P that a
+// lane forms could add up to more than 65504 (no search for a largest score in the
+// common step: 374 -> 367 us for 32 rows of 16 heads over 131072 positions); vref
+// when a larger scale is met. Both times the sums are rescaled. (With scales that
+// are powers of two the P of the largest score is then exact, which matters where
+// few keys leave no error to average out.) l sums the fp32 exponentials before P's
+// rounding.
 // (2^10 is a choice between the two ends of fp16: at 2^7 outputs near 2^-20, made
 // up of values of such weights, were off by up to twice an fp16 output's own
 // rounding; the higher P starts the more often m moves, and 4096 rows of 32 heads

@@ -19,7 +19,7 @@ namespace {
 // that the matrix unit and the vector unit work at the same time. One barrier
 // a tile: between the halves of tile i, when the keys of tile i + 1 are in
 // LDS; its values follow during the second half and are first read after the
-// next barrier. m and vref only move by powers of two, so that a P in flight can
+// next barrier. vref only moves by powers of two, so that a P in flight can
 // be rescaled exactly.
 //
 // 4096 rows of 32 heads over 49152 positions of 4 key heads: 3.04 to 3.09 ms, 1.02
@@ -371,7 +371,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     }
     top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
     if (!__any(top > m)) return;
-    const float to = __builtin_fmaxf(m, __builtin_ceilf(top));
+    const float to = __builtin_fmaxf(m, is_plain.value ? __builtin_ceilf(top) : top);
     const float keep = __builtin_amdgcn_exp2f(m - to);
     m = to;
     l *= keep;

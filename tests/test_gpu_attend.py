@@ -283,6 +283,33 @@ def test_scales_of_very_different_size(R, room):
     check(pool, table, q, starts, ends)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("R,room", [(1, 1), (30, 1), (30, 4096), (70, 4096)])
+def test_one_appended_token_is_what_read_gives(R, room, dtype):
+    # a row that sees one position has probability 1, and append's scales are
+    # powers of two: the very value that a read returns
+    say(f"case: single appended keys, {R} rows {dtype}")
+    L = mqa.KVLayout(kv_heads=2, head_dim=128, page_size=32, block=16, codes="e4m3")
+    table = torch.full((1, 7 + room), -1, dtype=torch.int32)
+    table[0, :7] = torch.randperm(7, generator=torch.Generator().manual_seed(3)).int()
+    cache = torch.zeros(7, L.page_bytes, dtype=torch.uint8, device="cuda")
+    g = torch.Generator().manual_seed(4)
+    k, v = (torch.randn(200, 2, 128, generator=g).to(dtype).cuda() for _ in range(2))
+    first = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mqa.mqa_kv_append(L, k, v, cache, table.cuda(), first)
+    starts = torch.arange(R).int() + 50
+    q = torch.randn(R, 8, 128, generator=g).to(dtype).cuda()
+    _, want = mqa.mqa_kv_read(L, cache, table.cuda(), first + 50, None, R, dtype=dtype)
+    want = want.repeat_interleave(4, dim=1)
+    out = mqa.mqa_attend_paged(L, q, cache, table.cuda(), starts.cuda(), (starts + 1).cuda())
+    assert torch.equal(out, want)
+    idx = torch.full((R, 8), -1, dtype=torch.int32)
+    idx[:, 3] = 0
+    out = mqa.mqa_attend_topk(L, q, cache, table.cuda(), idx.cuda(), starts.cuda(),
+                              (starts + 1).cuda())
+    assert torch.equal(out, want)
+
+
 def test_one_small_block_decides():
     # a row whose softmax lies in a block 2^30 below its neighbours' scale
     say("case: small block decides")

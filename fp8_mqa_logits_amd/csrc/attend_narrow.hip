@@ -170,8 +170,28 @@ void attend_narrow_kernel(AttendParams p) {
     load_k(st + WAVES);
     find(st + 2 * WAVES);
 
-    const float most = __builtin_fmaxf(v_scale[0] < __builtin_inff() ? v_scale[0] : 0.f,
-                                       v_scale[1] < __builtin_inff() ? v_scale[1] : 0.f);
+    const int pos0 = first + st * 32;
+    const bool clean = pos0 >= span.in_lo && pos0 + 32 <= span.in_hi;  // all rows see all keys
+    uint32_t sees[NT], ill = 0;  // bit 16 b + i: key 16 b + 4 g + i
+#pragma unroll
+    for (int t = 0; t < NT; ++t) sees[t] = ~0u;
+    // what lies between the rows' ranges may hold anything: a half that no column
+    // sees has no part in vref
+    float largest[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) largest[b] = v_scale[b] < __builtin_inff() ? v_scale[b] : 0.f;
+    if (!clean) {
+      uint32_t any = 0;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        sees[t] = seen_bits(pos0, col_s[t], col_e[t]) >> (4 * g);
+        any |= sees[t];
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        if (!__any(any & (0xFu << (16 * b)))) largest[b] = 0.f;
+    }
+    const float most = __builtin_fmaxf(largest[0], largest[1]);
     if (most > vref) {
       const float to = power_above(most), keep = vref / to;
       vref = uniform(to);
@@ -182,14 +202,7 @@ void attend_narrow_kernel(AttendParams p) {
         for (int u = 0; u < U; ++u) acc[t][u] *= keep;
     }
     const float vr[2] = {v_scale[0] * down, v_scale[1] * down};
-    const int pos0 = first + st * 32;
-    const bool clean = pos0 >= span.in_lo && pos0 + 32 <= span.in_hi;  // all rows see all keys
-    uint32_t sees[NT], ill = 0;  // bit 16 b + i: key 16 b + 4 g + i
-#pragma unroll
-    for (int t = 0; t < NT; ++t) sees[t] = ~0u;
     if (!clean) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t) sees[t] = seen_bits(pos0, col_s[t], col_e[t]) >> (4 * g);
       // values that no row sees become 0; a NaN code, which some rows may
       // see and others not, becomes 0 too and is put back through the P of
       // the rows that see it (0 * NaN would reach the others)

@@ -154,10 +154,11 @@ __device__ __forceinline__ float uniform(float x) {
   return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
 }
 
-// The power of two at or above a positive finite scale.
+// The power of two at or above a positive finite scale (2^127 above that).
 __device__ __forceinline__ float power_above(float x) {
   const uint32_t u = __float_as_uint(x);
-  return __uint_as_float((u & 0x7FFFFFu) ? (u & 0x7F800000u) + 0x800000u : u);
+  const uint32_t up = (u & 0x7FFFFFu) ? (u & 0x7F800000u) + 0x800000u : u;
+  return __uint_as_float(min(up, 0x7F000000u));
 }
 
 // Bits of the positions pos .. pos + 31 that lie in [s, e).

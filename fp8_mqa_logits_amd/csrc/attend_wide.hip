@@ -277,11 +277,20 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     above = __ballot(x > vref && x < __builtin_inff()) & 0xF0;
     plain = (__ballot(to_value >= 0x1p-60f && to_value <= kUp) & 0xF0) == 0xF0 && inside(i);
   };
-  // moves vref where a scale of tile i passes it
+  // moves vref where a scale of tile i passes it, of a group that some column of the
+  // wave sees (what lies between the rows' ranges may hold anything)
   auto settle_scales = [&](int i, Prob& pending) {
     if (!above) return;
+    bool seen = inside(i);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int pos = base + i * 64 + 16 * g;
+      if (__any(max(col_s, pos) < min(col_e, pos + 16))) seen |= (lane & 3) == g;
+    }
     const float x = s_scale[i & 3][4 + (lane & 3)];
-    const float to = uniform(power_above(wave_max(x < __builtin_inff() ? x : 0.f)));
+    const float most = wave_max(seen && x < __builtin_inff() ? x : 0.f);
+    if (!__any(most > vref)) return;
+    const float to = uniform(power_above(most));
     const float keep = vref / to;
 #pragma unroll
     for (int d = 0; d < DT; ++d) acc[d] *= keep;

@@ -1,0 +1,68 @@
+"""Attention over the paged 8-bit cache where value scales differ widely.
+Reference and tolerances: attend_ref.attend (scales here are large enough that its
+absolute term of 2^-25 has no part)."""
+import math
+
+import pytest
+import torch
+
+import attend_ref as ref
+import fp8_mqa_logits_amd as mqa
+from gpu_helpers import say
+from test_gpu_attend import layout, problem
+
+pytestmark = pytest.mark.gpu
+BF16, FP16 = torch.bfloat16, torch.float16
+
+# rows and query heads (of 2 key heads) that make tiles of 16, 32, 64, 128 and 256
+# columns where the table has room for long contexts; without room all take 16
+TILES = [(2, 8), (4, 16), (6, 16), (8, 32), (20, 32)]
+LENGTH, P, B = 700, 32, 16
+
+
+def garbage_gap(pool, table, gap, scale, codes, entries):
+    """The cache and table with `scale` and the largest codes in the blocks of
+    positions [gap[0], gap[1]); entries: of the pages that lie in it whole, "own" or
+    "none" (-1, which reads as page 0)."""
+    g = ref.Pool(len(pool.codes) + 1, *pool.dims, pool.kind, 1)
+    g.codes[1:], g.scales[1:] = pool.codes, pool.scales
+    g.codes[0] = 0x7E if codes == "e4m3" else 0x80
+    g.scales[0] = scale
+    moved = torch.where(table >= 0, table + 1, table)
+    for pos in range(gap[0], gap[1], B):
+        page, b = int(moved[0, pos // P]), pos % P // B
+        g.codes[page, :, :, pos % P:pos % P + B] = 0x7E if codes == "e4m3" else 0x80
+        g.scales[page, :, :, b] = scale
+    if entries == "none":
+        moved[0, -(-gap[0] // P):gap[1] // P] = -1
+    return g, moved
+
+
+@pytest.mark.parametrize("codes,dtype", [("e4m3", BF16), ("int8", FP16)])
+@pytest.mark.parametrize("room", [1, 4096])
+@pytest.mark.parametrize("R,Hq", TILES)
+def test_blocks_between_the_rows_ranges_may_hold_anything(R, Hq, room, codes, dtype):
+    # two packed requests, and windows apart, with whole blocks between them
+    # that no row sees: the same bits whatever those hold
+    pool, table, q, starts, ends = problem([LENGTH], R, Hq, 2, 128, P, B, dtype, codes, "full",
+                                           extra=room)
+    first = torch.arange(R) < R // 2
+    for see, gap in (("packed", (208, 416)), ("apart", (48, 640))):
+        if see == "packed":
+            starts = torch.where(first, 0, 421).int()
+            ends = torch.where(first, 202 - torch.arange(R), LENGTH).int()
+        else:
+            starts = torch.where(torch.arange(R) % 2 == 0, 645, 3).int()
+            ends = (starts + 40).int()
+        args = (starts.cuda(), ends.cuda())
+        want, want_lse = mqa.mqa_attend_paged(layout(pool), q.cuda(), pool.bytes().cuda(),
+                                              table.cuda(), *args, return_lse=True)
+        exact, exact_lse, tol, tol_lse = ref.attend(pool, q, table[:, :-(-LENGTH // P)], starts, ends)
+        assert ref.differs(want, exact, tol) == 0 and ref.differs(want_lse, exact_lse, tol_lse) == 0
+        for scale in (2.0 ** 20, 1e12, 1e30, 3e38, math.inf, math.nan):
+            for entries in ("own", "none"):
+                say(f"case: gap {R} {Hq} {room} {codes} {see} {scale} {entries}")
+                g, moved = garbage_gap(pool, table, gap, scale, codes, entries)
+                out, lse = mqa.mqa_attend_paged(layout(g), q.cuda(), g.bytes().cuda(),
+                                                moved.cuda(), *args, return_lse=True)
+                assert torch.equal(out, want) and torch.equal(lse, want_lse)

@@ -19,8 +19,7 @@ namespace {
 // that the matrix unit and the vector unit work at the same time. One barrier
 // a tile: between the halves of tile i, when the keys of tile i + 1 are in
 // LDS; its values follow during the second half and are first read after the
-// next barrier. vref only moves by powers of two, so that a P in flight can
-// be rescaled exactly.
+// next barrier.
 //
 // 4096 rows of 32 heads over 49152 positions of 4 key heads: 3.04 to 3.09 ms, 1.02
 // to 1.04 PFLOP/s, 86 to 88% of what a large matrix product reaches here; two
@@ -252,12 +251,6 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   float fk[4], lv[4], iv[4];
   bool plain = false;  // every row sees every key, and the scales are ordinary
 
-  auto rescale_pending = [&](Prob& pr, float keep) {
-    const _Float16 k16 = (_Float16)keep;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      pr.f[k] = __builtin_bit_cast(v4u, __builtin_bit_cast(v8h, pr.f[k]) * k16);
-  };
   uint64_t above = 0;  // scales of values that pass vref
   // lanes 0 .. 3 the groups' keys, 4 .. 7 their values (all at once: 3.18 ms, not
   // 3.34, on one card)
@@ -277,28 +270,6 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     above = __ballot(x > vref && x < __builtin_inff()) & 0xF0;
     plain = (__ballot(to_value >= 0x1p-60f && to_value <= kUp) & 0xF0) == 0xF0 && inside(i);
   };
-  // moves vref where a scale of tile i passes it, of a group that some column of the
-  // wave sees (what lies between the rows' ranges may hold anything)
-  auto settle_scales = [&](int i, Prob& pending) {
-    if (!above) return;
-    bool seen = inside(i);
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int pos = base + i * 64 + 16 * g;
-      if (__any(max(col_s, pos) < min(col_e, pos + 16))) seen |= (lane & 3) == g;
-    }
-    const float x = s_scale[i & 3][4 + (lane & 3)];
-    const float most = wave_max(seen && x < __builtin_inff() ? x : 0.f);
-    if (!__any(most > vref)) return;
-    const float to = uniform(power_above(most));
-    const float keep = vref / to;
-#pragma unroll
-    for (int d = 0; d < DT; ++d) acc[d] *= keep;
-    rescale_pending(pending, keep);
-    vref = to;
-    down = uniform(kUp / to);
-    take_scales(i);
-  };
   auto scores = [&](v16f& s, int i, int half) {
     const uint8_t* const from = s_k[i & 1] + k_slot(n, hh);
     s = v16f{};
@@ -315,6 +286,31 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
         acc[d] = mfma32<kFp16>(
             *reinterpret_cast<const v4u*>(from + v_slot(32 * d, 2 * (2 * half + k))), pr.f[k],
             acc[d]);
+  };
+  // moves vref where a scale of tile i passes it, of a group that some column of the
+  // wave sees (what lies between the rows' ranges may hold anything). The P of the tile before
+  // that are still to be multiplied are so at once: in fp16 they would lose bits
+  auto settle_scales = [&](int i, Prob& pending) {
+    if (!above) return;
+    bool seen = inside(i);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int pos = base + i * 64 + 16 * g;
+      if (__any(max(col_s, pos) < min(col_e, pos + 16))) seen |= (lane & 3) == g;
+    }
+    const float x = s_scale[i & 3][4 + (lane & 3)];
+    const float most = wave_max(seen && x < __builtin_inff() ? x : 0.f);
+    if (!__any(most > vref)) return;
+    const float to = uniform(power_above(most));
+    const float keep = vref / to;
+    values(pending, i - 1, 1);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) pending.f[k] = v4u{0, 0, 0, 0};
+#pragma unroll
+    for (int d = 0; d < DT; ++d) acc[d] *= keep;
+    vref = to;
+    down = uniform(kUp / to);
+    take_scales(i);
   };
   // bit key_at(e): whether the column sees the key of its score e
   auto seen_keys = [&](int i, int half) {

@@ -66,3 +66,37 @@ def test_blocks_between_the_rows_ranges_may_hold_anything(R, Hq, room, codes, dt
                 out, lse = mqa.mqa_attend_paged(layout(g), q.cuda(), g.bytes().cuda(),
                                                 moved.cuda(), *args, return_lse=True)
                 assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def quiet_weight(pool, table, loud, ratio):
+    """Blocks of the positions in `loud` get keys of the lowest code (scores far
+    below the others' for positive queries) and values 2^ratio louder."""
+    for pos in loud:
+        page, b = int(table[0, pos // P]), pos % P // B
+        pool.codes[page, 0, :, pos % P:pos % P + B] = 0xFE if pool.kind == "e4m3" else 0x81
+        pool.scales[page, 0, :, b] = 1.0 / 64 if pool.kind == "e4m3" else 1.0 / 18
+        pool.scales[page, 1, :, b] *= 2.0 ** ratio
+
+
+@pytest.mark.parametrize("ratio", [20, 26, 40])
+@pytest.mark.parametrize("tile", [0, 2])
+@pytest.mark.parametrize("codes", ["e4m3", "int8"])
+@pytest.mark.parametrize("R,Hq", [(8, 32), (20, 32), (40, 8)])
+def test_louder_tile_without_weight_after_a_tile_with_all_of_it(R, Hq, codes, tile, ratio):
+    # 64 keys of equal score hold the softmax; all others score far lower, and the
+    # next 64 have much larger scales: both halves of the 64 keep their weight
+    say(f"case: louder tile after {R} {Hq} {codes} {tile} {ratio}")
+    pool, table, q, starts, ends = problem([LENGTH], R, Hq, 2, 128, P, B, BF16, codes, "full",
+                                           extra=4096)
+    pool.scales[:, 1] = 0.125
+    quiet_weight(pool, table, range(0, LENGTH, B), 0)
+    for pos in range(64 * tile, 64 * tile + 64):
+        pool.codes[int(table[0, pos // P]), 0, :, pos % P] = 0
+    for pos in range(64 * tile + 64, 64 * tile + 128, B):
+        pool.scales[int(table[0, pos // P]), 1, :, pos % P // B] *= 2.0 ** ratio
+    q = (q.float().abs() + 1.0).to(BF16)
+    want, lse, tol, tol_lse = ref.attend(pool, q, table[:, :-(-LENGTH // P)], starts, ends)
+    out, got_lse = mqa.mqa_attend_paged(layout(pool), q.cuda(), pool.bytes().cuda(), table.cuda(),
+                                        starts.cuda(), ends.cuda(), return_lse=True)
+    assert ref.differs(out, want, tol) == 0
+    assert ref.differs(got_lse, lse, tol_lse) == 0

@@ -47,7 +47,7 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
   __shared__ __align__(16) union {
     struct {
       __align__(16) uint8_t rows[KW][BUFS][64 * D];  // 32 keys, 32 values
-      __align__(16) float ks[4][32], vs[4][32];
+      __align__(16) float ks[4][32], vs[4][32], loud[4][32];
     } step;
     Finish<D, NT, HW, KW> finish;
     int used[4];
@@ -93,7 +93,7 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
   const int step_hi = min(steps, step_lo + per_split);
 
   const float cs = p.scale * kLog2e;
-  float m[NT], l[NT], vref = kVref, down = kUp / kVref;  // down = kUp / vref
+  float m[NT], l[NT];
   v4f acc[NT][U];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -195,6 +195,9 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
       f[b] = *reinterpret_cast<const v4f*>(&sh.step.ks[wave][16 * b + 4 * g]);
       vr[b] = *reinterpret_cast<const v4f*>(&sh.step.vs[wave][16 * b + 4 * g]);
     }
+    float loudest = kFar;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) loudest = __builtin_fmaxf(loudest, vr[j >> 2][j & 3]);
     v4u pf[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -213,12 +216,15 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
         for (int j = 1; j < 8; ++j) sum += e[j];
       };
       exponentials();
-      if (__any(!(sum <= kMost))) {  // m moves
+      if (__any(!(sum * loudest <= kMost))) {  // m moves
         float top = -__builtin_inff();
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          top = __builtin_fmaxf(top, or_lowest(x[t][j >> 2][j & 3] * f[j >> 2][j & 3],
-                                               bit(sees, 16 * (j >> 2) + (j & 3))));
+        for (int j = 0; j < 8; ++j) {
+          const float loud = sh.step.loud[wave][16 * (j >> 2) + 4 * g + (j & 3)];
+          top = __builtin_fmaxf(
+              top, or_lowest(__builtin_fmaf(x[t][j >> 2][j & 3], f[j >> 2][j & 3], loud),
+                             bit(sees, 16 * (j >> 2) + (j & 3))));
+        }
         top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
         top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
         const float to = __builtin_fmaxf(m[t], top);
@@ -261,18 +267,9 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
     // a round's scales and which of its entries name positions
     auto take_scales = [&](const Codes& f) {
       const float k = f.named ? f.ks * cs : 0.f, v = f.named ? f.vs : 0.f;
-      const float finite = v < __builtin_inff() ? v : 0.f;
-      if (__any(finite > vref)) {
-        const float to = power_above(wave_max(finite)), keep = vref / to;
-        vref = uniform(to);
-        down = uniform(kUp / to);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int u = 0; u < U; ++u) acc[t][u] *= keep;
-      }
       sh.step.ks[wave][lane & 31] = k;
-      sh.step.vs[wave][lane & 31] = v * down;
+      sh.step.vs[wave][lane & 31] = v * kUp;
+      sh.step.loud[wave][lane & 31] = loudness(v * kUp);
       __builtin_amdgcn_wave_barrier();
     };
     // Loads come back in order: what a later round's addresses wait for is asked
@@ -308,7 +305,7 @@ __global__ __launch_bounds__(256, 2) void attend_list_kernel(AttendParams p) {
     for (; i < rounds; ++i) round(i, 0);
   }
   __syncthreads();  // (the steps' memory becomes the sums')
-  finish<T, true>(p, sh.finish, block, row, p.group, tile, h, wave, m, l, vref, acc);
+  finish<T, true>(p, sh.finish, block, row, p.group, tile, h, wave, m, l, acc);
 }
 
 template <int T, int C, int D>

@@ -85,7 +85,7 @@ void attend_narrow_kernel(AttendParams p) {
   const int step_hi = min(steps, (split + 1) * per_split);
 
   const float cs = p.scale * kLog2e;
-  float m[NT], l[NT], vref = kVref, down = kUp / kVref;  // down = kUp / vref
+  float m[NT], l[NT];
   v4f acc[NT][U];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -175,11 +175,6 @@ void attend_narrow_kernel(AttendParams p) {
     uint32_t sees[NT], ill = 0;  // bit 16 b + i: key 16 b + 4 g + i
 #pragma unroll
     for (int t = 0; t < NT; ++t) sees[t] = ~0u;
-    // what lies between the rows' ranges may hold anything: a half that no column
-    // sees has no part in vref
-    float largest[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) largest[b] = v_scale[b] < __builtin_inff() ? v_scale[b] : 0.f;
     if (!clean) {
       uint32_t any = 0;
 #pragma unroll
@@ -187,22 +182,10 @@ void attend_narrow_kernel(AttendParams p) {
         sees[t] = seen_bits(pos0, col_s[t], col_e[t]) >> (4 * g);
         any |= sees[t];
       }
+      // (what lies between the rows' ranges may hold anything)
 #pragma unroll
       for (int b = 0; b < 2; ++b)
-        if (!__any(any & (0xFu << (16 * b)))) largest[b] = 0.f;
-    }
-    const float most = __builtin_fmaxf(largest[0], largest[1]);
-    if (most > vref) {
-      const float to = power_above(most), keep = vref / to;
-      vref = uniform(to);
-      down = uniform(kUp / to);
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int u = 0; u < U; ++u) acc[t][u] *= keep;
-    }
-    const float vr[2] = {v_scale[0] * down, v_scale[1] * down};
-    if (!clean) {
+        if (!__any(any & (0xFu << (16 * b)))) v_scale[b] = 0.f;
       // values that no row sees become 0; a NaN code, which some rows may
       // see and others not, becomes 0 too and is put back through the P of
       // the rows that see it (0 * NaN would reach the others)
@@ -223,6 +206,8 @@ void attend_narrow_kernel(AttendParams p) {
           if (__ballot(bad != 0) >> (16 * g) & 0xFFFF) ill |= 1u << (16 * (j >> 2) + (j & 3));
       }
     }
+    const float vr[2] = {v_scale[0] * kUp, v_scale[1] * kUp};
+    const float loudest = __builtin_fmaxf(__builtin_fmaxf(vr[0], vr[1]), kFar);
     v4u pf[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -241,12 +226,14 @@ void attend_narrow_kernel(AttendParams p) {
         for (int j = 1; j < 8; ++j) sum += e[j];
       };
       exponentials();
-      if (__any(!(sum <= kMost))) {  // m moves
+      if (__any(!(sum * loudest <= kMost))) {  // m moves
+        const float loud[2] = {loudness(vr[0]), loudness(vr[1])};
         float top = -__builtin_inff();
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          top = __builtin_fmaxf(top, or_lowest(x[t][j >> 2][j & 3] * f[j >> 2],
-                                               bit(sees[t], 16 * (j >> 2) + (j & 3))));
+          top = __builtin_fmaxf(
+              top, or_lowest(__builtin_fmaf(x[t][j >> 2][j & 3], f[j >> 2], loud[j >> 2]),
+                             bit(sees[t], 16 * (j >> 2) + (j & 3))));
         top = __builtin_fmaxf(top, __shfl_xor(top, 16, 64));
         top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
         const float to = __builtin_fmaxf(m[t], top);
@@ -293,7 +280,7 @@ void attend_narrow_kernel(AttendParams p) {
 #pragma unroll
   for (int t = 0; t < NT; ++t)
     if (col_s[t] >= col_e[t]) l[t] = 0.f;  // sums of a row that sees nothing
-  finish<T, false>(p, s_finish, block, unit * p.R, columns, tile, h, wave, m, l, vref, acc);
+  finish<T, false>(p, s_finish, block, unit * p.R, columns, tile, h, wave, m, l, acc);
 }
 
 template <int T, int C, int D>

@@ -9,18 +9,18 @@
 // on the matrix unit in q's own type with fp32 sums, and the scales come in
 // afterwards, in fp32. The probabilities go to the second product in fp16
 // whatever q's type (11 bits; bf16's 8 would add an error as large as the
-// rounding of a bf16 output), as P = 2^10 exp2(S' - m) vs / vref with S' in
-// units of ln 2 and vref the power of two above the largest value scale met so
-// far: at most 65504, and full precision down to 2^-24 of the row's largest. (Of
-// the exponentials l sums 2^7 exp2(S' - m): a larger power would cost bits of lse
-// where it is near 0.)
-// Reference points move lazily: m, to the largest score, only when eight P that a
-// lane forms could add up to more than 65504 (no search for a largest score in the
-// common step: 374 -> 367 us for 32 rows of 16 heads over 131072 positions); vref
-// when a larger scale is met. Both times the sums are rescaled. (With scales that
-// are powers of two the P of the largest score is then exact, which matters where
-// few keys leave no error to average out.) l sums the fp32 exponentials before P's
-// rounding.
+// rounding of a bf16 output), as P = 2^10 e vs, where the exponentials e =
+// 2^7 exp2(S' - m), S' in units of ln 2, are what l sums in fp32, before P's
+// rounding. Every (row, head) column has its own reference point m, the largest of
+// its S' + log2(vs / kVref) when m last moved: its loudest weight exp2(S') vs has P
+// = 2^10 or more, at most 65504, and weights down to 2^-24 of it keep full
+// precision, whatever other rows see and however loud the blocks are to which it
+// gives no weight. m moves only when the P that a lane forms could pass 65504 (no
+// search for a largest weight in the common step: 374 -> 367 us for 32 rows of 16
+// heads over 131072 positions), and the sums are rescaled then. kVref is a value
+// scale such as activations have; it keeps e near 2^7, where l costs lse no bits.
+// In m, vs / kVref counts as 2^kLeast at least: e of a block of zeros stays finite,
+// and value scales below 2^-97 lose precision.
 // (2^10 is a choice between the two ends of fp16: at 2^7 outputs near 2^-20, made
 // up of values of such weights, were off by up to twice an fp16 output's own
 // rounding; the higher P starts the more often m moves, and 4096 rows of 32 heads
@@ -46,10 +46,13 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.4028234e38f;  // m of a column that has seen nothing
-constexpr float kBias = 7.f;               // exponentials are 2^kBias at a score of m
-constexpr float kUp = 8.f;                 // P = kUp times them, times vs / vref
-constexpr float kMost = 65504.f / kUp;     // most that eight of them may add up to
-constexpr float kVref = 0x1p-122f;         // vref at first
+constexpr float kVref = 0x1p-7f;
+constexpr float kBias = 7.f;               // e is 2^kBias at m, for a value scale of kVref
+constexpr float kTop = 10.f;               // and P 2^kTop
+constexpr float kUp = 0x1p10f;             // P = kUp vs e: 2^(kTop - kBias) / kVref
+constexpr float kMost = 65504.f;           // most that eight P may add up to
+constexpr float kFar = 0x1p-88f;           // eight e times kFar, too
+constexpr float kLeast = -90.f;            // least log2(vs / kVref) in m
 
 // 4 codes of one dword -> 4 values of the matrix unit's type.
 template <int T, int C>
@@ -150,15 +153,9 @@ __device__ __forceinline__ auto constant(const X* x) {
   return (const __attribute__((address_space(4))) X*)(uintptr_t)x;
 }
 
-__device__ __forceinline__ float uniform(float x) {
-  return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
-}
-
-// The power of two at or above a positive finite scale (2^127 above that).
-__device__ __forceinline__ float power_above(float x) {
-  const uint32_t u = __float_as_uint(x);
-  const uint32_t up = (u & 0x7FFFFFu) ? (u & 0x7F800000u) + 0x800000u : u;
-  return __uint_as_float(min(up, 0x7F000000u));
+// log2(vs / kVref) as m takes it, of kUp vs.
+__device__ __forceinline__ float loudness(float vr) {
+  return __builtin_fmaxf(__builtin_amdgcn_logf(vr) - (kTop - kBias), kLeast);
 }
 
 // Bits of the positions pos .. pos + 31 that lie in [s, e).
@@ -225,7 +222,7 @@ template <int T, bool INLINE, int D, int NT, int HW, int KW>
 __device__ __forceinline__ void finish(const AttendParams& p, Finish<D, NT, HW, KW>& sh,
                                        int64_t block, int first_row, int columns, int tile, int h,
                                        int wave, const float (&m)[NT], const float (&l_in)[NT],
-                                       float vref, const v4f (&acc)[NT][D / 16]) {
+                                       const v4f (&acc)[NT][D / 16]) {
   using F = Finish<D, NT, HW, KW>;
   constexpr int U = F::U, US = F::US, COLS = F::COLS;
   const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
@@ -247,7 +244,7 @@ __device__ __forceinline__ void finish(const AttendParams& p, Finish<D, NT, HW, 
     float top = kLowest;
 #pragma unroll
     for (int w = 0; w < KW; ++w) top = __builtin_fmaxf(top, sh.m[w][16 * (NT * hw + t) + n]);
-    part[t] = __builtin_amdgcn_exp2f(m[t] - top) * (vref / kUp);
+    part[t] = __builtin_amdgcn_exp2f(m[t] - top) * (1.f / kUp);
   }
   const int col = threadIdx.x % COLS, at_col = tile * COLS + col;  // what this thread writes
   const bool real = at_col < columns;

@@ -239,7 +239,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   };
 
   const float cs = p.scale * kLog2e;
-  float m = kLowest, l = 0.f, vref = kVref, down = kUp / kVref;  // down = kUp / vref
+  float m = kLowest, l = 0.f;
   v16f acc[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d) acc[d] = v16f{};
@@ -247,15 +247,14 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     v4u f[2];  // of the half's two groups of keys
   };
   // of the current tile, per group of 16 keys (the same in all lanes): the
-  // factor of the scores; the logarithm + kBias and the inverse of kUp vs / vref
+  // factor of the scores; the logarithm + kBias and the inverse of kUp vs
   float fk[4], lv[4], iv[4];
   bool plain = false;  // every row sees every key, and the scales are ordinary
 
-  uint64_t above = 0;  // scales of values that pass vref
   // lanes 0 .. 3 the groups' keys, 4 .. 7 their values (all at once: 3.18 ms, not
   // 3.34, on one card)
   auto take_scales = [&](int i) {
-    const float x = s_scale[i & 3][lane & 7], to_value = x * down;
+    const float x = s_scale[i & 3][lane & 7], to_value = x * kUp;
     const float key = x * cs, lg = __builtin_amdgcn_logf(to_value) + kBias;
     const float inv = __builtin_amdgcn_rcpf(to_value);
     auto of = [&](float y, int from) {
@@ -267,8 +266,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
       lv[g] = of(lg, 4 + g);
       iv[g] = of(inv, 4 + g);
     }
-    above = __ballot(x > vref && x < __builtin_inff()) & 0xF0;
-    plain = (__ballot(to_value >= 0x1p-60f && to_value <= kUp) & 0xF0) == 0xF0 && inside(i);
+    plain = (__ballot(to_value >= 0x1p-40f && to_value <= 0x1p40f) & 0xF0) == 0xF0 && inside(i);
   };
   auto scores = [&](v16f& s, int i, int half) {
     const uint8_t* const from = s_k[i & 1] + k_slot(n, hh);
@@ -287,31 +285,6 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
             *reinterpret_cast<const v4u*>(from + v_slot(32 * d, 2 * (2 * half + k))), pr.f[k],
             acc[d]);
   };
-  // moves vref where a scale of tile i passes it, of a group that some column of the
-  // wave sees (what lies between the rows' ranges may hold anything). The P of the tile before
-  // that are still to be multiplied are so at once: in fp16 they would lose bits
-  auto settle_scales = [&](int i, Prob& pending) {
-    if (!above) return;
-    bool seen = inside(i);
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int pos = base + i * 64 + 16 * g;
-      if (__any(max(col_s, pos) < min(col_e, pos + 16))) seen |= (lane & 3) == g;
-    }
-    const float x = s_scale[i & 3][4 + (lane & 3)];
-    const float most = wave_max(seen && x < __builtin_inff() ? x : 0.f);
-    if (!__any(most > vref)) return;
-    const float to = uniform(power_above(most));
-    const float keep = vref / to;
-    values(pending, i - 1, 1);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) pending.f[k] = v4u{0, 0, 0, 0};
-#pragma unroll
-    for (int d = 0; d < DT; ++d) acc[d] *= keep;
-    vref = to;
-    down = uniform(kUp / to);
-    take_scales(i);
-  };
   // bit key_at(e): whether the column sees the key of its score e
   auto seen_keys = [&](int i, int half) {
     return seen_bits(base + i * 64 + 32 * half, col_s, col_e) >> (4 * hh);
@@ -325,7 +298,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     return f;
   };
   // scores -> probabilities of one half; of a plain tile's, the largest sum of
-  // eight of them: over kUp kMost, m has to move and they are to be formed again
+  // eight of them: over kMost, m has to move and they are to be formed again
   auto soft = [&](auto is_plain, const v16f& s, Prob& pr, int i, int half) {
     float over = 0.f;
     if constexpr (is_plain.value) {
@@ -349,7 +322,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int g = 2 * half + k;
-        const float vr = s_scale[i & 3][4 + g] * down;
+        const float vr = s_scale[i & 3][4 + g] * kUp;
         float e[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -365,18 +338,22 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     }
     return over;
   };
-  // moves m to a half's largest score, where that is above it
+  // moves m to a half's loudest weight, where that is above it (to the next integer
+  // in plain tiles, where every column has many keys)
   auto settle = [&](auto is_plain, const v16f& s, int i, int half) {
     const uint32_t sees = is_plain.value ? 0 : seen_keys(i, half);
     float top = -__builtin_inff();
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const float x = s[e] * fk[2 * half + (e >> 3)];
+      const int g = 2 * half + (e >> 3);
+      const float x = __builtin_fmaf(
+          s[e], fk[g], is_plain.value ? lv[g] : __builtin_fmaxf(lv[g] - kTop, kLeast));
       top = __builtin_fmaxf(top, is_plain.value ? x : or_lowest(x, bit(sees, key_at(e))));
     }
     top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64));
+    if (is_plain.value) top = __builtin_ceilf(top) - kTop;
     if (!__any(top > m)) return;
-    const float to = __builtin_fmaxf(m, is_plain.value ? __builtin_ceilf(top) : top);
+    const float to = __builtin_fmaxf(m, top);
     const float keep = __builtin_amdgcn_exp2f(m - to);
     m = to;
     l *= keep;
@@ -424,7 +401,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
         clean_v(i + 1);
         find(i + 3);
         __syncthreads();
-        const bool again = __any(!(over <= kUp * kMost));
+        const bool again = __any(!(over <= kMost));
         if (again) l = before;
         return again;
       } else {
@@ -451,7 +428,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
         load_v(i + 2);
         look();
         keep_here(p1, l);
-        const bool again = __any(!(over <= kUp * kMost));
+        const bool again = __any(!(over <= kMost));
         if (again) l = before;
         return again;
       } else {
@@ -469,7 +446,6 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
     // or a tile needs masks.
     int i = 0;
     take_scales(0);
-    settle_scales(0, p1);
     scores(s0, 0, 0);
     while (true) {
       if (plain) {
@@ -488,10 +464,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
           if (!plain) break;
         }
         if (i >= tiles) break;
-        if (left == kTile) {
-          settle_scales(i, p1);
-          continue;
-        }
+        if (left == kTile) continue;
         if (left == kFirst) {
           settle(yes, s0, i, 0);
           soft(yes, s0, p0, i, 0);
@@ -507,7 +480,6 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
       }
       if (++i >= tiles) break;
       take_scales(i);
-      settle_scales(i, p1);
     }
     values(p1, tiles - 1, 1);
   }
@@ -532,7 +504,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   }
   // score row x of product d's sums is row 32 d + x of the staged values: four
   // neighbouring columns are in DT products (and halves of them)
-  const float by = direct ? vref / kUp / sum : vref / kUp;
+  const float by = direct ? 1.f / kUp / sum : 1.f / kUp;
 #pragma unroll
   for (int e = 0; e < 4 * DT; ++e) {
     float v[4];

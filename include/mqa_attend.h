@@ -128,7 +128,10 @@ size_t workspace_size_attend(int requests, int R, int heads, int kv_heads, int h
  * Scores, softmax sums and the output's sums are held in fp32. Positions that
  * no row sees may hold anything (also NaN codes and NaN or infinite scales); a
  * table entry outside [0, num_pages) is clamped into it. Scales of seen
- * positions must be >= 0. A row that sees a NaN code becomes NaN (of a value's,
+ * positions must be >= 0, the values' at most 2^100. Probabilities times value
+ * scales are rounded to 11 bits for the output's sums, down to 2^-24 of the row's
+ * and head's largest such product (whatever other rows see); smaller ones, and
+ * those of value scales below 2^-97, lose bits. A row that sees a NaN code becomes NaN (of a value's,
  * at least in its column), and no other row does.
  */
 int mqa_attend_paged(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,

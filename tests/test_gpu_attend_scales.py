@@ -1,6 +1,7 @@
-"""Attention over the paged 8-bit cache where value scales differ widely.
-Reference and tolerances: attend_ref.attend (scales here are large enough that its
-absolute term of 2^-25 has no part)."""
+"""Attention over the paged 8-bit cache where value scales differ widely: blocks
+that no row sees, rows beside louder rows, and rows whose softmax lies in quiet
+blocks. Reference and tolerances: attend_ref.attend (scales here are large enough
+that its absolute term of 2^-25 has no part)."""
 import math
 
 import pytest
@@ -9,7 +10,7 @@ import torch
 import attend_ref as ref
 import fp8_mqa_logits_amd as mqa
 from gpu_helpers import say
-from test_gpu_attend import layout, problem
+from test_gpu_attend import layout, lists, problem
 
 pytestmark = pytest.mark.gpu
 BF16, FP16 = torch.bfloat16, torch.float16
@@ -68,6 +69,27 @@ def test_blocks_between_the_rows_ranges_may_hold_anything(R, Hq, room, codes, dt
                 assert torch.equal(out, want) and torch.equal(lse, want_lse)
 
 
+@pytest.mark.parametrize("first,codes", [("quiet", "e4m3"), ("loud", "int8")])
+@pytest.mark.parametrize("apart", [12, 30, 60])
+@pytest.mark.parametrize("room", [1, 4096])
+@pytest.mark.parametrize("R,Hq", TILES)
+def test_rows_beside_louder_rows(R, Hq, room, codes, apart, first):
+    # two packed requests in a tile, the values of one 2^apart times the other's
+    say(f"case: beside louder rows {R} {Hq} {room} {codes} {apart} {first}")
+    pool, table, q, starts, ends = problem([LENGTH], R, Hq, 2, 128, P, B, BF16, codes, "full",
+                                           extra=room)
+    for pos in range(0, LENGTH, B):
+        if (pos < 320) == (first == "loud"):
+            pool.scales[int(table[0, pos // P]), 1, :, pos % P // B] *= 2.0 ** apart
+    early = torch.arange(R) < R // 2
+    starts, ends = torch.where(early, 0, 320).int(), torch.where(early, 320, LENGTH).int()
+    want, lse, tol, tol_lse = ref.attend(pool, q, table[:, :-(-LENGTH // P)], starts, ends)
+    out, got_lse = mqa.mqa_attend_paged(layout(pool), q.cuda(), pool.bytes().cuda(), table.cuda(),
+                                        starts.cuda(), ends.cuda(), return_lse=True)
+    assert ref.differs(out, want, tol) == 0
+    assert ref.differs(got_lse, lse, tol_lse) == 0
+
+
 def quiet_weight(pool, table, loud, ratio):
     """Blocks of the positions in `loud` get keys of the lowest code (scores far
     below the others' for positive queries) and values 2^ratio louder."""
@@ -76,6 +98,35 @@ def quiet_weight(pool, table, loud, ratio):
         pool.codes[page, 0, :, pos % P:pos % P + B] = 0xFE if pool.kind == "e4m3" else 0x81
         pool.scales[page, 0, :, b] = 1.0 / 64 if pool.kind == "e4m3" else 1.0 / 18
         pool.scales[page, 1, :, b] *= 2.0 ** ratio
+
+
+@pytest.mark.parametrize("where", ["before", "after", "between"])
+@pytest.mark.parametrize("ratio,codes", [(30, "e4m3"), (60, "e4m3"), (34, "int8")])
+@pytest.mark.parametrize("room", [1, 4096])
+@pytest.mark.parametrize("R,Hq", [(1, 8)] + TILES)
+def test_softmax_in_quiet_blocks(R, Hq, room, codes, ratio, where):
+    # every row sees blocks 2^ratio louder than those that hold its softmax
+    say(f"case: quiet blocks {R} {Hq} {room} {codes} {ratio} {where}")
+    pool, table, q, starts, ends = problem([LENGTH], R, Hq, 2, 128, P, B, BF16, codes, "full",
+                                           extra=room)
+    every = range(0, LENGTH, B)
+    loud = {"before": every[:22], "after": every[22:], "between": every[1::2]}[where]
+    quiet_weight(pool, table, loud, ratio)
+    q = (q.float().abs() + 1.0).to(BF16)
+    for p in set(every) - set(loud):  # scores of the others around 0
+        pool.scales[int(table[0, p // P]), 0, :, p % P // B] *= 2.0 ** -8
+    L, exact_table = layout(pool), table[:, :-(-LENGTH // P)]
+    want, lse, tol, tol_lse = ref.attend(pool, q, exact_table, starts, ends)
+    out, got_lse = mqa.mqa_attend_paged(L, q.cuda(), pool.bytes().cuda(), table.cuda(),
+                                        starts.cuda(), ends.cuda(), return_lse=True)
+    assert ref.differs(out, want, tol) == 0
+    assert ref.differs(got_lse, lse, tol_lse) == 0
+    idx = lists(starts, ends, 512, 7)
+    want, lse, tol, tol_lse = ref.attend(pool, q, exact_table, starts, ends, indices=idx)
+    out, got_lse = mqa.mqa_attend_topk(L, q.cuda(), pool.bytes().cuda(), table.cuda(), idx.cuda(),
+                                       starts.cuda(), ends.cuda(), return_lse=True)
+    assert ref.differs(out, want, tol) == 0
+    assert ref.differs(got_lse, lse, tol_lse) == 0
 
 
 @pytest.mark.parametrize("ratio", [20, 26, 40])
@@ -100,3 +151,26 @@ def test_louder_tile_without_weight_after_a_tile_with_all_of_it(R, Hq, codes, ti
                                         starts.cuda(), ends.cuda(), return_lse=True)
     assert ref.differs(out, want, tol) == 0
     assert ref.differs(got_lse, lse, tol_lse) == 0
+
+
+@pytest.mark.parametrize("where", ["first", "last"])
+@pytest.mark.parametrize("codes,silent", [("e4m3", 0.0), ("int8", 2.0 ** -126)])
+@pytest.mark.parametrize("room", [1, 4096])
+@pytest.mark.parametrize("R,Hq", [(1, 8)] + TILES)
+def test_blocks_without_values_count_in_the_softmax(R, Hq, room, codes, silent, where):
+    # half of the blocks have value scales of 0, or the least that append writes
+    say(f"case: silent blocks {R} {Hq} {room} {codes} {where}")
+    pool, table, q, starts, ends = problem([LENGTH], R, Hq, 2, 128, P, B, BF16, codes, "full",
+                                           extra=room)
+    for pos in range(0, LENGTH, B):
+        if (pos < 352) == (where == "first"):
+            pool.scales[int(table[0, pos // P]), 1, :, pos % P // B] = silent
+    exact_table = table[:, :-(-LENGTH // P)]
+    for idx in (None, lists(starts, ends, 512, 7)):
+        want, lse, tol, tol_lse = ref.attend(pool, q, exact_table, starts, ends, indices=idx)
+        args = [layout(pool), q.cuda(), pool.bytes().cuda(), table.cuda()]
+        args += [] if idx is None else [idx.cuda()]
+        call = mqa.mqa_attend_paged if idx is None else mqa.mqa_attend_topk
+        out, got_lse = call(*args, starts.cuda(), ends.cuda(), return_lse=True)
+        assert ref.differs(out, want, tol) == 0
+        assert ref.differs(got_lse, lse, tol_lse) == 0

@@ -16,10 +16,10 @@ import torch
 CODES = {"e4m3": 0, "int8": 1}
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 MAX_LIST = 1 << 16
-NO_WORKSPACE = 256  # workspace_size_attend of a call that needs none
+NO_WORKSPACE = 256  # workspace_size_attend_call of a call that needs none
 
 EXPORTS = ("mqa_kv_page_bytes", "mqa_kv_append", "mqa_kv_read", "workspace_size_attend",
-           "mqa_attend_paged", "mqa_attend_topk")
+           "workspace_size_attend_call", "mqa_attend_paged", "mqa_attend_topk")
 
 
 class _Cache(ctypes.Structure):
@@ -50,6 +50,8 @@ def _load() -> ctypes.CDLL:
         lib.mqa_kv_read.restype = I
         lib.workspace_size_attend.argtypes = [I, I, I, I, I, I, I]
         lib.workspace_size_attend.restype = SZ
+        lib.workspace_size_attend_call.argtypes = [I, I, I, I, I, I, I, I]
+        lib.workspace_size_attend_call.restype = SZ
         lib.mqa_attend_paged.argtypes = [C, P, I64, I64, I, P, P, P, P, I, I, I, F, P, SZ, P]
         lib.mqa_attend_paged.restype = I
         lib.mqa_attend_topk.argtypes = [C, P, I64, I64, I, P, I, P, P, P, P, I, I, I, F, P, SZ, P]
@@ -254,8 +256,9 @@ def mqa_kv_read(layout: KVLayout, cache, page_table, starts, counts, rows_per_re
 
 def workspace_size_attend(requests: int, rows_per_request: int, heads: int, layout: KVLayout,
                           positions: int, device: int | None = None) -> int:
-    """Bytes of workspace an attention call needs: positions is table_stride *
-    page_size for mqa_attend_paged, the list's width for mqa_attend_topk."""
+    """Bytes of workspace that suffice for every attention call of up to so many
+    requests, rows of each and positions (table_stride * page_size for
+    mqa_attend_paged, the list's width for mqa_attend_topk)."""
     if device is None:
         device = torch.cuda.current_device()
     return int(_load().workspace_size_attend(int(requests), int(rows_per_request), int(heads),
@@ -296,8 +299,9 @@ def _attend(layout, q, cache, page_table, indices, starts, ends, scale, out, lse
         elif return_lse:
             lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
         if workspace is None:
-            n = lib.workspace_size_attend(requests, R, heads, layout.kv_heads, layout.head_dim,
-                                          positions, dev.index)
+            n = lib.workspace_size_attend_call(requests, R, heads, layout.kv_heads,
+                                               layout.head_dim, positions,
+                                               int(indices is not None), dev.index)
             if n > NO_WORKSPACE:
                 workspace = torch.empty(n, dtype=torch.uint8, device=dev)
         else:

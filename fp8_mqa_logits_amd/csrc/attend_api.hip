@@ -73,6 +73,30 @@ struct Plan {
   size_t ml, o, total;  // workspace offsets
 };
 
+constexpr int kMostRounds = 4;  // of resident workgroups, where keys are split
+
+// Workgroups that the device holds at once, by their registers.
+int64_t resident(int cols, int head_dim, bool list, int cus) {
+  const int held = list ? 2 : cols == 16 ? 4 : cols == 32 ? (head_dim == 64 ? 4 : 2)
+                                                       : cols == 128 ? 2 : 1;
+  return (int64_t)held * cus;
+}
+
+// The widest tile for so many columns.
+int widest(int columns, bool list) {
+  int cols = 16;
+  while (cols < columns && cols < (list ? 64 : 256)) cols *= 2;
+  return cols;
+}
+
+// Workspace offsets for so many columns of parts.
+void lay_out(Plan& a, int64_t slots, int head_dim) {
+  a.ml = 0;
+  a.o = (size_t)((slots * 8 + 255) / 256 * 256);
+  a.total = a.o + (size_t)slots * head_dim * 4;
+  if (a.total == 0) a.total = kNoWorkspace;
+}
+
 // Tiles: the widest whose workgroups, with 512 keys each at least, give every
 // compute unit one, else the narrowest (333 rows of 12 heads, each its own key
 // head, over a window of 83: 6 us on 16 columns, 20 on 256 with the keys split).
@@ -87,32 +111,55 @@ Plan plan(int requests, int R, int heads, int kv_heads, int head_dim, int positi
   Plan a{};
   const int group = heads / kv_heads, columns = list ? group : R * group;
   const int64_t units = (int64_t)(list ? requests * R : requests) * kv_heads;
-  a.cols = 16;
-  while (a.cols < columns && a.cols < (list ? 64 : 256)) a.cols *= 2;
+  a.cols = widest(columns, list);
   auto items = [&]() { return units * ((columns + a.cols - 1) / a.cols); };
   const int64_t most = positions < 1024 ? 1 : positions / 512;
   while (!list && a.cols > 16 && items() * most < cus) a.cols /= 2;
   a.tiles = (columns + a.cols - 1) / a.cols;
-  // workgroups that a compute unit holds at once, by their registers
-  const bool wide = a.cols > 64;
-  const int held = list ? 2 : a.cols == 16 ? 4 : a.cols == 32 ? (head_dim == 64 ? 4 : 2)
-                                               : a.cols == 128 ? 2 : 1;
-  const int64_t resident = (int64_t)held * cus, n = items(), ends = wide ? 1024 : 512;
+  const int64_t room = resident(a.cols, head_dim, list, cus), n = items();
+  const int64_t ends = a.cols > 64 ? 1024 : 512;
   int64_t best = 0;
   for (int s = 1; s <= mqa::kMaxSplits && (s == 1 || s * 256 <= positions); ++s) {
-    const int64_t rounds = (n * s + resident - 1) / resident;
+    const int64_t rounds = (n * s + room - 1) / room;
     const int64_t cost = rounds * ((positions + s - 1) / s + ends) + (s > 1 ? 2 * ends : 0);
-    if (s > 1 && rounds > 4) break;
+    if (s > 1 && rounds > kMostRounds) break;
     if (s > 1 && cost >= best) continue;
     best = cost;
     a.splits = s;
   }
-  const int64_t slots = a.splits > 1 ? items() * a.splits * a.cols : 0;
-  a.ml = 0;
-  a.o = (size_t)((slots * 8 + 255) / 256 * 256);
-  a.total = a.o + (size_t)slots * head_dim * 4;
-  if (a.total == 0) a.total = kNoWorkspace;
+  lay_out(a, a.splits > 1 ? n * a.splits * a.cols : 0, head_dim);
   return a;
+}
+
+// Bytes that suffice for every plan of up to so many requests, rows of each and
+// positions: no plan has more parts than the positions allow, nor more than
+// kMostRounds rounds of workgroups.
+size_t most_workspace(int requests, int R, int heads, int kv_heads, int head_dim, int positions,
+                      bool list, int cus) {
+  const int group = heads / kv_heads, columns = list ? group : R * group;
+  const int64_t units = (int64_t)(list ? requests * R : requests) * kv_heads;
+  const int64_t splits = positions / 256 < mqa::kMaxSplits ? positions / 256 : mqa::kMaxSplits;
+  int64_t most = 0;
+  for (int cols = widest(columns, list); cols >= 16 && splits > 1; cols /= 2) {
+    const int64_t by_keys = units * ((columns + cols - 1) / cols) * splits;
+    const int64_t by_rounds = kMostRounds * resident(cols, head_dim, list, cus);
+    const int64_t slots = (by_keys < by_rounds ? by_keys : by_rounds) * cols;
+    most = slots > most ? slots : most;
+  }
+  Plan a{};
+  lay_out(a, most, head_dim);
+  return a.total;
+}
+
+// What either size function refuses.
+bool sizes_ok(int requests, int R, int heads, int kv_heads, int head_dim, int positions) {
+  return rows_ok(requests, R) && kv_heads >= 1 && heads >= kv_heads &&
+         heads <= MQA_MAX_ATTEND_HEADS && heads % kv_heads == 0 &&
+         (head_dim == 64 || head_dim == 128) && positions >= 1;
+}
+
+int at_most_keys(int64_t positions) {
+  return (int)(positions < MQA_MAX_KEYS ? positions : MQA_MAX_KEYS);
 }
 
 int move(const mqa_kv_cache* cache, KvMoveParams& p, int (*launch)(const KvMoveParams*, hipStream_t),
@@ -144,7 +191,7 @@ int attend(const mqa_kv_cache* cache, const void* q, int64_t q_row, int64_t q_he
                       indices != nullptr, cus);
   if (!workspace && a.total > kNoWorkspace) return MQA_ERR_NULL;
   if (workspace && workspace_bytes < a.total)
-    return mqa::workspace_failed("the workspace is smaller than workspace_size_attend()");
+    return mqa::workspace_failed("the workspace is smaller than workspace_size_attend_call()");
   AttendParams p{};
   p.c = kernel_cache(cache);
   p.q = q;
@@ -232,14 +279,24 @@ int mqa_kv_read(const mqa_kv_cache* cache, void* k, void* v, int dtype, const in
 
 size_t workspace_size_attend(int requests, int R, int heads, int kv_heads, int head_dim,
                              int positions, int device) {
-  if (!rows_ok(requests, R) || kv_heads < 1 || heads < kv_heads || heads > MQA_MAX_ATTEND_HEADS ||
-      heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128) || positions < 1 ||
-      !mqa::device_cus(device))
-    return 0;
+  if (!sizes_ok(requests, R, heads, kv_heads, head_dim, positions)) return 0;
   const int cus = mqa::device_cus(device);
-  const size_t range = plan(requests, R, heads, kv_heads, head_dim, positions, false, cus).total;
-  const size_t list = plan(requests, R, heads, kv_heads, head_dim, positions, true, cus).total;
+  if (!cus) return 0;
+  auto most = [&](bool list) {
+    return most_workspace(requests, R, heads, kv_heads, head_dim, at_most_keys(positions), list,
+                          cus);
+  };
+  const size_t range = most(false), list = most(true);
   return range > list ? range : list;
+}
+
+size_t workspace_size_attend_call(int requests, int R, int heads, int kv_heads, int head_dim,
+                                  int positions, int listed, int device) {
+  if (!sizes_ok(requests, R, heads, kv_heads, head_dim, positions)) return 0;
+  const int cus = mqa::device_cus(device);
+  if (!cus) return 0;
+  return plan(requests, R, heads, kv_heads, head_dim, at_most_keys(positions), listed != 0, cus)
+      .total;
 }
 
 int mqa_attend_paged(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
@@ -249,7 +306,7 @@ int mqa_attend_paged(const mqa_kv_cache* cache, const void* q, int64_t q_row_str
   const int64_t cap = cache ? (int64_t)cache->table_stride * cache->page_size : 0;
   return attend(cache, q, q_row_stride, q_head_stride, dtype, nullptr, 0, starts, ends, out, lse,
                 requests, R, heads, scale, workspace, workspace_bytes,
-                (int)(cap < MQA_MAX_KEYS ? cap : MQA_MAX_KEYS), stream);
+                at_most_keys(cap), stream);
 }
 
 int mqa_attend_topk(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,

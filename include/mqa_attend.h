@@ -98,14 +98,23 @@ int mqa_kv_read(const mqa_kv_cache* cache, void* k, void* v, int dtype, const in
                 const int32_t* counts, int requests, int R, void* stream);
 
 /*
- * Bytes of workspace an attention call needs on `device`: requests * R rows
- * of `heads` query heads; `positions` the most that a row may see
- * (mqa_attend_paged: table_stride * page_size; mqa_attend_topk: the list's
- * width). 256 where the call needs none (its workspace may then be NULL); 0 for
+ * Bytes of workspace on `device` that suffice for every attention call of up to
+ * `requests` requests, up to R rows of each and up to `positions` positions a row
+ * may see (mqa_attend_paged: table_stride * page_size; mqa_attend_topk: the list's
+ * width; MQA_MAX_KEYS where that is more), with `heads` query heads: what a caller
+ * allocates once, for its largest batch. 256 where no such call needs any; 0 for
  * sizes out of range or a device that is not gfx950.
  */
 size_t workspace_size_attend(int requests, int R, int heads, int kv_heads, int head_dim,
                              int positions, int device);
+
+/*
+ * Bytes that one call of exactly these sizes needs (listed: 0 mqa_attend_paged, 1
+ * mqa_attend_topk). Few rows need more than many, as their keys are split over
+ * more workgroups. 256 where it needs none (its workspace may then be NULL).
+ */
+size_t workspace_size_attend_call(int requests, int R, int heads, int kv_heads, int head_dim,
+                                  int positions, int listed, int device);
 
 /*
  * Attention of every row over its range: with h = query head / (heads /
@@ -122,9 +131,10 @@ size_t workspace_size_attend(int requests, int R, int heads, int kv_heads, int h
  *   heads     a multiple of kv_heads, at most MQA_MAX_ATTEND_HEADS
  *   scale     finite, >= 0
  *   requests * R <= MQA_MAX_ROWS
- *   workspace >= workspace_size_attend(requests, R, heads, kv_heads, head_dim,
- *             table_stride * page_size, device) bytes, 256-B aligned, owned by
- *             the call until the stream reaches its end; nothing needs clearing
+ *   workspace >= workspace_size_attend_call(requests, R, heads, kv_heads,
+ *             head_dim, table_stride * page_size, 0, device) bytes, 256-B aligned,
+ *             owned by the call until the stream reaches its end; nothing needs
+ *             clearing
  * Scores, softmax sums and the output's sums are held in fp32. Positions that
  * no row sees may hold anything (also NaN codes and NaN or infinite scales); a
  * table entry outside [0, num_pages) is clamped into it. Scales of seen
@@ -147,8 +157,8 @@ int mqa_attend_paged(const mqa_kv_cache* cache, const void* q, int64_t q_row_str
  * there twice counts twice.
  *   indices   [requests * R, width] int32, dense, 16-B aligned, width in [1,
  *             MQA_MAX_LIST]
- *   workspace >= workspace_size_attend(requests, R, heads, kv_heads, head_dim,
- *             width, device) bytes
+ *   workspace >= workspace_size_attend_call(requests, R, heads, kv_heads,
+ *             head_dim, width, 1, device) bytes
  */
 int mqa_attend_topk(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
                     int64_t q_head_stride, int dtype, const int32_t* indices, int width,

@@ -7,8 +7,10 @@ built, every entry point raises (there is no fallback).
 """
 from __future__ import annotations
 
+import collections
 import contextlib
 import ctypes
+import functools
 import math
 
 import torch
@@ -60,36 +62,33 @@ def _load() -> ctypes.CDLL:
     return _bound
 
 
-class KVLayout:
+@functools.lru_cache(maxsize=None)
+def _page_bytes(kv_heads: int, head_dim: int, page_size: int, block: int) -> int:
+    return int(_load().mqa_kv_page_bytes(kv_heads, head_dim, page_size, block))
+
+
+class KVLayout(collections.namedtuple("KVLayout", ("kv_heads", "head_dim", "page_size", "block",
+                                                   "codes"))):
     """What a page of the cache holds: kv_heads key heads and as many value
     heads of head_dim (64 or 128) 8-bit codes ("e4m3" or "int8") for
     page_size tokens, and an fp32 scale for each block of tokens and head
-    (page_size and block powers of two, 16 <= block <= page_size)."""
-    __slots__ = ("kv_heads", "head_dim", "page_size", "block", "codes", "_bytes")
+    (page_size and block powers of two, 16 <= block <= page_size). Immutable."""
+    __slots__ = ()
 
-    def __init__(self, kv_heads: int, head_dim: int, page_size: int = 64, block: int = 64,
-                 codes: str = "e4m3"):
+    def __new__(cls, kv_heads: int, head_dim: int, page_size: int = 64, block: int = 64,
+                codes: str = "e4m3"):
         if codes not in CODES:
             raise ValueError(f"codes: {codes!r} not in {tuple(CODES)}")
-        self.kv_heads, self.head_dim = int(kv_heads), int(head_dim)
-        self.page_size, self.block, self.codes = int(page_size), int(block), codes
-        self._bytes = 0
-
-    def __repr__(self):
-        return (f"KVLayout(kv_heads={self.kv_heads}, head_dim={self.head_dim}, "
-                f"page_size={self.page_size}, block={self.block}, codes={self.codes!r})")
+        return super().__new__(cls, int(kv_heads), int(head_dim), int(page_size), int(block), codes)
 
     @property
     def page_bytes(self) -> int:
         """Bytes of a page; raises for sizes that no page can have."""
-        if not self._bytes:
-            n = int(_load().mqa_kv_page_bytes(self.kv_heads, self.head_dim, self.page_size,
-                                              self.block))
-            if n == 0:
-                raise ValueError(f"{self}: head_dim must be 64 or 128, page_size and block powers "
-                                 "of two, 16 <= block <= page_size <= 65536, a page below 2 GiB")
-            self._bytes = n
-        return self._bytes
+        n = _page_bytes(self.kv_heads, self.head_dim, self.page_size, self.block)
+        if n == 0:
+            raise ValueError(f"{self}: head_dim must be 64 or 128, page_size and block powers "
+                             "of two, 16 <= block <= page_size <= 65536, a page below 2 GiB")
+        return n
 
     def alloc(self, num_pages: int, device="cuda") -> torch.Tensor:
         """A zeroed pool of pages [num_pages, page_bytes] uint8."""

@@ -145,3 +145,16 @@ def test_no_device_is_an_error_not_a_fallback():
         mqa.mqa_attend_paged(mqa.KVLayout(2, 128), torch.zeros(1, 8, 128, dtype=torch.bfloat16),
                              mqa.KVLayout(2, 128).alloc(2, "cpu"), torch.zeros(1, 1, dtype=torch.int32),
                              torch.zeros(1, dtype=torch.int32), torch.ones(1, dtype=torch.int32))
+
+
+def test_a_layout_s_sizes_stay_those_of_its_page():
+    # a cache is checked against the layout's page: sizes that change after that
+    # would let a call past it into memory that is not the cache's
+    L = mqa.KVLayout(2, 64, 16, 16)
+    assert L.page_bytes == 2 * 2 * (16 * 64 + 4) + 112
+    for field, value in (("kv_heads", 8), ("head_dim", 128), ("page_size", 64), ("block", 32),
+                         ("codes", "int8")):
+        with pytest.raises(AttributeError):
+            setattr(L, field, value)
+    assert mqa.KVLayout(2, 128, 16, 16).page_bytes == 2 * 2 * (16 * 128 + 4) + 112
+    assert repr(L) == "KVLayout(kv_heads=2, head_dim=64, page_size=16, block=16, codes='e4m3')"

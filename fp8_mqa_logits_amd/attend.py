@@ -119,7 +119,8 @@ def _dense(t, name: str, dtype, shape: tuple, device):
 
 def _heads(t, name: str, dtype, rows: int, heads: int | None, dim: int, device):
     """[rows, heads, dim] with a dense last axis; any row and head stride.
-    Returns the shape's heads and the strides."""
+    Returns the shape's heads and the strides (0 for an axis of one element, whose
+    stride torch leaves as it comes)."""
     _on(t, name, dtype, device)
     shape, stride = t.shape, t.stride()
     if len(shape) != 3 or shape[0] != rows or shape[2] != dim or \
@@ -128,7 +129,7 @@ def _heads(t, name: str, dtype, rows: int, heads: int | None, dim: int, device):
                          f"({rows}, {'heads' if heads is None else heads}, {dim})")
     if stride[2] != 1:
         raise ValueError(f"{name} must have a dense last axis")
-    return shape[1], stride[0], stride[1]
+    return shape[1], stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0
 
 
 def _cache(layout: KVLayout, cache, page_table):

@@ -472,3 +472,21 @@ def test_binding_refusals():
                             starts, ends)
     with pytest.raises(TypeError):
         mqa.mqa_attend_topk(L, q, cache, table, None, starts, ends)
+
+
+def test_strides_of_axes_of_one_element_do_not_matter():
+    # one row of a projection whose width is no multiple of 8, one key head
+    say("case: strides of single rows and heads")
+    pool, table, q, starts, ends = problem([300], 1, 8, 1, 128, 32, 32, BF16, "e4m3")
+    want, _, tol, _ = ref.attend(pool, q, table, starts, ends)
+    args = (pool.bytes().cuda(), table.cuda(), starts.cuda(), ends.cuda())
+    row = torch.empty(3 * 1037, dtype=BF16, device="cuda").as_strided((1, 8, 128), (1037, 128, 1))
+    row.copy_(q)
+    assert ref.differs(mqa.mqa_attend_paged(layout(pool), row, *args), want, tol) == 0
+    L, cache = layout(pool), args[0]
+    k = torch.empty(4000, dtype=BF16, device="cuda").as_strided((1, 1, 128), (1037, 131, 1))
+    k.copy_(torch.randn(1, 1, 128))
+    at = torch.tensor([299], dtype=torch.int32, device="cuda")
+    mqa.mqa_kv_append(L, k, k, cache, args[1], at)
+    got, _ = mqa.mqa_kv_read(L, cache, args[1], at, None, 1)
+    assert float((got - k).abs().max()) <= 2.0 ** -4 * float(k.abs().max())

@@ -202,7 +202,9 @@ def mqa_kv_append(layout: KVLayout, k, v, cache, page_table, starts, counts=None
     """Store new tokens: k and v [requests * R, kv_heads, head_dim] (bf16, fp16
     or fp32; any row and head strides), row i * R + t being token t of request
     i, go to its positions starts[i] + t for t < counts[i] (int32; None: R).
-    page_table [requests, table_stride] int32. Writes and returns cache."""
+    page_table [requests, table_stride] int32. The new tokens are the request's
+    last: what their last block held behind them is lost. Writes and returns
+    cache."""
     c, dev, requests = _cache(layout, cache, page_table)
     if not isinstance(k, torch.Tensor) or not isinstance(v, torch.Tensor):
         raise TypeError("k and v must be tensors")

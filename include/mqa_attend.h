@@ -81,7 +81,12 @@ size_t mqa_kv_page_bytes(int kv_heads, int head_dim, int page_size, int block);
  * again under the new one. Rounding is to nearest, ties to even. Powers of two
  * make x / scale exact, so that codes do not depend on how a GPU divides.
  * Infinities become the largest code, NaN code 0x7F (e4m3) or 0 (int8).
- * Requests must not share a page that they write to.
+ * Tokens come in the order of their positions: the new ones are the request's
+ * last, and what their last block held behind them (a longer draft that was taken
+ * back, a page's earlier use) stands for nothing afterwards -- its codes stay as
+ * they are, under a scale that may be another. To change tokens in the middle,
+ * store all from there on again. Requests must not share a page that they write
+ * to.
  */
 int mqa_kv_append(const mqa_kv_cache* cache, const void* k, int64_t k_row_stride,
                   int64_t k_head_stride, const void* v, int64_t v_row_stride,
@@ -91,8 +96,9 @@ int mqa_kv_append(const mqa_kv_cache* cache, const void* k, int64_t k_row_stride
 /*
  * Reads positions starts[i] .. starts[i] + count_i - 1 of each request back:
  * row i * R + t of k and v (dense [requests * R, kv_heads, head_dim] of
- * `dtype`, 16-B aligned) is position starts[i] + t, rounded once; rows at and
- * past count_i (counts NULL: R), outside [0, K) or without a page are zero.
+ * `dtype`, 16-B aligned) is position starts[i] + t: its code times its scale in
+ * fp32 (exact for append's scales), rounded to `dtype`; rows at and past count_i
+ * (counts NULL: R), outside [0, K) or without a page are zero.
  */
 int mqa_kv_read(const mqa_kv_cache* cache, void* k, void* v, int dtype, const int32_t* starts,
                 const int32_t* counts, int requests, int R, void* stream);
@@ -101,8 +107,8 @@ int mqa_kv_read(const mqa_kv_cache* cache, void* k, void* v, int dtype, const in
  * Bytes of workspace on `device` that suffice for every attention call of up to
  * `requests` requests, up to R rows of each and up to `positions` positions a row
  * may see (mqa_attend_paged: table_stride * page_size; mqa_attend_topk: the list's
- * width; MQA_MAX_KEYS where that is more), with `heads` query heads: what a caller
- * allocates once, for its largest batch. 256 where no such call needs any; 0 for
+ * width; more than MQA_MAX_KEYS count as that), with `heads` query heads: what a
+ * caller allocates once, for its largest batch. 256 where no such call needs any; 0 for
  * sizes out of range or a device that is not gfx950.
  */
 size_t workspace_size_attend(int requests, int R, int heads, int kv_heads, int head_dim,

@@ -174,3 +174,26 @@ def test_blocks_without_values_count_in_the_softmax(R, Hq, room, codes, silent, 
         out, got_lse = call(*args, starts.cuda(), ends.cuda(), return_lse=True)
         assert ref.differs(out, want, tol) == 0
         assert ref.differs(got_lse, lse, tol_lse) == 0
+
+
+@pytest.mark.parametrize("power", [-88, -60, 50, 94])
+@pytest.mark.parametrize("codes", ["e4m3", "int8"])
+@pytest.mark.parametrize("room", [1, 4096])
+@pytest.mark.parametrize("R,Hq", [(1, 8)] + TILES)
+def test_value_scales_of_any_size(R, Hq, room, codes, power):
+    # all values 2^power times as large: outputs too, at the same precision
+    say(f"case: value scales of 2^{power} {R} {Hq} {room} {codes}")
+    pool, table, q, starts, ends = problem([LENGTH], R, Hq, 2, 128, P, B, BF16, codes, extra=room)
+    exact_table = table[:, :-(-LENGTH // P)]
+    for idx in (None, lists(starts, ends, 512, 7)):
+        want, lse, tol, tol_lse = ref.attend(pool, q, exact_table, starts, ends, indices=idx)
+        big = ref.Pool(len(pool.codes), *pool.dims, codes, 1)
+        big.codes, big.scales = pool.codes, pool.scales.clone()
+        big.scales[:, 1] *= 2.0 ** power
+        args = [layout(big), q.cuda(), big.bytes().cuda(), table.cuda()]
+        args += [] if idx is None else [idx.cuda()]
+        call = mqa.mqa_attend_paged if idx is None else mqa.mqa_attend_topk
+        out, got_lse = call(*args, starts.cuda(), ends.cuda(), return_lse=True)
+        assert ref.differs(out.double() * 2.0 ** -power, want, tol) == 0
+        # (e lies 2^power off its usual place: 2^-24 of the exponent more in lse)
+        assert ref.differs(got_lse, lse, tol_lse + abs(power) * 2.0 ** -23) == 0

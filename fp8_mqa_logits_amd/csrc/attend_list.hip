@@ -15,12 +15,14 @@ namespace {
 // from LDS four times (4096 rows of 64 heads and 2048 positions, when they were
 // compared: 1.14 ms, 666 us, and 594 us for this).
 //
-// Bound by the gathered bytes: 64 x 2 rows of 2048 positions, 8 key heads of 4
-// query heads, take 93 us, 5.8 TB/s. So nearly with 64 query heads on one key
-// head, where each row gathers what others gather too, but from a cache larger
-// than an L2, and vector instructions (widening, exponentials) take 59% of the
-// cycles or more: 4096 rows of 2048 of 65536 positions 405 to 418 us, 5.1 to 5.3
-// TB/s of gathered codes, 660 to 680 TFLOP/s.
+// Bound by the gathered bytes where rows share little: 64 x 2 rows of 2048
+// positions, 8 key heads of 4 query heads, take 93 us, 5.8 TB/s. With 64 query heads
+// on one key head, 4096 rows of 2048 of 65536 positions take 411 to 421 us (eight
+// calls after start-up: 482 to 520), 650 to 670 TFLOP/s: of 2.1 GB of gathered codes
+// the L2s serve 92% of the requests and 0.23 GB come from beyond them, so that memory
+// is not the limit. Vector instructions (widening, which both waves of a pair do
+// for every code, and exponentials) take 59% of the cycles or more, the matrix unit
+// 26%, and two waves per SIMD overlap them in part.
 //
 // A step's tokens (slots in the pool) are found by lanes 0 .. 31, an entry
 // each, two steps ahead, and go to the other lanes by permutation; scales go

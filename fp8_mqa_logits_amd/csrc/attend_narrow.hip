@@ -29,12 +29,12 @@ namespace {
 //
 // Bound by the cache's bytes in long contexts: 32 requests x 131072 positions of
 // 2 key heads of 128 take 367 us, 5.86 TB/s; 48 uneven ones of up to 20011
-// positions 123 us, 4.35 TB/s, as the longest parts end last. Heads of 64 cost
+// positions 121 to 124 us, 4.4 TB/s, as the longest parts end last. Heads of 64 cost
 // as many instructions a key for half the bytes: 24 x 4 rows over up
-// to 9001 positions 38 us with the join, 3.6 TB/s.
+// to 9001 positions 36 to 38 us with the join, 3.6 TB/s.
 //
-// Waves per SIMD: as many as hold the sums. Four of (D, NT) = (64, 2) spill four
-// registers outside the loop; three, without them, take 40.4 us for those 38.
+// Waves per SIMD: as many as hold the sums. Four of (D, NT) = (64, 2) spill five
+// registers outside the loop; three, without them, took 40.4 us when four took 37.6.
 template <int T, int C, int D, int NT>
 __global__ __launch_bounds__(256, NT == 4 ? 1 : NT == 2 && D == 128 ? 2 : 4)
 void attend_narrow_kernel(AttendParams p) {

@@ -21,16 +21,17 @@ namespace {
 // LDS; its values follow during the second half and are first read after the
 // next barrier.
 //
-// 4096 rows of 32 heads over 49152 positions of 4 key heads: 3.04 to 3.09 ms, 1.02
-// to 1.04 PFLOP/s, 86 to 88% of what a large matrix product reaches here; two
-// requests of 1024 rows packed into 32768 positions of 8 key heads 570 us, 934
-// TFLOP/s. By the counters the matrix unit is busy 46% of the cycles, vector
-// instructions take 40% or more at four cycles each (exponentials need more), LDS
-// is active a third: two waves per SIMD overlap the first two only in part. 64
-// columns a wave would halve the LDS reads but leave one wave per SIMD (3.97 ms);
-// two groups of waves in turn on the matrix and the vector unit met at too many
-// barriers (4.46 ms). What the two waves per SIMD spill lies outside the plain
-// tiles' loop.
+// 4096 rows of 32 heads over 49152 positions of 4 key heads, on several cards: 2.84
+// to 2.95 ms in long runs, 1.07 to 1.11 PFLOP/s, 90 to 94% of what a large matrix
+// product reaches here (eight calls after start-up: 2.97 to 3.17); two requests of
+// 1024 rows packed into 32768 positions of 8 key heads 513 to 547 us, 0.97 to 1.04
+// PFLOP/s. By the counters the matrix unit is busy 51% of the cycles, vector
+// instructions take 44% or more at four cycles each (exponentials need more), LDS
+// is active 37%: two waves per SIMD overlap the first two only in part. When it
+// took 3.46 ms, 64 columns a wave, which halve the LDS reads but leave one wave per
+// SIMD, took 3.97, and two groups of waves in turn on the matrix and the vector
+// unit, which met at too many barriers, 4.46. What the two waves per SIMD spill lies
+// outside the plain tiles' loop, but for one reload a tile.
 template <int T, int C, int D, int W>
 __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) {
   constexpr int THREADS = 64 * W;
@@ -118,8 +119,9 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   auto v_d = [&](int r) { return piece(r) % (D / 4) * 4; };
   // What a wave takes lies in one group of 16 keys, so that its page, its
   // addresses (but for an offset that each lane keeps) and its scales are the
-  // wave's (3.08 ms, not 3.24, for those 4096 rows on one card). A group that no row sees is read from the nearest one that some row
-  // sees (masked later; no branch in the loop). Its table entry is loaded a tile
+  // wave's (3.08 ms, not 3.24, for those 4096 rows on one card). A group outside all
+  // rows' ranges is read from the nearest one inside, one between them as it stands
+  // (masked later; no branch in the loop). Its table entry is loaded a tile
   // before its use, and only looked at then, by a vector load: a scalar one would
   // have every LDS read in flight waited for.
   static_assert(64 / (D / KB) == 64 / (D / 4) * VK && 64 / (D / KB) <= 16);

@@ -213,3 +213,49 @@ def test_binding_refusals():
     with pytest.raises(mqa.MQAError) as e:
         mqa.mqa_kv_append(L, k[:0], k[:0], cache, table, z)
     assert e.value.code in (1, 3)  # no rows: also no memory
+
+
+@pytest.mark.parametrize("R,Hq", [(1, 8), (3, 32), (40, 16)])
+@pytest.mark.parametrize("codes", ["e4m3", "int8"])
+def test_a_captured_step_stores_and_then_reads_what_it_stored(R, Hq, codes):
+    # append, attention over the range and over a list, and read back in one graph,
+    # replayed as the requests grow; every replay against the eager calls
+    say(f"case: captured step {R} {Hq} {codes}")
+    L = mqa.KVLayout(2, 128, 32, 16, codes)
+    table, pages = ref.make_table([400, 300], 32, 2)
+    table = table.cuda()
+    caches = [torch.zeros(pages, L.page_bytes, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    k, v = (torch.zeros(2 * R, 2, 128, dtype=BF16, device="cuda") for _ in range(2))
+    q = torch.zeros(2 * R, Hq, 128, dtype=BF16, device="cuda")
+    first = torch.zeros(2, dtype=torch.int32, device="cuda")
+    starts = torch.zeros(2 * R, dtype=torch.int32, device="cuda")
+    ends = torch.zeros_like(starts)
+    idx = torch.arange(64, dtype=torch.int32, device="cuda").repeat(2 * R, 1)
+
+    def step(cache):
+        mqa.mqa_kv_append(L, k, v, cache, table, first)
+        out = [mqa.mqa_attend_paged(L, q, cache, table, starts, ends),
+               mqa.mqa_attend_topk(L, q, cache, table, idx, starts, ends)]
+        return out + list(mqa.mqa_kv_read(L, cache, table, first, None, R))
+
+    step(caches[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(caches[0])
+    for i in range(6):
+        first.copy_(torch.tensor([i * R, 37 + i * R], dtype=torch.int32))
+        for x in (k, v, q):
+            x.copy_(torch.randn(x.shape, generator=g, device="cuda") * 2.0 ** (i % 3))
+        ends.copy_((first[:, None] + 1 + torch.arange(R, device="cuda")).flatten())
+        starts.copy_((ends - 70).clamp(min=0))
+        for o in got:
+            o.zero_()
+        graph.replay()
+        want = step(caches[1])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got)), i
+        if i == 0:  # (the call before the capture stored zeros into the first one)
+            caches[0].copy_(caches[1])
+        assert torch.equal(*caches)

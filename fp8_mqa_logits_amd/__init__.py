@@ -645,6 +645,6 @@ def read_stats(workspace: torch.Tensor) -> dict:
             "rows_block_scan": int(h[32])}
 
 
-from .attend import (KVLayout, mqa_attend_paged, mqa_attend_topk, mqa_kv_append,  # noqa: E402
-                     mqa_kv_read, workspace_size_attend)
+from .attend import (KVLayout, mqa_attend_paged, mqa_attend_topk, mqa_attend_tree,  # noqa: E402
+                     mqa_attend_window, mqa_kv_append, mqa_kv_read, workspace_size_attend)
 from .attend import EXPORTS as ATTEND_EXPORTS  # noqa: E402

@@ -1,5 +1,6 @@
 """Python binding of the paged 8-bit key/value cache: storing tokens, reading
-them back, and attention over ranges or listed positions of the cache.
+them back, and attention over ranges of the cache, through sliding windows with
+sinks, over trees of drafted tokens and over listed positions.
 
 Argument marshalling only, as in the package's other entry points; the C ABI
 and its contract are declared in include/mqa_attend.h. If the library is not
@@ -21,7 +22,8 @@ MAX_LIST = 1 << 16
 NO_WORKSPACE = 256  # workspace_size_attend_call of a call that needs none
 
 EXPORTS = ("mqa_kv_page_bytes", "mqa_kv_append", "mqa_kv_read", "workspace_size_attend",
-           "workspace_size_attend_call", "mqa_attend_paged", "mqa_attend_topk")
+           "workspace_size_attend_call", "mqa_attend_paged", "mqa_attend_topk",
+           "mqa_attend_window", "mqa_attend_tree")
 
 
 class _Cache(ctypes.Structure):
@@ -58,6 +60,10 @@ def _load() -> ctypes.CDLL:
         lib.mqa_attend_paged.restype = I
         lib.mqa_attend_topk.argtypes = [C, P, I64, I64, I, P, I, P, P, P, P, I, I, I, F, P, SZ, P]
         lib.mqa_attend_topk.restype = I
+        lib.mqa_attend_window.argtypes = [C, P, I64, I64, I, P, P, I, I, P, P, I, I, I, F, P, SZ, P]
+        lib.mqa_attend_window.restype = I
+        lib.mqa_attend_tree.argtypes = [C, P, I64, I64, I, P, P, P, I, P, P, I, I, I, F, P, SZ, P]
+        lib.mqa_attend_tree.restype = I
         _bound = lib
     return _bound
 
@@ -269,7 +275,7 @@ def workspace_size_attend(requests: int, rows_per_request: int, heads: int, layo
 
 
 def _attend(layout, q, cache, page_table, indices, starts, ends, scale, out, lse, return_lse,
-            workspace, stream, where):
+            workspace, stream, where, window=None, mask=None):
     c, dev, requests = _cache(layout, cache, page_table)
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a tensor")
@@ -282,6 +288,16 @@ def _attend(layout, q, cache, page_table, indices, starts, ends, scale, out, lse
     _dense(ends, "ends", torch.int32, (rows,), dev)
     if indices is None:
         positions = min(c.table_stride * c.page_size, 1 << 20)
+        if window is not None:
+            for name, n in zip(("window", "sinks"), window):
+                if not 0 <= n < 1 << 31:
+                    raise ValueError(f"{name}: {n} out of range")
+            positions = min(positions, max(window[0], 1) + window[1] + R - 1)
+        elif mask is not None:
+            if not isinstance(mask, torch.Tensor) or mask.dim() != 2:
+                raise ValueError("mask must be a tensor [rows, words]")
+            words = mask.shape[1]
+            _dense(mask, "mask", torch.int32, (rows, words), dev)
     else:
         if not isinstance(indices, torch.Tensor) or indices.dim() != 2:
             raise ValueError("indices must be a tensor [rows, width]")
@@ -311,14 +327,18 @@ def _attend(layout, q, cache, page_table, indices, starts, ends, scale, out, lse
             if not workspace.is_contiguous():
                 raise ValueError("workspace must be contiguous")
         head = (c, q.data_ptr(), q_row, q_head, DTYPES[q.dtype])
-        tail = (starts.data_ptr(), ends.data_ptr(), out.data_ptr(),
-                None if lse is None else lse.data_ptr(), requests, R, heads, float(scale),
-                None if workspace is None else workspace.data_ptr(),
+        ranges = (starts.data_ptr(), ends.data_ptr())
+        tail = (out.data_ptr(), None if lse is None else lse.data_ptr(), requests, R, heads,
+                float(scale), None if workspace is None else workspace.data_ptr(),
                 0 if workspace is None else workspace.numel(), s)
-        if indices is None:
-            rc = lib.mqa_attend_paged(*head, *tail)
+        if indices is not None:
+            rc = lib.mqa_attend_topk(*head, indices.data_ptr(), positions, *ranges, *tail)
+        elif window is not None:
+            rc = lib.mqa_attend_window(*head, *ranges, *window, *tail)
+        elif mask is not None:
+            rc = lib.mqa_attend_tree(*head, *ranges, mask.data_ptr(), words, *tail)
         else:
-            rc = lib.mqa_attend_topk(*head, indices.data_ptr(), positions, *tail)
+            rc = lib.mqa_attend_paged(*head, *ranges, *tail)
     _raise(rc, where)
     return (out, lse) if return_lse else out
 
@@ -347,3 +367,27 @@ def mqa_attend_topk(layout: KVLayout, q, cache, page_table, indices, starts, end
         raise TypeError("indices must be a tensor")
     return _attend(layout, q, cache, page_table, indices, starts, ends, scale, out, lse,
                    return_lse, workspace, stream, "mqa_attend_topk")
+
+
+def mqa_attend_window(layout: KVLayout, q, cache, page_table, starts, ends, window: int,
+                      sinks: int = 0, scale=None, out=None, lse=None, return_lse: bool = False,
+                      workspace=None, stream=None):
+    """Attention of every row over the last `window` (at least 1) positions of its
+    range [starts, ends) and the first `sinks` of it, each once. Pages that hold
+    none of them may be in other use. Other arguments and results as
+    mqa_attend_paged."""
+    return _attend(layout, q, cache, page_table, None, starts, ends, scale, out, lse, return_lse,
+                   workspace, stream, "mqa_attend_window", window=(int(window), int(sinks)))
+
+
+def mqa_attend_tree(layout: KVLayout, q, cache, page_table, starts, ends, mask, scale=None, out=None,
+                    lse=None, return_lse: bool = False, workspace=None, stream=None):
+    """Attention of drafted tokens that form trees: every row sees [starts, ends) of
+    its request and the positions ends + x whose bit x % 32 of mask[row, x // 32] is
+    set (mask [requests * R, words] int32, up to 32 words): itself and its
+    ancestors, where mqa_kv_append stored the drafts behind the context. Other
+    arguments and results as mqa_attend_paged."""
+    if mask is None:
+        raise TypeError("mask must be a tensor")
+    return _attend(layout, q, cache, page_table, None, starts, ends, scale, out, lse, return_lse,
+                   workspace, stream, "mqa_attend_tree", mask=mask)

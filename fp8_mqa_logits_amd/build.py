@@ -12,8 +12,10 @@ CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libmqa_topk.so")
 SOURCES = ["fused.hip", "dense.hip", "probe.hip", "api.hip", "kvcache.hip", "attend.hip",
-           "attend_narrow.hip", "attend_list.hip", "attend_wide.hip", "attend_api.hip"]
-HEADERS = ["common.h", "launch.h", "attend.h", "attend_tiles.h"]
+           "attend_narrow.hip", "attend_narrow_window.hip", "attend_narrow_tree.hip",
+           "attend_list.hip", "attend_wide.hip", "attend_wide_window.hip", "attend_wide_tree.hip",
+           "attend_api.hip"]
+HEADERS = ["common.h", "launch.h", "attend.h", "attend_tiles.h", "attend_narrow.h", "attend_wide.h"]
 
 
 def hipcc() -> str:

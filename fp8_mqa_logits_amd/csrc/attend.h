@@ -12,6 +12,9 @@ namespace mqa {
 enum { kE4m3 = 0, kInt8 = 1 };
 enum { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
 constexpr int kMaxSplits = 256;  // parts of a tile's keys, a multiple of 64
+// What a row sees: its range; the first and the last positions of it; its range and
+// some of the positions behind it.
+enum { kRange = 0, kWindow = 1, kTree = 2 };
 
 struct KvCache {
   uint8_t* pages;
@@ -45,6 +48,10 @@ struct AttendParams {
   const int32_t* ends;
   const int32_t* indices;  // [rows][width]; nullptr: every position of the range
   int width;
+  int sight;               // kRange, kWindow, kTree
+  int window, sinks;       // kWindow
+  const int32_t* mask;     // kTree: [rows][words]
+  int words;
   void* out;
   float* lse;
   int requests, R, rows, heads, group, dtype;

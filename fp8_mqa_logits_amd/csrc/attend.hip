@@ -97,12 +97,20 @@ extern "C" int mqa_attend_launch(const mqa::AttendParams* all, hipStream_t s) {
   const int64_t units = all->indices ? all->rows : all->requests;
   in_pieces(*all, units * all->tiles * all->c.kv_heads * all->splits,
             [&](const AttendParams& p, dim3 grid) {
+              auto ranges = [&](auto sight) {
+                if (p.cols <= 64)
+                  attend_narrow<sight.value>(p, grid, s);
+                else
+                  attend_wide<sight.value>(p, grid, s);
+              };
               if (p.indices)
                 attend_list(p, grid, s);
-              else if (p.cols <= 64)
-                attend_narrow(p, grid, s);
+              else if (p.sight == kWindow)
+                ranges(std::integral_constant<int, kWindow>{});
+              else if (p.sight == kTree)
+                ranges(std::integral_constant<int, kTree>{});
               else
-                attend_wide(p, grid, s);
+                ranges(std::integral_constant<int, kRange>{});
             });
   if (all->splits > 1) {
     const int64_t pairs = (int64_t)all->rows * all->heads;

@@ -162,6 +162,11 @@ int at_most_keys(int64_t positions) {
   return (int)(positions < MQA_MAX_KEYS ? positions : MQA_MAX_KEYS);
 }
 
+// Positions that a request's table has room for.
+int64_t positions_of(const mqa_kv_cache* cache) {
+  return cache ? (int64_t)cache->table_stride * cache->page_size : 0;
+}
+
 int move(const mqa_kv_cache* cache, KvMoveParams& p, int (*launch)(const KvMoveParams*, hipStream_t),
          void* stream) {
   if (!mqa::current_device_cus()) return MQA_ERR_DEVICE;
@@ -170,37 +175,37 @@ int move(const mqa_kv_cache* cache, KvMoveParams& p, int (*launch)(const KvMoveP
   return rc != 0 ? mqa::launch_failed(rc) : MQA_OK;
 }
 
+// What the entry points differ in: p holds what rows see (sight and its fields, or a
+// list), `good` says whether that is in range, and `positions` bounds what a row's tile
+// of keys may span.
 int attend(const mqa_kv_cache* cache, const void* q, int64_t q_row, int64_t q_head, int dtype,
-           const int32_t* indices, int width, const int32_t* starts, const int32_t* ends,
+           AttendParams p, bool good, const int32_t* starts, const int32_t* ends,
            void* out, float* lse, int requests, int R, int heads, float scale, void* workspace,
-           size_t workspace_bytes, int positions, void* stream) {
+           size_t workspace_bytes, int64_t positions, void* stream) {
   if (!cache || !q || !starts || !ends || !out) return MQA_ERR_NULL;
   const int rc = cache_pointers(cache);
   if (rc != MQA_OK) return rc;
   if (!aligned(q, 16) || q_row % 8 != 0 || q_head % 8 != 0 || !aligned(starts, 4) ||
-      !aligned(ends, 4) || !aligned(indices, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 256))
+      !aligned(ends, 4) || !aligned(p.indices, 16) || !aligned(p.mask, 4) || !aligned(out, 16) ||
+      !aligned(lse, 4) || !aligned(workspace, 256))
     return MQA_ERR_ALIGN;
   if (!cache_shape(cache) || !rows_ok(requests, R) || heads < 1 || heads > MQA_MAX_ATTEND_HEADS ||
       heads % cache->kv_heads != 0 || (dtype != MQA_BF16 && dtype != MQA_FP16) || q_row < 0 ||
-      q_head < 0 || !(scale >= 0.f) || scale > 3.4e38f ||
-      (indices && (width < 1 || width > MQA_MAX_LIST)))
+      q_head < 0 || !(scale >= 0.f) || scale > 3.4e38f || !good)
     return MQA_ERR_SHAPE;
   const int cus = mqa::current_device_cus();
   if (!cus) return MQA_ERR_DEVICE;
-  const Plan a = plan(requests, R, heads, cache->kv_heads, cache->head_dim, positions,
-                      indices != nullptr, cus);
+  const Plan a = plan(requests, R, heads, cache->kv_heads, cache->head_dim,
+                      at_most_keys(positions), p.indices != nullptr, cus);
   if (!workspace && a.total > kNoWorkspace) return MQA_ERR_NULL;
   if (workspace && workspace_bytes < a.total)
     return mqa::workspace_failed("the workspace is smaller than workspace_size_attend_call()");
-  AttendParams p{};
   p.c = kernel_cache(cache);
   p.q = q;
   p.q_row = q_row;
   p.q_head = q_head;
   p.starts = starts;
   p.ends = ends;
-  p.indices = indices;
-  p.width = width;
   p.out = out;
   p.lse = lse;
   p.requests = requests;
@@ -303,10 +308,9 @@ int mqa_attend_paged(const mqa_kv_cache* cache, const void* q, int64_t q_row_str
                      int64_t q_head_stride, int dtype, const int32_t* starts, const int32_t* ends,
                      void* out, float* lse, int requests, int R, int heads, float scale,
                      void* workspace, size_t workspace_bytes, void* stream) {
-  const int64_t cap = cache ? (int64_t)cache->table_stride * cache->page_size : 0;
-  return attend(cache, q, q_row_stride, q_head_stride, dtype, nullptr, 0, starts, ends, out, lse,
-                requests, R, heads, scale, workspace, workspace_bytes,
-                at_most_keys(cap), stream);
+  return attend(cache, q, q_row_stride, q_head_stride, dtype, AttendParams{}, true, starts, ends,
+                out, lse, requests, R, heads, scale, workspace, workspace_bytes, positions_of(cache),
+                stream);
 }
 
 int mqa_attend_topk(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
@@ -315,8 +319,41 @@ int mqa_attend_topk(const mqa_kv_cache* cache, const void* q, int64_t q_row_stri
                     int requests, int R, int heads, float scale, void* workspace,
                     size_t workspace_bytes, void* stream) {
   if (!indices) return MQA_ERR_NULL;
-  return attend(cache, q, q_row_stride, q_head_stride, dtype, indices, width, starts, ends, out,
-                lse, requests, R, heads, scale, workspace, workspace_bytes, width, stream);
+  AttendParams p{};
+  p.indices = indices;
+  p.width = width;
+  return attend(cache, q, q_row_stride, q_head_stride, dtype, p,
+                width >= 1 && width <= MQA_MAX_LIST, starts, ends, out, lse, requests, R, heads,
+                scale, workspace, workspace_bytes, width, stream);
+}
+
+int mqa_attend_window(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
+                      int64_t q_head_stride, int dtype, const int32_t* starts, const int32_t* ends,
+                      int window, int sinks, void* out, float* lse, int requests, int R, int heads,
+                      float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  AttendParams p{};
+  p.sight = mqa::kWindow;
+  p.window = window;
+  p.sinks = sinks;
+  const int64_t most = positions_of(cache), spanned = (int64_t)window + sinks + R - 1;
+  return attend(cache, q, q_row_stride, q_head_stride, dtype, p, window >= 1 && sinks >= 0, starts,
+                ends, out, lse, requests, R, heads, scale, workspace, workspace_bytes,
+                spanned < most ? spanned : most, stream);
+}
+
+int mqa_attend_tree(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
+                    int64_t q_head_stride, int dtype, const int32_t* starts, const int32_t* ends,
+                    const int32_t* mask, int words, void* out, float* lse, int requests, int R,
+                    int heads, float scale, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+  if (!mask) return MQA_ERR_NULL;
+  AttendParams p{};
+  p.sight = mqa::kTree;
+  p.mask = mask;
+  p.words = words;
+  return attend(cache, q, q_row_stride, q_head_stride, dtype, p,
+                words >= 1 && words <= MQA_MAX_DRAFT_WORDS, starts, ends, out, lse, requests, R,
+                heads, scale, workspace, workspace_bytes, positions_of(cache), stream);
 }
 
 }  // extern "C"

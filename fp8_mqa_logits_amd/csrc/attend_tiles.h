@@ -178,33 +178,170 @@ __device__ __forceinline__ float or_lowest(float x, uint32_t see) {
   return __uint_as_float((__float_as_uint(x) & see) | (~see & 0xFF800000u));
 }
 
-// The positions that some of `rows` rows from row_lo see, [lo, hi), and those
-// that all of them see, [in_lo, in_hi); rows that see nothing are left out. A
-// lane takes every step-th row from `first`; the result is the wave's.
-struct Span {
-  int lo, hi, in_lo, in_hi;
+// What a row sees (M: kRange, kWindow, kTree), by the range [s, e) that row_range
+// gives: all of it; its first p.sinks and its last p.window positions; all of it and
+// positions e + x for the set bits x of the row's mask, up to the table's end.
+__device__ __forceinline__ int sinks_end(const AttendParams& p, int s, int e) {
+  return e - s < p.sinks ? e : s + p.sinks;
+}
+__device__ __forceinline__ int window_start(const AttendParams& p, int s, int e) {
+  return e - s < p.window ? s : e - p.window;
+}
+
+// 32 bits of the row's mask from bit x on; none before its first and behind its last.
+__device__ __forceinline__ uint32_t mask_bits(const AttendParams& p, int row, int x) {
+  const int32_t* const at = p.mask + (int64_t)row * p.words;
+  const int word = x >> 5;
+  const uint32_t lo = (uint32_t)word < (uint32_t)p.words ? at[word] : 0;
+  const uint32_t hi = (uint32_t)(word + 1) < (uint32_t)p.words ? at[word + 1] : 0;
+  return (uint32_t)(((uint64_t)hi << 32 | lo) >> (x & 31));
+}
+
+// Bits of the positions pos .. pos + 31 that the row sees.
+template <int M>
+__device__ __forceinline__ uint32_t row_bits(const AttendParams& p, int row, int pos, int s, int e) {
+  uint32_t bits = seen_bits(pos, M == kWindow ? window_start(p, s, e) : s, e);
+  if constexpr (M == kWindow) bits |= seen_bits(pos, s, sinks_end(p, s, e));
+  if constexpr (M == kTree)
+    if (pos + 32 > e) bits |= mask_bits(p, row, pos - e) & seen_bits(pos, e, p.c.cap);
+  return bits;
+}
+
+// The lowest (-1: none) and the highest position behind e that the row's mask names.
+struct Drafts {
+  int lo, hi;
 };
+__device__ __forceinline__ Drafts drafts(const AttendParams& p, int row, int e) {
+  Drafts d{-1, -1};
+  for (int w = 0; w < p.words && e + 32 * w < p.c.cap; ++w) {
+    const uint32_t bits = mask_bits(p, row, 32 * w) & seen_bits(e + 32 * w, e, p.c.cap);
+    if (!bits) continue;
+    if (d.lo < 0) d.lo = e + 32 * w + __builtin_ctz(bits);
+    d.hi = e + 32 * w + 31 - __builtin_clz(bits);
+  }
+  return d;
+}
+
+template <int M>
+__device__ __forceinline__ bool sees_nothing(const AttendParams& p, int row, int s, int e) {
+  if constexpr (M == kTree)
+    if (s >= e) return drafts(p, row, e).lo < 0;
+  return s >= e;
+}
+
+// Of `rows` rows from row_lo, those that see nothing left out: the positions that some
+// of them see lie in [lo, hi), where kWindow: in [lo, hi) or among the sinks' [s_lo,
+// s_hi); those that all of them see hold [in_lo, in_hi). A lane takes every step-th row
+// from `first`; the result is the wave's.
+struct Span {
+  int lo, hi, in_lo, in_hi, s_lo, s_hi;
+};
+template <int M>
+__device__ __forceinline__ Span join(const Span& a, const Span& b) {
+  Span c{min(a.lo, b.lo), max(a.hi, b.hi), max(a.in_lo, b.in_lo), min(a.in_hi, b.in_hi), 0, 0};
+  if constexpr (M == kWindow) {
+    c.s_lo = min(a.s_lo, b.s_lo);
+    c.s_hi = max(a.s_hi, b.s_hi);
+  }
+  return c;
+}
+template <int M>
 __device__ __forceinline__ Span row_span(const AttendParams& p, int row_lo, int rows, int first,
                                          int step) {
-  Span a{p.c.cap, 0, 0, p.c.cap};
+  Span a{p.c.cap, 0, 0, p.c.cap, p.c.cap, 0};
   for (int r = first; r < rows; r += step) {
     int s, e;
     row_range(p, row_lo + r, s, e);
-    if (s < e) a = {min(a.lo, s), max(a.hi, e), max(a.in_lo, s), min(a.in_hi, e)};
+    Span b{s, e, s, e, p.c.cap, 0};
+    if constexpr (M == kTree) {
+      const Drafts d = drafts(p, row_lo + r, e);
+      if (s >= e) b.lo = d.lo < 0 ? p.c.cap : d.lo;
+      if (s >= e && d.lo < 0) continue;
+      if (d.hi >= 0) b.hi = d.hi + 1;
+    } else {
+      if (s >= e) continue;
+    }
+    if constexpr (M == kWindow) {
+      b.lo = b.in_lo = window_start(p, s, e);
+      if (p.sinks > 0 && s < b.lo) {
+        b.s_lo = s;
+        b.s_hi = sinks_end(p, s, e);
+      }
+    }
+    a = join<M>(a, b);
   }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) {
-    a.lo = min(a.lo, __shfl_xor(a.lo, o, 64));
-    a.hi = max(a.hi, __shfl_xor(a.hi, o, 64));
-    a.in_lo = max(a.in_lo, __shfl_xor(a.in_lo, o, 64));
-    a.in_hi = min(a.in_hi, __shfl_xor(a.in_hi, o, 64));
+    Span b{__shfl_xor(a.lo, o, 64), __shfl_xor(a.hi, o, 64), __shfl_xor(a.in_lo, o, 64),
+           __shfl_xor(a.in_hi, o, 64), 0, 0};
+    if constexpr (M == kWindow) {
+      b.s_lo = __shfl_xor(a.s_lo, o, 64);
+      b.s_hi = __shfl_xor(a.s_hi, o, 64);
+    }
+    a = join<M>(a, b);
   }
   return a;
 }
 __device__ __forceinline__ Span uniform(Span a) {
-  return {__builtin_amdgcn_readfirstlane(a.lo), __builtin_amdgcn_readfirstlane(a.hi),
-          __builtin_amdgcn_readfirstlane(a.in_lo), __builtin_amdgcn_readfirstlane(a.in_hi)};
+  return {__builtin_amdgcn_readfirstlane(a.lo),    __builtin_amdgcn_readfirstlane(a.hi),
+          __builtin_amdgcn_readfirstlane(a.in_lo), __builtin_amdgcn_readfirstlane(a.in_hi),
+          __builtin_amdgcn_readfirstlane(a.s_lo),  __builtin_amdgcn_readfirstlane(a.s_hi)};
 }
+
+// The keys that a tile of columns walks over, STEP at a time from a multiple of 16:
+// its span, and before it the sinks' (kWindow), where they do not meet.
+template <int M, int STEP>
+struct Walk {
+  Span span;
+  int first, steps;     // of all steps, where there are no sinks
+  int s_first, s_steps; // the sinks' steps come first
+  __device__ __forceinline__ explicit Walk(const Span& of) : span(of) {
+    s_first = s_steps = 0;
+    if constexpr (M == kWindow) {
+      if (span.s_hi > span.s_lo) {
+        span.s_lo = min(span.s_lo, span.lo);  // (a short row's window, before others' sinks)
+        s_first = span.s_lo & ~15;
+        s_steps = (span.s_hi - s_first + STEP - 1) / STEP;
+        // what windows see of the sinks' steps is walked over there
+        const int end = s_first + s_steps * STEP;
+        if (span.lo < end) {
+          span.s_hi = max(span.s_hi, min(span.hi, end));
+          span.lo = end;
+        }
+      } else {
+        span.s_lo = span.s_hi = 0;
+      }
+    }
+    first = span.lo & ~15;
+    steps = s_steps + (span.hi > span.lo ? (span.hi - first + STEP - 1) / STEP : 0);
+  }
+  // Position of step st's first key.
+  __device__ __forceinline__ int pos(int st) const {
+    if constexpr (M == kWindow)
+      return st < s_steps ? s_first + st * STEP : first + (st - s_steps) * STEP;
+    else
+      return first + st * STEP;
+  }
+  // Where the 16 keys from `at` keys into step st are read: those that lie outside what
+  // some row sees, from the nearest that does not.
+  __device__ __forceinline__ int read_pos(int st, int at) const {
+    if constexpr (M == kWindow)
+      if (st < s_steps || span.hi <= span.lo)
+        return min(max(pos(st) + at, span.s_lo), span.s_hi - 1) & ~15;
+    return min(max(pos(st) + at, span.lo), span.hi - 1) & ~15;
+  }
+  __device__ __forceinline__ bool inside(int at) const {  // every row sees keys at .. at + STEP - 1
+    return at >= span.in_lo && at + STEP <= span.in_hi;
+  }
+  __device__ __forceinline__ bool some(int at) const {  // position `at` is in what some rows see
+    return (at >= span.lo && at < span.hi) ||
+           (M == kWindow && at >= span.s_lo && at < span.s_hi);
+  }
+  __device__ __forceinline__ uint32_t some_bits(int at) const {
+    return seen_bits(at, span.lo, span.hi) |
+           (M == kWindow ? seen_bits(at, span.s_lo, span.s_hi) : 0u);
+  }
+};
 
 // The end of a workgroup whose waves hold O^T sums in v_mfma_f32_16x16x32's
 // layout: wave kb * HW + hw has 16 NT columns from 16 NT hw, over part kb of the
@@ -329,10 +466,12 @@ void dispatch(const AttendParams& p, F f) {
     of(std::integral_constant<int, kFp16>{});
 }
 
-// One launch of p.block0 .. each (attend_narrow.hip, attend_list.hip,
-// attend_wide.hip).
+// One launch of p.block0 .. each: tiles of up to 64 columns, lists, and tiles of 128
+// or 256 columns.
+template <int M>
 void attend_narrow(const AttendParams& p, dim3 grid, hipStream_t s);
 void attend_list(const AttendParams& p, dim3 grid, hipStream_t s);
+template <int M>
 void attend_wide(const AttendParams& p, dim3 grid, hipStream_t s);
 
 }  // namespace mqa

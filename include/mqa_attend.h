@@ -1,9 +1,10 @@
 /*
  * mqa_attend.h -- C ABI of the paged 8-bit key/value cache in libmqa_topk.so:
  * storing tokens (mqa_kv_append), reading them back (mqa_kv_read), attention
- * over each row's range of positions (mqa_attend_paged) and over each row's
- * listed positions (mqa_attend_topk, which takes the output of the
- * mqa_topk_* calls as it is).
+ * over each row's range of positions (mqa_attend_paged), through a sliding window
+ * with sinks (mqa_attend_window), over trees of drafted tokens (mqa_attend_tree)
+ * and over each row's listed positions (mqa_attend_topk, which takes the output of
+ * the mqa_topk_* calls as it is).
  *
  * The cache. A page holds page_size tokens of kv_heads key heads and as many
  * value heads of head_dim 8-bit codes:
@@ -46,6 +47,7 @@ extern "C" {
 
 #define MQA_MAX_ATTEND_HEADS 1024
 #define MQA_MAX_LIST (1 << 16) /* listed positions per row of mqa_attend_topk */
+#define MQA_MAX_DRAFT_WORDS 32  /* mask words per row of mqa_attend_tree */
 
 typedef struct mqa_kv_cache {
   void* pages;          /* first page, 16-B aligned */
@@ -171,6 +173,34 @@ int mqa_attend_topk(const mqa_kv_cache* cache, const void* q, int64_t q_row_stri
                     const int32_t* starts, const int32_t* ends, void* out, float* lse,
                     int requests, int R, int heads, float scale, void* workspace,
                     size_t workspace_bytes, void* stream);
+
+/*
+ * mqa_attend_paged through a sliding window: a row sees the last `window`
+ * positions of its range [s, e) and the first `sinks` of it, j with e - window <=
+ * j < e or s <= j < min(s + sinks, e), each once. Only these are read: pages that hold
+ * none of them may be in other use, their table entries anything.
+ *   window    >= 1; sinks >= 0
+ *   workspace >= workspace_size_attend_call(requests, R, heads, kv_heads, head_dim,
+ *             min(window + sinks + R - 1, table_stride * page_size), 0, device) bytes
+ */
+int mqa_attend_window(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
+                      int64_t q_head_stride, int dtype, const int32_t* starts, const int32_t* ends,
+                      int window, int sinks, void* out, float* lse, int requests, int R, int heads,
+                      float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mqa_attend_paged over a tree of drafted tokens, which stand in the cache behind
+ * the tokens that are settled: a row sees its range [s, e) and those positions e + x
+ * below K whose bit x % 32 of mask[r][x / 32] is set -- itself and its ancestors,
+ * where drafts are stored in any order.
+ *   mask      [requests * R, words] int32, dense, 4-B aligned, words in [1,
+ *             MQA_MAX_DRAFT_WORDS]
+ */
+int mqa_attend_tree(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
+                    int64_t q_head_stride, int dtype, const int32_t* starts, const int32_t* ends,
+                    const int32_t* mask, int words, void* out, float* lse, int requests, int R,
+                    int heads, float scale, void* workspace, size_t workspace_bytes,
+                    void* stream);
 
 #ifdef __cplusplus
 }

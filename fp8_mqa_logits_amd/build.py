@@ -14,7 +14,7 @@ LIB = os.path.join(LIB_DIR, "libmqa_topk.so")
 SOURCES = ["fused.hip", "dense.hip", "probe.hip", "api.hip", "kvcache.hip", "attend.hip",
            "attend_narrow.hip", "attend_narrow_window.hip", "attend_narrow_tree.hip",
            "attend_list.hip", "attend_wide.hip", "attend_wide_window.hip", "attend_wide_tree.hip",
-           "attend_api.hip"]
+           "attend_api.hip", "rotate.hip"]
 HEADERS = ["common.h", "launch.h", "attend.h", "attend_tiles.h", "attend_narrow.h", "attend_wide.h"]
 
 
@@ -40,7 +40,7 @@ def stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + \
-           [os.path.join(ROOT, "include", h) for h in ("mqa_topk.h", "mqa_attend.h")]
+           [os.path.join(ROOT, "include", h) for h in ("mqa_topk.h", "mqa_attend.h", "mqa_serve.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -2,12 +2,19 @@
 refused before any device memory is touched. No GPU needed (nothing here launches
 work; the addresses are never used)."""
 import ctypes
+import os
+import re
+import shutil
+import subprocess
 
 import pytest
 
+import fp8_mqa_logits_amd as mqa
 from fp8_mqa_logits_amd import attend as A
+from fp8_mqa_logits_amd import serve as S
 from test_attend_host import A16, MIS, WS, cache
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P = ctypes.c_void_p
 
 
@@ -66,3 +73,60 @@ def test_no_device_is_an_error_not_a_fallback():
     assert window() == 5
     assert window(window=(1 << 31) - 1, sinks=(1 << 31) - 1) == 5
     assert tree() == 5
+    assert rotate() == 5
+    assert rotate(k=None, kv_heads=0, rot=0, pos=0, f=0) == 5
+
+
+H = S._HeadRows
+
+
+def rotate(**kw):
+    a = dict(q=H(A16, 1024, 128), q_out=H(A16, 1024, 128), heads=8, k=H(A16, 256, 128),
+             k_out=H(A16, 256, 128), kv_heads=2, qw=A16, kw=A16, wt=0, pos=A16, f=A16, rot=128, pairs=0,
+             rows=4, D=128, dtype=0, norm=1, eps=1e-6)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return S._load().mqa_norm_rotate(a["q"], a["q_out"], a["heads"], a["k"], a["k_out"], a["kv_heads"],
+                                     P(a["qw"]), P(a["kw"]), a["wt"], P(a["pos"]), P(a["f"]), a["rot"],
+                                     a["pairs"], a["rows"], a["D"], a["dtype"], a["norm"], a["eps"], None)
+
+
+def test_norm_rotate_errors():
+    for name in ("q", "q_out", "k", "k_out"):
+        assert rotate(**{name: None}) == 1, name
+        assert rotate(**{name: H(0, 1024, 128)}) == 1, name
+        assert rotate(**{name: H(0x10008, 1024, 128)}) == 2, name
+        assert rotate(**{name: H(A16, 1020, 128)}) == 2, name
+        assert rotate(**{name: H(A16, 1024, 4)}) == 2, name
+        assert rotate(**{name: H(A16, -1024, 128)}) == 3, name
+    assert rotate(pos=0) == 1 and rotate(f=0) == 1
+    for kw in (dict(qw=0x10008), dict(kw=0x10008), dict(pos=0x10002), dict(f=0x10004)):
+        assert rotate(**kw) == 2, kw
+    for kw in (dict(rows=0), dict(rows=(1 << 20) + 1), dict(heads=0), dict(heads=1025), dict(kv_heads=-1),
+               dict(kv_heads=1025), dict(D=96), dict(D=512), dict(dtype=2), dict(wt=1), dict(rot=24),
+               dict(rot=144), dict(rot=-16), dict(eps=-1.0), dict(eps=float("nan")),
+               dict(eps=float("inf")), dict(q_out=H(A16, 0, 128)), dict(k_out=H(A16, 256, 0))):
+        assert rotate(**kw) == 3, kw
+
+
+def test_exports_match_the_header():
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "mqa_serve.h")).read(), flags=re.S)
+    names = set(re.findall(r"^[a-z_][a-z0-9_ ]*[ *]+(\w+)\(", text, flags=re.M))
+    assert names == set(mqa.SERVE_EXPORTS)
+    for n in names:
+        assert hasattr(S._load(), n), n
+
+
+def test_header_is_c_and_the_structure_is_the_bindings(tmp_path):
+    cc = shutil.which("gcc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    src = tmp_path / "t.c"
+    src.write_text('#include <stdio.h>\n#include "mqa_serve.h"\nint main(void) {'
+                   + "".join(f'printf("%zu ", offsetof(mqa_head_rows, {f}));' for f, _ in H._fields_)
+                   + 'printf("%zu", sizeof(mqa_head_rows)); return 0; }\n')
+    exe = tmp_path / "t"
+    subprocess.run([cc, "-std=c99", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(ROOT, "include"),
+                    str(src), "-o", str(exe)], check=True)
+    got = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()
+    assert [int(x) for x in got] == [getattr(H, f).offset for f, _ in H._fields_] + [ctypes.sizeof(H)]

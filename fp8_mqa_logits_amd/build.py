@@ -14,8 +14,10 @@ LIB = os.path.join(LIB_DIR, "libmqa_topk.so")
 SOURCES = ["fused.hip", "dense.hip", "probe.hip", "api.hip", "kvcache.hip", "attend.hip",
            "attend_narrow.hip", "attend_narrow_window.hip", "attend_narrow_tree.hip",
            "attend_list.hip", "attend_wide.hip", "attend_wide_window.hip", "attend_wide_tree.hip",
-           "attend_api.hip", "rotate.hip"]
-HEADERS = ["common.h", "launch.h", "attend.h", "attend_tiles.h", "attend_narrow.h", "attend_wide.h"]
+           "attend_api.hip", "rotate.hip", "weigh.hip", "evict.hip",
+           "serve_api.hip"]
+HEADERS = ["common.h", "launch.h", "attend.h", "attend_tiles.h", "attend_narrow.h", "attend_wide.h",
+           "cache_api.h", "kvcodes.h", "serve.h"]
 
 
 def hipcc() -> str:

@@ -1,0 +1,43 @@
+// Parameter blocks and launch entry points of weigh.hip and evict.hip.
+#pragma once
+
+#include "attend.h"
+
+namespace mqa {
+
+struct WeighParams {
+  AttendParams a;    // q, ranges, heads, scale; out and lists unused
+  const float* lse;  // [rows][heads]
+  float* weights;    // [requests][width]
+  int width;
+  int tiles;  // workgroups of a request
+};
+
+struct SelectParams {
+  const float* weights;  // [requests][width]
+  const int32_t* lengths;
+  int32_t* positions;  // [requests][keep]
+  int32_t* counts;
+  float* kept;  // [requests][width] or nullptr
+  int width, keep, sinks, recent, requests;
+};
+
+struct KeepParams {
+  KvCache c;
+  const int32_t* positions;  // [requests][width]
+  const int32_t* counts;
+  const int32_t* starts;  // nullptr: 0
+  int width, requests, blocks;  // blocks of a request that moved tokens can fall into
+  // moved blocks on their way: codes [item][B][head_dim], scales [item], item =
+  // ((request * blocks + block) * 2 + w) * kv_heads + head
+  uint8_t* codes;
+  float* scales;
+};
+
+}  // namespace mqa
+
+extern "C" {
+int mqa_kv_weigh_launch(const mqa::WeighParams* p, hipStream_t stream);
+int mqa_kv_select_launch(const mqa::SelectParams* p, hipStream_t stream);
+int mqa_kv_keep_launch(const mqa::KeepParams* p, hipStream_t stream);
+}

@@ -1,0 +1,149 @@
+// C ABI of eviction from the paged 8-bit cache: argument checks, workspace layout and
+// launches. The declarations and their contracts are in include/mqa_serve.h.
+#include <hip/hip_runtime.h>
+
+#include "cache_api.h"
+#include "launch.h"
+#include "mqa_serve.h"
+#include "serve.h"
+
+namespace {
+
+using namespace mqa;
+
+// Blocks that `width` tokens from any position on can fall into.
+int64_t blocks_of(int width, int block) {
+  return ((int64_t)block - 1 + width - 1) / block + 1;
+}
+
+struct KeepLayout {
+  size_t scales, total;
+};
+KeepLayout keep_layout(int requests, int width, int kv_heads, int head_dim, int block) {
+  const size_t items = (size_t)requests * blocks_of(width, block) * 2 * kv_heads;
+  KeepLayout a{};
+  a.scales = (items * block * head_dim + 255) / 256 * 256;
+  a.total = a.scales + (items * 4 + 255) / 256 * 256;
+  return a;
+}
+
+bool keep_sizes_ok(int requests, int width) {
+  return requests >= 1 && requests <= MQA_MAX_ROWS && width >= 1 && width <= MQA_MAX_KEYS &&
+         (int64_t)requests * width <= (int64_t)MQA_MAX_KEPT;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t workspace_size_weigh(int requests, int R, int heads, int kv_heads, int head_dim,
+                            int positions, int device) {
+  if (!rows_ok(requests, R) || kv_heads < 1 || heads < kv_heads || heads > MQA_MAX_ATTEND_HEADS ||
+      heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128) || positions < 1)
+    return 0;
+  return device_cus(device) ? kNoWorkspace : 0;
+}
+
+int mqa_kv_weigh(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
+                 int64_t q_head_stride, int dtype, const int32_t* starts, const int32_t* ends,
+                 const float* lse, float* weights, int width, int requests, int R, int heads,
+                 float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  (void)workspace_bytes;
+  if (!cache || !q || !starts || !ends || !lse || !weights) return MQA_ERR_NULL;
+  const int rc = cache_pointers(cache);
+  if (rc != MQA_OK) return rc;
+  if (!aligned(q, 16) || q_row_stride % 8 != 0 || q_head_stride % 8 != 0 || !aligned(starts, 4) ||
+      !aligned(ends, 4) || !aligned(lse, 4) || !aligned(weights, 4) || !aligned(workspace, 256))
+    return MQA_ERR_ALIGN;
+  if (!cache_shape(cache) || !rows_ok(requests, R) || heads < 1 || heads > MQA_MAX_ATTEND_HEADS ||
+      heads % cache->kv_heads != 0 || (dtype != MQA_BF16 && dtype != MQA_FP16) ||
+      q_row_stride < 0 || q_head_stride < 0 || !(scale >= 0.f) || scale > 3.4e38f || width < 1)
+    return MQA_ERR_SHAPE;
+  const int cus = current_device_cus();
+  if (!cus) return MQA_ERR_DEVICE;
+  WeighParams p{};
+  p.a.c = kernel_cache(cache);
+  p.a.q = q;
+  p.a.q_row = q_row_stride;
+  p.a.q_head = q_head_stride;
+  p.a.starts = starts;
+  p.a.ends = ends;
+  p.a.requests = requests;
+  p.a.R = R;
+  p.a.rows = requests * R;
+  p.a.heads = heads;
+  p.a.group = heads / cache->kv_heads;
+  p.a.dtype = dtype;
+  p.a.scale = scale;
+  p.lse = lse;
+  p.weights = weights;
+  p.width = width;
+  const int keys = cache->kv_heads >= 4 ? 32 : cache->kv_heads >= 2 ? 64 : 128;
+  const int most = (p.a.c.cap + keys - 1) / keys, share = 16 * cus / requests;
+  p.tiles = most < share ? most : share < 1 ? 1 : share;
+  const int err = mqa_kv_weigh_launch(&p, static_cast<hipStream_t>(stream));
+  return err != 0 ? launch_failed(err) : MQA_OK;
+}
+
+int mqa_kv_select(const float* weights, int width, const int32_t* lengths, int keep, int sinks,
+                  int recent, int32_t* positions, int32_t* counts, float* kept, int requests,
+                  void* stream) {
+  if (!weights || !lengths || !positions || !counts) return MQA_ERR_NULL;
+  if (!aligned(weights, 4) || !aligned(lengths, 4) || !aligned(positions, 4) ||
+      !aligned(counts, 4) || !aligned(kept, 4))
+    return MQA_ERR_ALIGN;
+  if (!keep_sizes_ok(requests, keep) || width < 1 || width > MQA_MAX_KEYS || sinks < 0 ||
+      recent < 0 || (int64_t)sinks + recent > keep)
+    return MQA_ERR_SHAPE;
+  if (!current_device_cus()) return MQA_ERR_DEVICE;
+  SelectParams p{};
+  p.weights = weights;
+  p.lengths = lengths;
+  p.positions = positions;
+  p.counts = counts;
+  p.kept = kept;
+  p.width = width;
+  p.keep = keep;
+  p.sinks = sinks;
+  p.recent = recent;
+  p.requests = requests;
+  const int err = mqa_kv_select_launch(&p, static_cast<hipStream_t>(stream));
+  return err != 0 ? launch_failed(err) : MQA_OK;
+}
+
+size_t workspace_size_keep(int requests, int width, int kv_heads, int head_dim, int block) {
+  if (!keep_sizes_ok(requests, width) || page_bytes(kv_heads, head_dim, block, block) == 0) return 0;
+  return keep_layout(requests, width, kv_heads, head_dim, block).total;
+}
+
+int mqa_kv_keep(const mqa_kv_cache* cache, const int32_t* positions, const int32_t* counts,
+                const int32_t* starts, int width, int requests, void* workspace,
+                size_t workspace_bytes, void* stream) {
+  if (!cache || !positions || !counts) return MQA_ERR_NULL;
+  const int rc = cache_pointers(cache);
+  if (rc != MQA_OK) return rc;
+  if (!aligned(positions, 4) || !aligned(counts, 4) || !aligned(starts, 4) ||
+      !aligned(workspace, 256))
+    return MQA_ERR_ALIGN;
+  if (!cache_shape(cache) || !keep_sizes_ok(requests, width)) return MQA_ERR_SHAPE;
+  if (!current_device_cus()) return MQA_ERR_DEVICE;
+  const KeepLayout a =
+      keep_layout(requests, width, cache->kv_heads, cache->head_dim, cache->block);
+  if (!workspace) return MQA_ERR_NULL;
+  if (workspace_bytes < a.total)
+    return workspace_failed("the workspace is smaller than workspace_size_keep()");
+  KeepParams p{};
+  p.c = kernel_cache(cache);
+  p.positions = positions;
+  p.counts = counts;
+  p.starts = starts;
+  p.width = width;
+  p.requests = requests;
+  p.blocks = (int)blocks_of(width, cache->block);
+  p.codes = static_cast<uint8_t*>(workspace);
+  p.scales = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + a.scales);
+  const int err = mqa_kv_keep_launch(&p, static_cast<hipStream_t>(stream));
+  return err != 0 ? launch_failed(err) : MQA_OK;
+}
+
+}  // extern "C"

@@ -1,7 +1,9 @@
 /*
  * mqa_serve.h -- C ABI of what a serving step does around attention over the paged
  * 8-bit key/value cache of mqa_attend.h, in libmqa_topk.so: norm and rotation of queries
- * and keys before they go there (mqa_norm_rotate).
+ * and keys before they go there (mqa_norm_rotate), and eviction: the attention weight
+ * that positions receive (mqa_kv_weigh), which of them stay (mqa_kv_select), and moving
+ * these together (mqa_kv_keep, also for the accepted tokens of a draft's tree).
  *
  * The conventions of mqa_topk.h and mqa_attend.h hold (device pointers, no allocation,
  * no state, asynchronous on `stream`, nothing launched on an error, checks in the order
@@ -52,6 +54,80 @@ int mqa_norm_rotate(const mqa_head_rows* q, const mqa_head_rows* q_out, int head
                     const void* q_weight, const void* k_weight, int weight_dtype,
                     const int32_t* positions, const float* inv_freq, int rot, int pairs, int rows,
                     int head_dim, int dtype, int norm, float eps, void* stream);
+
+#define MQA_MAX_KEPT (1 << 26) /* listed positions of all requests of a call */
+
+/*
+ * Adds to every position's weight what the rows' attention gave it:
+ *     weights[i][j] += sum over request i's rows r and heads h with s_r <= j < e_r of
+ *                      exp(S_j - lse[r][h]),   S_j, s_r and e_r as in mqa_attend_paged
+ * With the lse that mqa_attend_paged returned for the same q, ranges and scale, a row's
+ * heads share out `heads` in all.
+ *   lse       dense [requests * R, heads] fp32, 4-B aligned; a row and head of -inf adds
+ *             nothing
+ *   weights   dense [requests, width] fp32, 4-B aligned, width >= 1; positions from width
+ *             on are left out
+ *   workspace >= workspace_size_weigh(requests, R, heads, kv_heads, head_dim,
+ *             table_stride * page_size, device) bytes, 256-B aligned, owned by the call
+ *             until the stream reaches its end; nothing needs clearing. NULL where that is
+ *             256.
+ *   q, starts, ends, R, heads and scale as in mqa_attend_paged
+ * Scores and sums are held in fp32, added in a fixed order. Positions that no row sees
+ * may hold anything; one whose key holds a NaN becomes NaN if some row sees it.
+ */
+int mqa_kv_weigh(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
+                 int64_t q_head_stride, int dtype, const int32_t* starts, const int32_t* ends,
+                 const float* lse, float* weights, int width, int requests, int R, int heads,
+                 float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of workspace on `device` that suffice for every mqa_kv_weigh of up to so many
+ * requests, rows of each and positions (more than MQA_MAX_KEYS count as that); 256 where
+ * none is needed, 0 for sizes out of range or a device that is not gfx950.
+ */
+size_t workspace_size_weigh(int requests, int R, int heads, int kv_heads, int head_dim,
+                            int positions, int device);
+
+/*
+ * Which positions of each request stay: of its n = clamp(lengths[i], 0, width) positions
+ * the first `sinks`, the last `recent`, and of those between the largest weights, until
+ * counts[i] = min(n, keep) are chosen. Equal weights: the smallest positions; NaN counts
+ * as larger than any number.
+ *   weights   dense [requests, width] fp32; lengths [requests] int32
+ *   positions [requests, keep] int32: the chosen ones in ascending order, then -1
+ *   counts    [requests] int32
+ *   kept      dense [requests, width] fp32 or NULL, not overlapping weights: the chosen
+ *             positions' weights in the same order, then 0 -- what mqa_kv_weigh goes on
+ *             with after mqa_kv_keep
+ *   keep, width in [1, MQA_MAX_KEYS], requests * keep <= MQA_MAX_KEPT, sinks and recent
+ *   >= 0, sinks + recent <= keep; all pointers 4-B aligned
+ */
+int mqa_kv_select(const float* weights, int width, const int32_t* lengths, int keep, int sinks,
+                  int recent, int32_t* positions, int32_t* counts, float* kept, int requests,
+                  void* stream);
+
+/*
+ * Moves the first counts[i] (clamped to [0, width]) listed positions of request i to its
+ * positions starts[i] .. (starts NULL: 0 ..): what mqa_kv_append makes of what
+ * mqa_kv_read returns for them in fp32, but for blocks whose tokens all stay where they
+ * are, which stay as they are. A list ascends and names no position before starts[i]; an
+ * entry without a position in [0, K) or without a page stands for zeros. What stood behind
+ * the moved tokens stands for nothing afterwards: the request is starts[i] + counts[i]
+ * long. Requests must not share a page that they write to.
+ *   positions [requests, width] int32, counts and starts [requests] int32, 4-B aligned
+ *   workspace >= workspace_size_keep(requests, width, kv_heads, head_dim, block) bytes,
+ *             256-B aligned, owned by the call until the stream reaches its end; nothing
+ *             needs clearing
+ *   width in [1, MQA_MAX_KEYS], requests in [1, MQA_MAX_ROWS], requests * width <=
+ *   MQA_MAX_KEPT
+ */
+int mqa_kv_keep(const mqa_kv_cache* cache, const int32_t* positions, const int32_t* counts,
+                const int32_t* starts, int width, int requests, void* workspace,
+                size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of an mqa_kv_keep of up to so many requests and listed positions; 0
+ * for sizes out of range. */
+size_t workspace_size_keep(int requests, int width, int kv_heads, int head_dim, int block);
 
 #ifdef __cplusplus
 }

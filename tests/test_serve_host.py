@@ -74,6 +74,9 @@ def test_no_device_is_an_error_not_a_fallback():
     assert window(window=(1 << 31) - 1, sinks=(1 << 31) - 1) == 5
     assert tree() == 5
     assert rotate() == 5
+    assert weigh() == 5
+    assert select() == 5
+    assert keep() == 5
     assert rotate(k=None, kv_heads=0, rot=0, pos=0, f=0) == 5
 
 
@@ -130,3 +133,75 @@ def test_header_is_c_and_the_structure_is_the_bindings(tmp_path):
                     str(src), "-o", str(exe)], check=True)
     got = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split()
     assert [int(x) for x in got] == [getattr(H, f).offset for f, _ in H._fields_] + [ctypes.sizeof(H)]
+
+
+def weigh(c=None, **kw):
+    a = dict(q=A16, q_row=1024, q_head=128, dtype=0, starts=A16, ends=A16, lse=A16, weights=A16, width=256,
+             requests=1, R=4, heads=8, scale=1.0, ws=WS, wsb=1 << 40)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return S._load().mqa_kv_weigh(
+        cache() if c is None else c, P(a["q"]), a["q_row"], a["q_head"], a["dtype"], P(a["starts"]),
+        P(a["ends"]), P(a["lse"]), P(a["weights"]), a["width"], a["requests"], a["R"], a["heads"],
+        a["scale"], P(a["ws"]), a["wsb"], None)
+
+
+def select(**kw):
+    a = dict(weights=A16, width=256, lengths=A16, keep=64, sinks=4, recent=16, positions=A16, counts=A16,
+             kept=A16, requests=2)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return S._load().mqa_kv_select(P(a["weights"]), a["width"], P(a["lengths"]), a["keep"], a["sinks"],
+                                   a["recent"], P(a["positions"]), P(a["counts"]), P(a["kept"]),
+                                   a["requests"], None)
+
+
+def keep(c=None, **kw):
+    a = dict(positions=A16, counts=A16, starts=A16, width=64, requests=2, ws=WS, wsb=1 << 40)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return S._load().mqa_kv_keep(cache() if c is None else c, P(a["positions"]), P(a["counts"]),
+                                 P(a["starts"]), a["width"], a["requests"], P(a["ws"]), a["wsb"], None)
+
+
+def test_weigh_errors():
+    for name in ("q", "starts", "ends", "lse", "weights"):
+        assert weigh(**{name: 0}) == 1, name
+    assert weigh(cache(table=0)) == 1
+    for kw in (dict(q=0x10008), dict(starts=0x10002), dict(ends=0x10002), dict(lse=0x10002),
+               dict(weights=0x10002), dict(ws=0x20080), dict(q_row=1020), dict(q_head=132)):
+        assert weigh(**kw) == 2, kw
+    for kw in (dict(width=0), dict(requests=0), dict(R=0), dict(requests=1 << 11, R=1 << 10), dict(heads=7),
+               dict(heads=0), dict(heads=1026), dict(dtype=2), dict(scale=-1.0), dict(scale=float("inf")),
+               dict(q_row=-1024)):
+        assert weigh(**kw) == 3, kw
+    assert weigh(cache(block=128)) == 3
+
+
+def test_select_errors():
+    for name in ("weights", "lengths", "positions", "counts"):
+        assert select(**{name: 0}) == 1, name
+        assert select(**{name: 0x10002}) == 2, name
+    assert select(kept=0x10002) == 2
+    for kw in (dict(width=0), dict(width=(1 << 20) + 1), dict(keep=0), dict(keep=(1 << 20) + 1), dict(sinks=-1),
+               dict(recent=-1), dict(sinks=60, recent=5), dict(sinks=(1 << 31) - 1, recent=(1 << 31) - 1),
+               dict(requests=0), dict(requests=(1 << 20) + 1), dict(requests=1 << 20, keep=65)):
+        assert select(**kw) == 3, kw
+
+
+def test_keep_errors():
+    for name in ("positions", "counts"):
+        assert keep(**{name: 0}) == 1, name
+    for kw in (dict(positions=0x10002), dict(counts=0x10002), dict(starts=0x10002), dict(ws=0x20080)):
+        assert keep(**kw) == 2, kw
+    for kw in (dict(width=0), dict(width=(1 << 20) + 1), dict(requests=0), dict(requests=1 << 20, width=65)):
+        assert keep(**kw) == 3, kw
+    assert keep(cache(head_dim=96)) == 3
+    size = S._load().workspace_size_keep
+    assert size(1, 1, 1, 64, 16) >= 2 * 16 * 64
+    for bad in ((0, 1, 1, 64, 16), (1, 0, 1, 64, 16), (1, 1, 0, 64, 16), (1, 1, 1, 96, 16), (1, 1, 1, 64, 8),
+                (1, 1, 1, 64, 48), (1 << 20, 65, 1, 64, 16)):
+        assert size(*bad) == 0, bad
+    most = size(16, 4096, 8, 128, 64)
+    for n, w in ((16, 4096), (1, 4096), (16, 1), (3, 777)):
+        assert 0 < size(n, w, 8, 128, 64) <= most

@@ -11,7 +11,16 @@ struct WeighParams {
   float* weights;    // [requests][width]
   int width;
   int tiles;  // workgroups of a request
+  // many columns: the sums of a workgroup's share [request][slots][kWeighKeys], and how a
+  // request was cut, {first position, tiles of keys, shares of a tile, -} and its span
+  bool wide;
+  int slots;
+  float* part;
+  int4* cut;  // [requests][2]
 };
+
+// Tiles of keys that a workgroup of the wide kernel takes.
+constexpr int kWeighKeys = 512;
 
 struct SelectParams {
   const float* weights;  // [requests][width]

@@ -16,6 +16,30 @@ int64_t blocks_of(int width, int block) {
   return ((int64_t)block - 1 + width - 1) / block + 1;
 }
 
+// Calls of more columns (rows x query heads of a key head) run on the wide kernel.
+constexpr int kNarrowColumns = 64;
+constexpr int kWeighGroups = 1024;  // workgroups that the wide kernel's work is cut for
+
+struct WeighLayout {
+  bool wide;
+  int tiles, slots;  // of a request: workgroups; sums of 512 keys
+  size_t cut, total;
+};
+WeighLayout weigh_layout(int requests, int R, int heads, int kv_heads, int positions) {
+  WeighLayout a{};
+  a.wide = (int64_t)R * (heads / kv_heads) > kNarrowColumns;
+  if (!a.wide) {
+    a.total = kNoWorkspace;
+    return a;
+  }
+  const int keys = (positions + kWeighKeys - 1) / kWeighKeys;
+  a.tiles = kWeighGroups / requests < 1 ? 1 : kWeighGroups / requests;
+  a.slots = keys > a.tiles ? keys : a.tiles;
+  a.cut = (size_t)requests * a.slots * kWeighKeys * 4;
+  a.total = a.cut + (size_t)requests * 32;
+  return a;
+}
+
 struct KeepLayout {
   size_t scales, total;
 };
@@ -41,14 +65,18 @@ size_t workspace_size_weigh(int requests, int R, int heads, int kv_heads, int he
   if (!rows_ok(requests, R) || kv_heads < 1 || heads < kv_heads || heads > MQA_MAX_ATTEND_HEADS ||
       heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128) || positions < 1)
     return 0;
-  return device_cus(device) ? kNoWorkspace : 0;
+  if (!device_cus(device)) return 0;
+  const WeighLayout a = weigh_layout(requests, R, heads, kv_heads, at_most_keys(positions));
+  if (!a.wide) return a.total;
+  // (fewer requests have more workgroups each: never more than kWeighGroups in all)
+  const size_t slots = (size_t)requests * a.slots;
+  return (slots > kWeighGroups ? slots : kWeighGroups) * kWeighKeys * 4 + (size_t)requests * 32;
 }
 
 int mqa_kv_weigh(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
                  int64_t q_head_stride, int dtype, const int32_t* starts, const int32_t* ends,
                  const float* lse, float* weights, int width, int requests, int R, int heads,
                  float scale, void* workspace, size_t workspace_bytes, void* stream) {
-  (void)workspace_bytes;
   if (!cache || !q || !starts || !ends || !lse || !weights) return MQA_ERR_NULL;
   const int rc = cache_pointers(cache);
   if (rc != MQA_OK) return rc;
@@ -61,6 +89,11 @@ int mqa_kv_weigh(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
     return MQA_ERR_SHAPE;
   const int cus = current_device_cus();
   if (!cus) return MQA_ERR_DEVICE;
+  const WeighLayout l =
+      weigh_layout(requests, R, heads, cache->kv_heads, at_most_keys(positions_of(cache)));
+  if (l.wide && !workspace) return MQA_ERR_NULL;
+  if (l.wide && workspace_bytes < l.total)
+    return workspace_failed("the workspace is smaller than workspace_size_weigh()");
   WeighParams p{};
   p.a.c = kernel_cache(cache);
   p.a.q = q;
@@ -78,9 +111,14 @@ int mqa_kv_weigh(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
   p.lse = lse;
   p.weights = weights;
   p.width = width;
+  p.wide = l.wide;
+  p.tiles = l.tiles;
+  p.slots = l.slots;
+  p.part = static_cast<float*>(workspace);
+  p.cut = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + l.cut);
   const int keys = cache->kv_heads >= 4 ? 32 : cache->kv_heads >= 2 ? 64 : 128;
   const int most = (p.a.c.cap + keys - 1) / keys, share = 16 * cus / requests;
-  p.tiles = most < share ? most : share < 1 ? 1 : share;
+  if (!l.wide) p.tiles = most < share ? most : share < 1 ? 1 : share;
   const int err = mqa_kv_weigh_launch(&p, static_cast<hipStream_t>(stream));
   return err != 0 ? launch_failed(err) : MQA_OK;
 }

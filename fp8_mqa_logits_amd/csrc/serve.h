@@ -11,12 +11,16 @@ struct WeighParams {
   float* weights;    // [requests][width]
   int width;
   int tiles;  // workgroups of a request
-  // many columns: the sums of a workgroup's share [request][slots][kWeighKeys], and how a
-  // request was cut, {first position, tiles of keys, shares of a tile, -} and its span
+  // Many columns: what is known of a column, {lse', its factor}, [request][head][32 *
+  // row_tiles]; of 32 columns, {largest start, smallest end, smallest start, largest end};
+  // of a request, {first position, tiles of keys, shares of a tile, -} and its span; and
+  // the sums of a workgroup's share [request][slots][kWeighKeys].
   bool wide;
-  int slots;
-  float* part;
+  int slots, row_tiles;
+  float2* columns;
+  int4* sight;
   int4* cut;  // [requests][2]
+  float* part;
 };
 
 // Tiles of keys that a workgroup of the wide kernel takes.

@@ -22,8 +22,8 @@ constexpr int kWeighGroups = 1024;  // workgroups that the wide kernel's work is
 
 struct WeighLayout {
   bool wide;
-  int tiles, slots;  // of a request: workgroups; sums of 512 keys
-  size_t cut, total;
+  int tiles, slots, row_tiles;  // of a request: workgroups; sums of 512 keys; 32 rows
+  size_t part, sight, cut, total;
 };
 WeighLayout weigh_layout(int requests, int R, int heads, int kv_heads, int positions) {
   WeighLayout a{};
@@ -35,8 +35,14 @@ WeighLayout weigh_layout(int requests, int R, int heads, int kv_heads, int posit
   const int keys = (positions + kWeighKeys - 1) / kWeighKeys;
   a.tiles = kWeighGroups / requests < 1 ? 1 : kWeighGroups / requests;
   a.slots = keys > a.tiles ? keys : a.tiles;
-  a.cut = (size_t)requests * a.slots * kWeighKeys * 4;
-  a.total = a.cut + (size_t)requests * 32;
+  a.row_tiles = (R + 31) / 32;
+  const size_t tiles = (size_t)requests * heads * a.row_tiles;
+  // (fewer requests have more workgroups each: never more than kWeighGroups in all)
+  const size_t slots = (size_t)requests * a.slots;
+  a.part = tiles * 32 * sizeof(float2);
+  a.sight = a.part + (slots > kWeighGroups ? slots : kWeighGroups) * kWeighKeys * 4;
+  a.cut = a.sight + tiles * sizeof(int4);
+  a.total = a.cut + (size_t)requests * 2 * sizeof(int4);
   return a;
 }
 
@@ -66,11 +72,7 @@ size_t workspace_size_weigh(int requests, int R, int heads, int kv_heads, int he
       heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128) || positions < 1)
     return 0;
   if (!device_cus(device)) return 0;
-  const WeighLayout a = weigh_layout(requests, R, heads, kv_heads, at_most_keys(positions));
-  if (!a.wide) return a.total;
-  // (fewer requests have more workgroups each: never more than kWeighGroups in all)
-  const size_t slots = (size_t)requests * a.slots;
-  return (slots > kWeighGroups ? slots : kWeighGroups) * kWeighKeys * 4 + (size_t)requests * 32;
+  return weigh_layout(requests, R, heads, kv_heads, at_most_keys(positions)).total;
 }
 
 int mqa_kv_weigh(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
@@ -114,8 +116,12 @@ int mqa_kv_weigh(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
   p.wide = l.wide;
   p.tiles = l.tiles;
   p.slots = l.slots;
-  p.part = static_cast<float*>(workspace);
-  p.cut = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + l.cut);
+  p.row_tiles = l.row_tiles;
+  uint8_t* const base = static_cast<uint8_t*>(workspace);
+  p.columns = reinterpret_cast<float2*>(base);
+  p.part = reinterpret_cast<float*>(base + l.part);
+  p.sight = reinterpret_cast<int4*>(base + l.sight);
+  p.cut = reinterpret_cast<int4*>(base + l.cut);
   const int keys = cache->kv_heads >= 4 ? 32 : cache->kv_heads >= 2 ? 64 : 128;
   const int most = (p.a.c.cap + keys - 1) / keys, share = 16 * cus / requests;
   if (!l.wide) p.tiles = most < share ? most : share < 1 ? 1 : share;

@@ -125,20 +125,62 @@ __global__ __launch_bounds__(256, 4) void weigh_narrow_kernel(WeighParams p) {
   }
 }
 
-// Many columns: a wave holds 64 keys of one head, widened, in registers as the first
-// operand of v_mfma_f32_32x32x16; 512 keys a workgroup. Queries pass through LDS, 64
-// columns at a time, with what belongs to a column: lse', its factor, its range. So a
-// staged query meets 512 keys, and a wave's only traffic per 64 keys x 32 columns is one
-// read of the columns from LDS.
-//
-// A request's columns of all heads are cut into shares so that about p.tiles workgroups
-// have work, whatever its span turns out to be; a workgroup goes from head to head in its
-// share with the same sums, and weigh_join_kernel adds up a position's shares.
-struct Column {
-  float to, by;  // lse' and the factor of what it lacks
-  int s, e;      // its range, empty where it adds nothing
-};
+// Many columns. A column here is a row of one query head; 32 rows of a head, the last
+// ones repeated, are a tile of columns. weigh_columns_kernel forms what the exponentials
+// take of a column, once for all keys, and how a request's work is cut: its columns into
+// shares so that about p.tiles workgroups have work, whatever its span turns out to be.
+__global__ __launch_bounds__(256) void weigh_columns_kernel(WeighParams p, int blocks) {
+  const AttendParams& a = p.a;
+  const int lane = threadIdx.x & 63;
+  if ((int)blockIdx.x < a.requests) {
+    const int unit = blockIdx.x, wave = threadIdx.x >> 6;
+    __shared__ Span s_span[4];
+    Span span = row_span<kRange>(a, unit * a.R, a.R, threadIdx.x, 256);
+    if (lane == 0) s_span[wave] = span;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int w = 1; w < 4; ++w) span = join<kRange>(span, s_span[w]);
+    const int first = span.lo & ~15;
+    const int tiles = span.hi > first ? (span.hi - first + kWeighKeys - 1) / kWeighKeys : 0;
+    const int stages = (a.group * p.row_tiles + 1) / 2 * a.c.kv_heads;
+    p.cut[2 * unit] = int4{first, tiles, tiles > 0 ? min(max(p.tiles / tiles, 1), stages) : 1, 0};
+    p.cut[2 * unit + 1] = int4{span.lo, span.hi, 0, 0};
+    return;
+  }
+  const int64_t tiles = (int64_t)a.requests * a.heads * p.row_tiles;
+  for (int64_t x = ((int64_t)(blockIdx.x - a.requests) * 256 + threadIdx.x) / 32; x < tiles;
+       x += (int64_t)blocks * 8) {
+    const int64_t pair = x / p.row_tiles;  // request, head
+    const int at = (int)(x % p.row_tiles) * 32 + (lane & 31);
+    const int row = (int)(pair / a.heads) * a.R + min(at, a.R - 1);
+    const float lse = p.lse[(int64_t)row * a.heads + pair % a.heads];
+    int s, e;
+    row_range(a, row, s, e);
+    const bool adds = at < a.R && s < e && lse != -__builtin_inff();
+    const float to = lse * kLog2e;
+    p.columns[x * 32 + (lane & 31)] = adds ? float2{to, lacking(lse, to)} : float2{0.f, 0.f};
+    int4 m{adds ? s : a.c.cap, adds ? e : 0, adds ? s : a.c.cap, adds ? e : 0};
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      m.x = max(m.x, __shfl_xor(m.x, o, 64));
+      m.y = min(m.y, __shfl_xor(m.y, o, 64));
+      m.z = min(m.z, __shfl_xor(m.z, o, 64));
+      m.w = max(m.w, __shfl_xor(m.w, o, 64));
+    }
+    if ((lane & 31) == 0) p.sight[x] = m;
+  }
+}
 
+// A wave holds 64 keys of one key head, widened, in registers as the first operand of
+// v_mfma_f32_32x32x16, 512 keys a workgroup. Queries pass through LDS, two tiles of
+// columns a stage, so that what is staged meets 512 keys and a wave's traffic per 64 keys
+// x 32 columns is one read of the columns from LDS. A workgroup goes from head to head
+// in its share of the columns with the same sums; weigh_join_kernel adds the shares up.
+//
+// A unit: 32 keys x 32 columns. The products of one unit and the exponentials of the one
+// before it are independent, so that the matrix and the vector unit work at the same
+// time; `late` are the scores whose exponentials are still to be taken. Stages that some
+// column sees in part are done unit by unit, with masks.
 template <int T, int C, int D>
 __global__ __launch_bounds__(512, 2) void weigh_wide_kernel(WeighParams p) {
   constexpr int KS = D / 16, COLS = 64, QROW = 2 * D + 16;
@@ -148,55 +190,42 @@ __global__ __launch_bounds__(512, 2) void weigh_wide_kernel(WeighParams p) {
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int hh = lane >> 5, n = lane & 31;
   const int unit = blockIdx.x / p.tiles, g0 = blockIdx.x % p.tiles;
-  const int columns = a.R * a.group, per_head = (columns + COLS - 1) / COLS;
-  const int all = per_head * c.kv_heads;
-
   __shared__ __align__(16) uint8_t s_q[2][COLS * QROW];
-  __shared__ __align__(16) Column s_col[2][COLS];
-  __shared__ int4 s_sight[2][2];  // of 32 columns: {largest s, smallest e, smallest s, largest e}
-  __shared__ Span s_span[8];
 
-  Span span = row_span<kRange>(a, unit * a.R, a.R, t, 512);
-  if (lane == 0) s_span[wave] = span;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 8; ++w) span = join<kRange>(span, s_span[w]);
-  const int lo = __builtin_amdgcn_readfirstlane(span.lo), hi = __builtin_amdgcn_readfirstlane(span.hi);
-  const int first = lo & ~15;
-  const int tiles = hi > first ? (hi - first + kWeighKeys - 1) / kWeighKeys : 0;
-  const int shares = tiles > 0 ? min(max(p.tiles / tiles, 1), all) : 1;
-  if (g0 == 0 && t == 0) {
-    p.cut[2 * unit] = int4{first, tiles, shares, 0};
-    p.cut[2 * unit + 1] = int4{lo, hi, 0, 0};
-  }
+  const int4 cut = p.cut[2 * unit];
+  const int first = __builtin_amdgcn_readfirstlane(cut.x);
+  const int tiles = __builtin_amdgcn_readfirstlane(cut.y);
+  const int shares = __builtin_amdgcn_readfirstlane(cut.z);
+  const int hi = __builtin_amdgcn_readfirstlane(p.cut[2 * unit + 1].y);
+  const int subs = a.group * p.row_tiles;  // tiles of columns of a key head
+  const int per_head = (subs + 1) / 2, all = per_head * c.kv_heads;
   const int share = (all + shares - 1) / shares;
   const float cs = a.scale * kLog2e;
   const int32_t* const table = c.table + (int64_t)unit * c.table_stride;
+  const int64_t tile0 = (int64_t)unit * a.heads * p.row_tiles;
 
-  // stage x: 64 columns of head x / per_head
+  // A stage: tiles y and y + 1 of key head h's columns (the last one may be missing).
+  struct Stage {
+    int h, y;
+  };
+  auto next = [&](Stage x) {
+    const bool over = x.y + 2 >= subs;
+    return Stage{over ? x.h + 1 : x.h, over ? 0 : x.y + 2};
+  };
+  auto tile_of = [&](const Stage& x, int sub) {  // clamped into the key head's
+    return min(x.h, c.kv_heads - 1) * subs + min(x.y + sub, subs - 1);
+  };
   v4u q_reg[EACH];
-  float lse_reg = 0.f;
-  int s_reg = 0, e_reg = 0;
-  auto load = [&](int x) {
-    const int h = x / per_head, col0 = x % per_head * COLS;
+  auto load = [&](const Stage& x) {
 #pragma unroll
     for (int r = 0; r < EACH; ++r) {
-      const int piece = t + 512 * r, col = col0 + piece / (D / 8);
-      const bool real = col < columns;
-      const int row = unit * a.R + (real ? col / a.group : 0);
-      const int head = h * a.group + (real ? col % a.group : 0);
+      const int piece = t + 512 * r;
+      const int tile = tile_of(x, piece / (32 * D / 8));
+      const int head = tile / p.row_tiles;
+      const int row = unit * a.R +
+                      min(tile % p.row_tiles * 32 + piece % (32 * D / 8) / (D / 8), a.R - 1);
       q_reg[r] = *reinterpret_cast<const v4u*>(static_cast<const uint16_t*>(a.q) + row * a.q_row +
                                                head * a.q_head + piece % (D / 8) * 8);
-      if (!real) q_reg[r] = v4u{0, 0, 0, 0};
-    }
-    if (wave == 0) {
-      const int col = col0 + lane;
-      const bool real = col < columns;
-      const int row = unit * a.R + (real ? col / a.group : 0);
-      const int head = h * a.group + (real ? col % a.group : 0);
-      lse_reg = p.lse[(int64_t)row * a.heads + head];
-      row_range(a, row, s_reg, e_reg);
-      if (!real) e_reg = s_reg;
     }
   };
   auto stage = [&](int buf) {
@@ -205,24 +234,20 @@ __global__ __launch_bounds__(512, 2) void weigh_wide_kernel(WeighParams p) {
       const int piece = t + 512 * r;
       *reinterpret_cast<v4u*>(s_q[buf] + piece / (D / 8) * QROW + piece % (D / 8) * 16) = q_reg[r];
     }
-    if (wave == 0) {
-      const bool adds = s_reg < e_reg && lse_reg != -__builtin_inff();
-      Column k;
-      k.to = lse_reg * kLog2e;
-      k.by = lacking(lse_reg, k.to);
-      k.s = adds ? s_reg : 0;
-      k.e = adds ? e_reg : 0;
-      s_col[buf][lane] = k;
-      int4 m{k.s, k.e, adds ? k.s : c.cap, k.e};
+  };
+  // of a stage: its lane's column of either tile, and in lanes 0 .. 7 what its tiles see
+  struct Known {
+    float2 col[2];
+    int sight;
+  };
+  auto know = [&](const Stage& x) {
+    Known k;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        m.x = max(m.x, __shfl_xor(m.x, o, 64));
-        m.y = min(m.y, __shfl_xor(m.y, o, 64));
-        m.z = min(m.z, __shfl_xor(m.z, o, 64));
-        m.w = max(m.w, __shfl_xor(m.w, o, 64));
-      }
-      if (n == 0) s_sight[buf][hh] = m;
-    }
+    for (int sub = 0; sub < 2; ++sub)
+      k.col[sub] = p.columns[(tile0 + tile_of(x, sub)) * 32 + n];
+    k.sight = reinterpret_cast<const int*>(
+        p.sight + tile0 + tile_of(x, lane >> 2 & 1))[lane & 3];
+    return k;
   };
 
   int count = 0;  // of stages: which buffer
@@ -237,14 +262,44 @@ __global__ __launch_bounds__(512, 2) void weigh_wide_kernel(WeighParams p) {
     v4u kf[2][KS];
     float f[2][2];
     int at_head = -1;
-    if (x_lo < x_hi) load(x_lo);
+    v16f late = v16f{};
+    float2 last{0.f, 0.f};
+    bool pending = false;
+    auto add = [&](int b, const v16f& s, const float* by_block, const float2& col) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        acc[b][e] = __builtin_fmaf(
+            __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], by_block[e >> 3], -col.x)), col.y,
+            acc[b][e]);
+    };
+    auto flush = [&]() {
+      if (pending) add(1, late, f[1], last);
+      pending = false;
+    };
+    v4u q[KS];
+    auto take_q = [&](int buf, int sub) {
+      const uint8_t* const from = s_q[buf] + (32 * sub + n) * QROW + 32 * hh;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+        q[k] = *reinterpret_cast<const v4u*>(from + 64 * (k >> 1) + 16 * (k & 1));
+    };
+    auto products = [&](v16f& s, int b) {
+      s = v16f{};
+#pragma unroll
+      for (int k = 0; k < KS; ++k) s = mfma32<T>(kf[b][k], q[k], s);
+    };
+    if (x_lo >= x_hi) continue;  // (the join reads no such share)
+    Stage now{x_lo / per_head, x_lo % per_head * 2}, ahead = next(now);
+    load(now);
+    stage(count & 1);
+    load(ahead);
+    Known known = know(now);
+    __syncthreads();
     for (int x = x_lo; x < x_hi; ++x, ++count) {
       const int buf = count & 1;
-      stage(buf);
-      if (x + 1 < x_hi) load(x + 1);
-      const int h = x / per_head;
-      if (h != at_head) {
-        at_head = h;
+      if (now.h != at_head) {
+        flush();
+        at_head = now.h;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const int pos = min(pos0 + 32 * b + n, ((hi - 1) & ~15) + (n & 15));
@@ -253,55 +308,76 @@ __global__ __launch_bounds__(512, 2) void weigh_wide_kernel(WeighParams p) {
           const int slot = pos & ((1 << c.page_shift) - 1);
 #pragma unroll
           for (int j = 0; j < KS / 2; ++j) {
-            const v4u raw = *reinterpret_cast<const v4u*>(page + code_at(c, 0, h, slot) +
+            const v4u raw = *reinterpret_cast<const v4u*>(page + code_at(c, 0, at_head, slot) +
                                                           16 * (2 * j + hh));
             kf[b][2 * j] = widen8<T, C>(raw[0], raw[1]);
             kf[b][2 * j + 1] = widen8<T, C>(raw[2], raw[3]);
           }
-          const float scale = *reinterpret_cast<const float*>(page + scale_at(c, 0, h, slot)) * cs;
+          const float scale =
+              *reinterpret_cast<const float*>(page + scale_at(c, 0, at_head, slot)) * cs;
           f[b][0] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale), 0));
           f[b][1] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale), 16));
         }
       }
-      __syncthreads();
-#pragma unroll
-      for (int sub = 0; sub < 2; ++sub) {
-        const int4 sight = s_sight[buf][sub];
-        const int smax = __builtin_amdgcn_readfirstlane(sight.x);
-        const int emin = __builtin_amdgcn_readfirstlane(sight.y);
-        const int smin = __builtin_amdgcn_readfirstlane(sight.z);
-        const int emax = __builtin_amdgcn_readfirstlane(sight.w);
-        if (emax <= pos0 || smin >= pos0 + 64) continue;
-        const Column col = s_col[buf][32 * sub + n];
-        const uint8_t* const from = s_q[buf] + (32 * sub + n) * QROW + 32 * hh;
-        v16f s[2] = {v16f{}, v16f{}};
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const v4u q = *reinterpret_cast<const v4u*>(from + 64 * (k >> 1) + 16 * (k & 1));
-#pragma unroll
-          for (int b = 0; b < 2; ++b) s[b] = mfma32<T>(kf[b][k], q, s[b]);
+      auto word = [&](int i) { return __builtin_amdgcn_readlane(known.sight, i); };
+      const Known then = know(ahead);
+      const Stage after = next(ahead);
+      if (max(word(0), word(4)) <= pos0 && min(word(1), word(5)) >= pos0 + 64 && now.y + 1 < subs) {
+        // every column sees every key
+        const float late_f[2] = {pending ? f[1][0] : 0.f, pending ? f[1][1] : 0.f};
+        if (!pending) {
+          late = v16f{};
+          last = float2{0.f, 0.f};
         }
-        const bool clean = smax <= pos0 && emin >= pos0 + 64;
+        v16f s0, s1;
+        take_q(buf, 0);
+        products(s0, 0);
+        add(1, late, late_f, last);
+        products(s1, 1);
+        add(0, s0, f[0], known.col[0]);
+        take_q(buf, 1);
+        stage(buf ^ 1);
+        products(s0, 0);
+        add(1, s1, f[1], known.col[0]);
+        load(after);
+        products(late, 1);
+        add(0, s0, f[0], known.col[1]);
+        last = known.col[1];
+        pending = true;
+      } else {
+        flush();
+        stage(buf ^ 1);
+        load(after);
+#pragma unroll 1
+        for (int sub = 0; sub < 2; ++sub) {
+          if (word(4 * sub + 3) <= pos0 || word(4 * sub + 2) >= pos0 + 64 || now.y + sub >= subs)
+            continue;
+          const float2 col = sub ? known.col[1] : known.col[0];
+          const int tile = tile_of(now, sub), at = tile % p.row_tiles * 32 + n;
+          int s, e;
+          row_range(a, unit * a.R + min(at, a.R - 1), s, e);
+          if (at >= a.R || col.y == 0.f) s = e = 0;  // (adds nothing)
+          take_q(buf, sub);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const uint32_t sees =
-              clean ? ~0u : seen_bits(pos0 + 32 * b, col.s, col.e) >> (4 * hh);
-          if (clean) {
+          for (int b = 0; b < 2; ++b) {
+            const uint32_t sees = seen_bits(pos0 + 32 * b, s, e) >> (4 * hh);
+            v16f score;
+            products(score, b);
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              acc[b][e] = __builtin_fmaf(
-                  __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][e], f[b][e >> 3], -col.to)), col.by,
-                  acc[b][e]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][e], f[b][e >> 3], -col.to));
-              acc[b][e] += or_zero(w * col.by, bit(sees, 8 * (e >> 2) + (e & 3)));
+            for (int i = 0; i < 16; ++i) {
+              const float w =
+                  __builtin_amdgcn_exp2f(__builtin_fmaf(score[i], f[b][i >> 3], -col.x));
+              acc[b][i] += or_zero(w * col.y, bit(sees, 8 * (i >> 2) + (i & 3)));
             }
           }
         }
       }
+      known = then;
+      now = ahead;
+      ahead = after;
+      __syncthreads();
     }
+    flush();
     float* const part = p.part + ((int64_t)unit * p.slots + item) * kWeighKeys + wave * 64;
 #pragma unroll
     for (int b = 0; b < 2; ++b)
@@ -320,12 +396,14 @@ __global__ __launch_bounds__(256) void weigh_join_kernel(WeighParams p, int bloc
   const int unit = blockIdx.x / blocks;
   const int4 cut = p.cut[2 * unit], span = p.cut[2 * unit + 1];
   const int end = min(span.y, p.width);
+  const int all = (p.a.group * p.row_tiles + 1) / 2 * p.a.c.kv_heads;
+  const int share = (all + cut.z - 1) / cut.z, shares = (all + share - 1) / share;
   for (int pos = cut.x + (blockIdx.x % blocks) * 256 + (int)threadIdx.x; pos < end;
        pos += blocks * 256) {
     if (pos < span.x) continue;
     const float* part = p.part + (int64_t)unit * p.slots * kWeighKeys + (pos - cut.x);
     float sum = 0.f;
-    for (int s = 0; s < cut.z; ++s) sum += part[(int64_t)s * cut.y * kWeighKeys];
+    for (int s = 0; s < shares; ++s) sum += part[(int64_t)s * cut.y * kWeighKeys];
     p.weights[(int64_t)unit * p.width + pos] += sum;
   }
 }
@@ -342,6 +420,10 @@ extern "C" int mqa_kv_weigh_launch(const mqa::WeighParams* p, hipStream_t s) {
     });
     return (int)hipGetLastError();
   }
+  const int64_t columns = (int64_t)p->a.requests * p->a.heads * p->row_tiles;
+  const int column_blocks = (int)((columns + 7) / 8 < 4096 ? (columns + 7) / 8 : 4096);
+  weigh_columns_kernel<<<dim3((unsigned)(p->a.requests + column_blocks)), 256, 0, s>>>(
+      *p, column_blocks);
   dispatch(p->a, [&](auto t, auto c, auto d) {
     weigh_wide_kernel<t.value, c.value, d.value><<<grid, 512, 0, s>>>(*p);
   });

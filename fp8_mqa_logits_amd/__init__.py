@@ -649,5 +649,5 @@ from .attend import (KVLayout, mqa_attend_paged, mqa_attend_topk, mqa_attend_tre
                      mqa_attend_window, mqa_kv_append, mqa_kv_read, workspace_size_attend)
 from .attend import EXPORTS as ATTEND_EXPORTS  # noqa: E402
 from .serve import (mqa_kv_keep, mqa_kv_select, mqa_kv_weigh, mqa_norm_rotate,  # noqa: E402
-                    workspace_size_keep, workspace_size_weigh)
+                    workspace_size_keep, workspace_size_select, workspace_size_weigh)
 from .serve import EXPORTS as SERVE_EXPORTS  # noqa: E402

@@ -11,16 +11,18 @@ struct WeighParams {
   float* weights;    // [requests][width]
   int width;
   int tiles;  // workgroups of a request
-  // Many columns: what is known of a column, {lse', its factor}, [request][head][32 *
-  // row_tiles]; of 32 columns, {largest start, smallest end, smallest start, largest end};
-  // of a request, {first position, tiles of keys, shares of a tile, -} and its span; and
-  // the sums of a workgroup's share [request][slots][kWeighKeys].
+  // Many columns, tile by tile of 32 (row_tiles for a query head's rows, an even number
+  // for a key head's): the queries [tile][32][head_dim]; {lse', its factor} [tile][32];
+  // {largest start, smallest end, smallest start, largest end} [tile]. The sums of a
+  // workgroup's share [request][slots][kWeighKeys]. Of a request, {first position, tiles of
+  // keys, shares of a tile, -} and its span [request][2].
   bool wide;
   int slots, row_tiles;
+  uint16_t* queries;
   float2* columns;
   int4* sight;
-  int4* cut;  // [requests][2]
   float* part;
+  int4* cut;
 };
 
 // Tiles of keys that a workgroup of the wide kernel takes.
@@ -33,6 +35,8 @@ struct SelectParams {
   int32_t* counts;
   float* kept;  // [requests][width] or nullptr
   int width, keep, sinks, recent, requests;
+  int parts, part;  // of a request's positions, their length (a multiple of 1024)
+  uint32_t* hist;   // parts > 1: [requests][parts][3][2048]
 };
 
 struct KeepParams {

@@ -23,9 +23,10 @@ constexpr int kWeighGroups = 1024;  // workgroups that the wide kernel's work is
 struct WeighLayout {
   bool wide;
   int tiles, slots, row_tiles;  // of a request: workgroups; sums of 512 keys; 32 rows
-  size_t part, sight, cut, total;
+  size_t columns, sight, part, cut, total;
 };
-WeighLayout weigh_layout(int requests, int R, int heads, int kv_heads, int positions) {
+WeighLayout weigh_layout(int requests, int R, int heads, int kv_heads, int head_dim,
+                         int positions) {
   WeighLayout a{};
   a.wide = (int64_t)R * (heads / kv_heads) > kNarrowColumns;
   if (!a.wide) {
@@ -36,13 +37,36 @@ WeighLayout weigh_layout(int requests, int R, int heads, int kv_heads, int posit
   a.tiles = kWeighGroups / requests < 1 ? 1 : kWeighGroups / requests;
   a.slots = keys > a.tiles ? keys : a.tiles;
   a.row_tiles = (R + 31) / 32;
-  const size_t tiles = (size_t)requests * heads * a.row_tiles;
+  const size_t tiles =
+      (size_t)requests * kv_heads * ((heads / kv_heads * (size_t)a.row_tiles + 1) / 2 * 2);
   // (fewer requests have more workgroups each: never more than kWeighGroups in all)
   const size_t slots = (size_t)requests * a.slots;
-  a.part = tiles * 32 * sizeof(float2);
-  a.sight = a.part + (slots > kWeighGroups ? slots : kWeighGroups) * kWeighKeys * 4;
-  a.cut = a.sight + tiles * sizeof(int4);
+  a.columns = tiles * 32 * head_dim * 2;
+  a.sight = a.columns + tiles * 32 * sizeof(float2);
+  a.part = a.sight + tiles * sizeof(int4);
+  a.cut = a.part + (slots > kWeighGroups ? slots : kWeighGroups) * kWeighKeys * 4;
   a.total = a.cut + (size_t)requests * 2 * sizeof(int4);
+  return a;
+}
+
+// Parts of a request's positions in mqa_kv_select. Up to 16384 weights stay in one
+// workgroup's registers (32 requests of 9001: 18 us, in three parts 27); more are cut into
+// as many parts as fill the card, of 4096 or more (65536 weights of one request: 16 parts,
+// 37 us, in one 99); 512 requests and more have one workgroup each.
+constexpr int kSelectWhole = 16384;
+int64_t select_parts(int width) { return width <= kSelectWhole ? 1 : (width + 4095) / 4096; }
+
+struct SelectLayout {
+  int parts, part;
+  size_t total;
+};
+SelectLayout select_layout(int requests, int width) {
+  SelectLayout a{};
+  const int most = 512 / requests < 64 ? 512 / requests : 64, want = (int)select_parts(width);
+  const int parts = most < 1 ? 1 : want < most ? want : most;
+  a.part = ((width + parts - 1) / parts + 1023) / 1024 * 1024;
+  a.parts = (width + a.part - 1) / a.part;
+  a.total = a.parts > 1 ? (size_t)requests * a.parts * 3 * 2048 * 4 : kNoWorkspace;
   return a;
 }
 
@@ -72,7 +96,7 @@ size_t workspace_size_weigh(int requests, int R, int heads, int kv_heads, int he
       heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128) || positions < 1)
     return 0;
   if (!device_cus(device)) return 0;
-  return weigh_layout(requests, R, heads, kv_heads, at_most_keys(positions)).total;
+  return weigh_layout(requests, R, heads, kv_heads, head_dim, at_most_keys(positions)).total;
 }
 
 int mqa_kv_weigh(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
@@ -92,7 +116,8 @@ int mqa_kv_weigh(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
   const int cus = current_device_cus();
   if (!cus) return MQA_ERR_DEVICE;
   const WeighLayout l =
-      weigh_layout(requests, R, heads, cache->kv_heads, at_most_keys(positions_of(cache)));
+      weigh_layout(requests, R, heads, cache->kv_heads, cache->head_dim,
+                   at_most_keys(positions_of(cache)));
   if (l.wide && !workspace) return MQA_ERR_NULL;
   if (l.wide && workspace_bytes < l.total)
     return workspace_failed("the workspace is smaller than workspace_size_weigh()");
@@ -118,7 +143,8 @@ int mqa_kv_weigh(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
   p.slots = l.slots;
   p.row_tiles = l.row_tiles;
   uint8_t* const base = static_cast<uint8_t*>(workspace);
-  p.columns = reinterpret_cast<float2*>(base);
+  p.queries = reinterpret_cast<uint16_t*>(base);
+  p.columns = reinterpret_cast<float2*>(base + l.columns);
   p.part = reinterpret_cast<float*>(base + l.part);
   p.sight = reinterpret_cast<int4*>(base + l.sight);
   p.cut = reinterpret_cast<int4*>(base + l.cut);
@@ -131,16 +157,23 @@ int mqa_kv_weigh(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
 
 int mqa_kv_select(const float* weights, int width, const int32_t* lengths, int keep, int sinks,
                   int recent, int32_t* positions, int32_t* counts, float* kept, int requests,
-                  void* stream) {
+                  void* workspace, size_t workspace_bytes, void* stream) {
   if (!weights || !lengths || !positions || !counts) return MQA_ERR_NULL;
   if (!aligned(weights, 4) || !aligned(lengths, 4) || !aligned(positions, 4) ||
-      !aligned(counts, 4) || !aligned(kept, 4))
+      !aligned(counts, 4) || !aligned(kept, 4) || !aligned(workspace, 256))
     return MQA_ERR_ALIGN;
   if (!keep_sizes_ok(requests, keep) || width < 1 || width > MQA_MAX_KEYS || sinks < 0 ||
       recent < 0 || (int64_t)sinks + recent > keep)
     return MQA_ERR_SHAPE;
   if (!current_device_cus()) return MQA_ERR_DEVICE;
+  const SelectLayout l = select_layout(requests, width);
+  if (l.parts > 1 && !workspace) return MQA_ERR_NULL;
+  if (l.parts > 1 && workspace_bytes < l.total)
+    return workspace_failed("the workspace is smaller than workspace_size_select()");
   SelectParams p{};
+  p.parts = l.parts;
+  p.part = l.part;
+  p.hist = static_cast<uint32_t*>(workspace);
   p.weights = weights;
   p.lengths = lengths;
   p.positions = positions;
@@ -153,6 +186,13 @@ int mqa_kv_select(const float* weights, int width, const int32_t* lengths, int k
   p.requests = requests;
   const int err = mqa_kv_select_launch(&p, static_cast<hipStream_t>(stream));
   return err != 0 ? launch_failed(err) : MQA_OK;
+}
+
+size_t workspace_size_select(int requests, int width) {
+  if (requests < 1 || requests > MQA_MAX_ROWS || width < 1 || width > MQA_MAX_KEYS) return 0;
+  // fewer requests may have more parts each, but never more than 512 in all
+  const int64_t most = select_parts(width), parts = requests * most < 512 ? requests * most : 512;
+  return most > 1 ? (size_t)parts * 3 * 2048 * 4 : kNoWorkspace;
 }
 
 size_t workspace_size_keep(int requests, int width, int kv_heads, int head_dim, int block) {

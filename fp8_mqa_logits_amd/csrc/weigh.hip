@@ -125,40 +125,56 @@ __global__ __launch_bounds__(256, 4) void weigh_narrow_kernel(WeighParams p) {
   }
 }
 
-// Many columns. A column here is a row of one query head; 32 rows of a head, the last
-// ones repeated, are a tile of columns. weigh_columns_kernel forms what the exponentials
-// take of a column, once for all keys, and how a request's work is cut: its columns into
-// shares so that about p.tiles workgroups have work, whatever its span turns out to be.
+// Many columns. A column here is a row of one query head; a tile is 32 rows of a head
+// (the last ones repeated), and a stage two tiles of one key head's query heads (the last
+// one may be empty). weigh_columns_kernel lays out what all keys meet, stage by stage:
+// the queries, what the exponentials take of a column, and what a tile sees; and how a
+// request's work is cut: its stages into shares so that about p.tiles workgroups have
+// work, whatever its span turns out to be.
+template <int D>
 __global__ __launch_bounds__(256) void weigh_columns_kernel(WeighParams p, int blocks) {
   const AttendParams& a = p.a;
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int per_head = (a.group * p.row_tiles + 1) / 2;  // stages of a key head
   if ((int)blockIdx.x < a.requests) {
-    const int unit = blockIdx.x, wave = threadIdx.x >> 6;
+    const int unit = blockIdx.x;
     __shared__ Span s_span[4];
     Span span = row_span<kRange>(a, unit * a.R, a.R, threadIdx.x, 256);
     if (lane == 0) s_span[wave] = span;
     __syncthreads();
     if (threadIdx.x != 0) return;
     for (int w = 1; w < 4; ++w) span = join<kRange>(span, s_span[w]);
-    const int first = span.lo & ~15;
+    const int first = span.lo & ~15, stages = per_head * a.c.kv_heads;
     const int tiles = span.hi > first ? (span.hi - first + kWeighKeys - 1) / kWeighKeys : 0;
-    const int stages = (a.group * p.row_tiles + 1) / 2 * a.c.kv_heads;
     p.cut[2 * unit] = int4{first, tiles, tiles > 0 ? min(max(p.tiles / tiles, 1), stages) : 1, 0};
     p.cut[2 * unit + 1] = int4{span.lo, span.hi, 0, 0};
     return;
   }
-  const int64_t tiles = (int64_t)a.requests * a.heads * p.row_tiles;
-  for (int64_t x = ((int64_t)(blockIdx.x - a.requests) * 256 + threadIdx.x) / 32; x < tiles;
-       x += (int64_t)blocks * 8) {
-    const int64_t pair = x / p.row_tiles;  // request, head
-    const int at = (int)(x % p.row_tiles) * 32 + (lane & 31);
-    const int row = (int)(pair / a.heads) * a.R + min(at, a.R - 1);
-    const float lse = p.lse[(int64_t)row * a.heads + pair % a.heads];
+  const int64_t tiles = (int64_t)a.requests * a.c.kv_heads * per_head * 2;
+  for (int64_t x = (int64_t)(blockIdx.x - a.requests) * 4 + wave; x < tiles;
+       x += (int64_t)blocks * 4) {
+    const int y = (int)(x % (per_head * 2));
+    const int64_t key_head = x / (per_head * 2);  // of all requests
+    const int unit = (int)(key_head / a.c.kv_heads);
+    const bool real = y < a.group * p.row_tiles;
+    const int head = (int)(key_head % a.c.kv_heads) * a.group + (real ? y / p.row_tiles : 0);
+    const int row0 = real ? y % p.row_tiles * 32 : 0;
+    const uint16_t* const q = static_cast<const uint16_t*>(a.q) + head * a.q_head;
+    v4u* const to_q = reinterpret_cast<v4u*>(p.queries + x * (32 * D));
+#pragma unroll
+    for (int r = 0; r < 32 * D / 8 / 64; ++r) {
+      const int piece = lane + 64 * r;
+      const int row = unit * a.R + min(row0 + piece / (D / 8), a.R - 1);
+      to_q[piece] = *reinterpret_cast<const v4u*>(q + row * a.q_row + piece % (D / 8) * 8);
+    }
+    const int at = row0 + (lane & 31), row = unit * a.R + min(at, a.R - 1);
+    const float lse = p.lse[(int64_t)row * a.heads + head];
     int s, e;
     row_range(a, row, s, e);
-    const bool adds = at < a.R && s < e && lse != -__builtin_inff();
+    const bool adds = real && at < a.R && s < e && lse != -__builtin_inff();
     const float to = lse * kLog2e;
-    p.columns[x * 32 + (lane & 31)] = adds ? float2{to, lacking(lse, to)} : float2{0.f, 0.f};
+    if (lane < 32)
+      p.columns[x * 32 + lane] = adds ? float2{to, lacking(lse, to)} : float2{0.f, 0.f};
     int4 m{adds ? s : a.c.cap, adds ? e : 0, adds ? s : a.c.cap, adds ? e : 0};
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -167,8 +183,27 @@ __global__ __launch_bounds__(256) void weigh_columns_kernel(WeighParams p, int b
       m.z = min(m.z, __shfl_xor(m.z, o, 64));
       m.w = max(m.w, __shfl_xor(m.w, o, 64));
     }
-    if ((lane & 31) == 0) p.sight[x] = m;
+    if (lane == 0) p.sight[x] = m;
   }
+}
+
+// Zeros made here and now: a vector of them would be kept in registers through all loops.
+__device__ __forceinline__ v16f fresh_zeros() {
+  v16f z;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float x;
+    asm volatile("v_mov_b32 %0, 0" : "=v"(x));
+    z[e] = x;
+  }
+  return z;
+}
+
+// The lane's number, formed anew: addresses made of it are not kept (and spilled).
+__device__ __forceinline__ int lane_again() {
+  int lane;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(lane));
+  return lane;
 }
 
 // A wave holds 64 keys of one key head, widened, in registers as the first operand of
@@ -189,117 +224,131 @@ __global__ __launch_bounds__(512, 2) void weigh_wide_kernel(WeighParams p) {
   const KvCache& c = a.c;
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int hh = lane >> 5, n = lane & 31;
-  const int unit = blockIdx.x / p.tiles, g0 = blockIdx.x % p.tiles;
+  const int request = blockIdx.x / p.tiles, g0 = blockIdx.x % p.tiles;
+  const int unit_row = request * a.R;
   __shared__ __align__(16) uint8_t s_q[2][COLS * QROW];
 
-  const int4 cut = p.cut[2 * unit];
+  const int4 cut = p.cut[2 * request];
   const int first = __builtin_amdgcn_readfirstlane(cut.x);
   const int tiles = __builtin_amdgcn_readfirstlane(cut.y);
   const int shares = __builtin_amdgcn_readfirstlane(cut.z);
-  const int hi = __builtin_amdgcn_readfirstlane(p.cut[2 * unit + 1].y);
-  const int subs = a.group * p.row_tiles;  // tiles of columns of a key head
-  const int per_head = (subs + 1) / 2, all = per_head * c.kv_heads;
+  const int hi = __builtin_amdgcn_readfirstlane(p.cut[2 * request + 1].y);
+  const int per_head = (a.group * p.row_tiles + 1) / 2, all = per_head * c.kv_heads;
   const int share = (all + shares - 1) / shares;
   const float cs = a.scale * kLog2e;
-  const int32_t* const table = c.table + (int64_t)unit * c.table_stride;
-  const int64_t tile0 = (int64_t)unit * a.heads * p.row_tiles;
+  const int32_t* const table = c.table + (int64_t)request * c.table_stride;
+  // what lies behind a request's last stage is read (and not used): the workspace goes on
+  const v4u* const queries =
+      reinterpret_cast<const v4u*>(p.queries + (int64_t)request * all * (COLS * D));
+  const float2* const columns = p.columns + (int64_t)request * all * COLS;
+  const int* const sight = reinterpret_cast<const int*>(p.sight + (int64_t)request * all * 2);
 
-  // A stage: tiles y and y + 1 of key head h's columns (the last one may be missing).
-  struct Stage {
-    int h, y;
-  };
-  auto next = [&](Stage x) {
-    const bool over = x.y + 2 >= subs;
-    return Stage{over ? x.h + 1 : x.h, over ? 0 : x.y + 2};
-  };
-  auto tile_of = [&](const Stage& x, int sub) {  // clamped into the key head's
-    return min(x.h, c.kv_heads - 1) * subs + min(x.y + sub, subs - 1);
-  };
   v4u q_reg[EACH];
-  auto load = [&](const Stage& x) {
+  auto load = [&](int x) {
 #pragma unroll
-    for (int r = 0; r < EACH; ++r) {
-      const int piece = t + 512 * r;
-      const int tile = tile_of(x, piece / (32 * D / 8));
-      const int head = tile / p.row_tiles;
-      const int row = unit * a.R +
-                      min(tile % p.row_tiles * 32 + piece % (32 * D / 8) / (D / 8), a.R - 1);
-      q_reg[r] = *reinterpret_cast<const v4u*>(static_cast<const uint16_t*>(a.q) + row * a.q_row +
-                                               head * a.q_head + piece % (D / 8) * 8);
-    }
+    for (int r = 0; r < EACH; ++r) q_reg[r] = (queries + (int64_t)x * (COLS * D / 8) + 512 * r)[t];
   };
   auto stage = [&](int buf) {
+    const int piece = wave * 64 + lane_again();
+    uint8_t* const to = s_q[buf] + piece / (D / 8) * QROW + piece % (D / 8) * 16;
 #pragma unroll
-    for (int r = 0; r < EACH; ++r) {
-      const int piece = t + 512 * r;
-      *reinterpret_cast<v4u*>(s_q[buf] + piece / (D / 8) * QROW + piece % (D / 8) * 16) = q_reg[r];
-    }
+    for (int r = 0; r < EACH; ++r)
+      *reinterpret_cast<v4u*>(to + 512 * r / (D / 8) * QROW) = q_reg[r];
   };
   // of a stage: its lane's column of either tile, and in lanes 0 .. 7 what its tiles see
   struct Known {
     float2 col[2];
     int sight;
   };
-  auto know = [&](const Stage& x) {
-    Known k;
-#pragma unroll
-    for (int sub = 0; sub < 2; ++sub)
-      k.col[sub] = p.columns[(tile0 + tile_of(x, sub)) * 32 + n];
-    k.sight = reinterpret_cast<const int*>(
-        p.sight + tile0 + tile_of(x, lane >> 2 & 1))[lane & 3];
-    return k;
+  auto know = [&](int x) {
+    const float2* const at = columns + (int64_t)x * COLS;
+    return Known{{at[n], (at + 32)[n]}, (sight + (int64_t)x * 8)[lane & 7]};
   };
 
   int count = 0;  // of stages: which buffer
   for (int item = g0; item < tiles * shares; item += p.tiles) {
     const int x_lo = item / tiles * share, x_hi = min(x_lo + share, all);
     const int pos0 = first + item % tiles * kWeighKeys + wave * 64;
-    float acc[2][16];
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[b][e] = 0.f;
+    v16f acc[2] = {fresh_zeros(), fresh_zeros()};
     v4u kf[2][KS];
     float f[2][2];
-    int at_head = -1;
-    v16f late = v16f{};
-    float2 last{0.f, 0.f};
-    bool pending = false;
-    auto add = [&](int b, const v16f& s, const float* by_block, const float2& col) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        acc[b][e] = __builtin_fmaf(
-            __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], by_block[e >> 3], -col.x)), col.y,
-            acc[b][e]);
-    };
-    auto flush = [&]() {
-      if (pending) add(1, late, f[1], last);
-      pending = false;
-    };
+    // piece k of this lane's operands of a tile of columns
     v4u q[KS];
-    auto take_q = [&](int buf, int sub) {
-      const uint8_t* const from = s_q[buf] + (32 * sub + n) * QROW + 32 * hh;
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-        q[k] = *reinterpret_cast<const v4u*>(from + 64 * (k >> 1) + 16 * (k & 1));
+    const uint8_t* q_from;
+    auto take_from = [&](int buf, int sub) {
+      const int l = lane_again();
+      q_from = s_q[buf] + (32 * sub + (l & 31)) * QROW + (l & 32);
     };
-    auto products = [&](v16f& s, int b) {
-      s = v16f{};
-#pragma unroll
-      for (int k = 0; k < KS; ++k) s = mfma32<T>(kf[b][k], q[k], s);
+    auto take = [&](int k) {
+      q[k] = *reinterpret_cast<const v4u*>(q_from + 64 * (k >> 1) + 16 * (k & 1));
     };
+    // The products of a unit, s = keys b x q, one at a time, each beside a part of the
+    // exponentials of another, pb and pc's keys and column, in the order written (the
+    // compiler's own puts products behind products: 632 us for those 2048 rows).
+    // `beside` comes after product k.
+    auto unit = [&](v16f& s, int b, const v16f& prev, int pb, const float* pf, const float2& pc,
+                    auto beside) {
+      constexpr int E = 16 / KS;
+      float arg[E], ex[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) arg[i] = __builtin_fmaf(prev[i], pf[0], -pc.x);
+#pragma unroll
+      for (int k = 0; k <= KS; ++k) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (k < KS) {
+          s = mfma32<T>(kf[b][k], q[k], k ? s : v16f{});
+          beside(k);
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          if (k > 0) {
+            const int e = (k - 1) * E + i;
+            float sum = __builtin_fmaf(ex[i], pc.y, acc[pb][e]);
+            asm volatile("" : "+v"(sum));  // (used behind a branch only: it would go there)
+            acc[pb][e] = sum;
+          }
+          if (k < KS) ex[i] = __builtin_amdgcn_exp2f(arg[i]);
+          if (k + 1 < KS) {
+            const int e = (k + 1) * E + i;
+            arg[i] = __builtin_fmaf(prev[e], pf[e >> 3], -pc.x);
+          }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto nothing = [](int) {};
     if (x_lo >= x_hi) continue;  // (the join reads no such share)
-    Stage now{x_lo / per_head, x_lo % per_head * 2}, ahead = next(now);
-    load(now);
+    load(x_lo);
     stage(count & 1);
-    load(ahead);
-    Known known = know(now);
+    load(x_lo + 1);
+    Known known = know(x_lo);
     __syncthreads();
-    for (int x = x_lo; x < x_hi; ++x, ++count) {
-      const int buf = count & 1;
-      if (now.h != at_head) {
-        flush();
-        at_head = now.h;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      if (k == 0) take_from(count & 1, 0);
+      take(k);
+    }
+    int x = x_lo;
+    Known then;
+    auto begin = [&]() {  // of a stage: the next one on its way
+      then = know(x + 1);
+      stage(~count & 1);  // (the other buffer was last read before the last barrier)
+      load(x + 2);
+    };
+    auto end = [&]() {
+      known = then;
+      ++x;
+      ++count;
+    };
+    auto word = [&](int i) { return __builtin_amdgcn_readlane(known.sight, i); };
+    auto plain = [&]() {  // every column sees every key
+      return max(word(0), word(4)) <= pos0 && min(word(1), word(5)) >= pos0 + 64;
+    };
+    int head_end = x_lo;  // the stage where another key head begins
+    while (x < x_hi) {
+      if (x == head_end) {
+        const int at_head = x / per_head;
+        head_end = (at_head + 1) * per_head;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const int pos = min(pos0 + 32 * b + n, ((hi - 1) & ~15) + (n & 15));
@@ -317,68 +366,83 @@ __global__ __launch_bounds__(512, 2) void weigh_wide_kernel(WeighParams p) {
               *reinterpret_cast<const float*>(page + scale_at(c, 0, at_head, slot)) * cs;
           f[b][0] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale), 0));
           f[b][1] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(scale), 16));
+          __builtin_amdgcn_sched_barrier(0);  // (registers are few)
         }
       }
-      auto word = [&](int i) { return __builtin_amdgcn_readlane(known.sight, i); };
-      const Known then = know(ahead);
-      const Stage after = next(ahead);
-      if (max(word(0), word(4)) <= pos0 && min(word(1), word(5)) >= pos0 + 64 && now.y + 1 < subs) {
-        // every column sees every key
-        const float late_f[2] = {pending ? f[1][0] : 0.f, pending ? f[1][1] : 0.f};
-        if (!pending) {
-          late = v16f{};
-          last = float2{0.f, 0.f};
-        }
-        v16f s0, s1;
-        take_q(buf, 0);
-        products(s0, 0);
-        add(1, late, late_f, last);
-        products(s1, 1);
-        add(0, s0, f[0], known.col[0]);
-        take_q(buf, 1);
-        stage(buf ^ 1);
-        products(s0, 0);
-        add(1, s1, f[1], known.col[0]);
-        load(after);
-        products(late, 1);
-        add(0, s0, f[0], known.col[1]);
-        last = known.col[1];
-        pending = true;
-      } else {
-        flush();
-        stage(buf ^ 1);
-        load(after);
+      if (plain()) {
+        // a loop of its own, whose sums stay in place; `late`: the scores whose
+        // exponentials are still to be taken (at first none: a factor of 0)
+        v16f late = fresh_zeros();
+        float2 last{0.f, 0.f};
+        float late_f[2] = {0.f, 0.f};
+        do {
+          const int buf = count & 1;
+          v16f s0, s1;
+          begin();
+          unit(s0, 0, late, 1, late_f, last, nothing);
+          unit(s1, 1, s0, 0, f[0], known.col[0], [&](int k) {
+            if (k == 0) take_from(buf, 1);
+            take(k);
+          });
+          unit(s0, 0, s1, 1, f[1], known.col[0], nothing);
+          __syncthreads();
+          unit(late, 1, s0, 0, f[0], known.col[1], [&](int k) {
+            if (k == 0) take_from(buf ^ 1, 0);
+            take(k);
+          });
+          last = known.col[1];
+          late_f[0] = f[1][0];
+          late_f[1] = f[1][1];
+          end();
+        } while (x < min(x_hi, head_end) && plain());
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          acc[1][e] = __builtin_fmaf(
+              __builtin_amdgcn_exp2f(__builtin_fmaf(late[e], late_f[e >> 3], -last.x)), last.y,
+              acc[1][e]);
+        continue;
+      }
+      const int buf = count & 1;
+      begin();
 #pragma unroll 1
-        for (int sub = 0; sub < 2; ++sub) {
-          if (word(4 * sub + 3) <= pos0 || word(4 * sub + 2) >= pos0 + 64 || now.y + sub >= subs)
-            continue;
-          const float2 col = sub ? known.col[1] : known.col[0];
-          const int tile = tile_of(now, sub), at = tile % p.row_tiles * 32 + n;
-          int s, e;
-          row_range(a, unit * a.R + min(at, a.R - 1), s, e);
-          if (at >= a.R || col.y == 0.f) s = e = 0;  // (adds nothing)
-          take_q(buf, sub);
+      for (int sub = 0; sub < 2; ++sub) {
+        if (sub) {
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const uint32_t sees = seen_bits(pos0 + 32 * b, s, e) >> (4 * hh);
-            v16f score;
-            products(score, b);
+          for (int k = 0; k < KS; ++k) {
+            if (k == 0) take_from(buf, 1);
+            take(k);
+          }
+        }
+        if (word(4 * sub + 3) <= pos0 || word(4 * sub + 2) >= pos0 + 64) continue;
+        const float2 col = sub ? known.col[1] : known.col[0];
+        int column = n, s, e;
+        asm("" : "+v"(column));  // (nothing of this is kept in the other loop)
+        const int at = (x % per_head * 2 + sub) % p.row_tiles * 32 + column;
+        row_range(a, unit_row + min(at, a.R - 1), s, e);
+        if (at >= a.R || col.y == 0.f) s = e = 0;  // (adds nothing)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float w =
-                  __builtin_amdgcn_exp2f(__builtin_fmaf(score[i], f[b][i >> 3], -col.x));
-              acc[b][i] += or_zero(w * col.y, bit(sees, 8 * (i >> 2) + (i & 3)));
-            }
+        for (int b = 0; b < 2; ++b) {
+          const uint32_t sees = seen_bits(pos0 + 32 * b, s, e) >> (4 * hh);
+          v16f score = v16f{};
+#pragma unroll
+          for (int k = 0; k < KS; ++k) score = mfma32<T>(kf[b][k], q[k], score);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float w =
+                __builtin_amdgcn_exp2f(__builtin_fmaf(score[i], f[b][i >> 3], -col.x));
+            acc[b][i] += or_zero(w * col.y, bit(sees, 8 * (i >> 2) + (i & 3)));
           }
         }
       }
-      known = then;
-      now = ahead;
-      ahead = after;
       __syncthreads();
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        if (k == 0) take_from(buf ^ 1, 0);
+        take(k);
+      }
+      end();
     }
-    flush();
-    float* const part = p.part + ((int64_t)unit * p.slots + item) * kWeighKeys + wave * 64;
+    float* const part = p.part + ((int64_t)request * p.slots + item) * kWeighKeys + wave * 64;
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -396,7 +460,7 @@ __global__ __launch_bounds__(256) void weigh_join_kernel(WeighParams p, int bloc
   const int unit = blockIdx.x / blocks;
   const int4 cut = p.cut[2 * unit], span = p.cut[2 * unit + 1];
   const int end = min(span.y, p.width);
-  const int all = (p.a.group * p.row_tiles + 1) / 2 * p.a.c.kv_heads;
+  const int all = (p.a.group * p.row_tiles + 1) / 2 * p.a.c.kv_heads;  // stages
   const int share = (all + cut.z - 1) / cut.z, shares = (all + share - 1) / share;
   for (int pos = cut.x + (blockIdx.x % blocks) * 256 + (int)threadIdx.x; pos < end;
        pos += blocks * 256) {
@@ -420,11 +484,12 @@ extern "C" int mqa_kv_weigh_launch(const mqa::WeighParams* p, hipStream_t s) {
     });
     return (int)hipGetLastError();
   }
-  const int64_t columns = (int64_t)p->a.requests * p->a.heads * p->row_tiles;
-  const int column_blocks = (int)((columns + 7) / 8 < 4096 ? (columns + 7) / 8 : 4096);
-  weigh_columns_kernel<<<dim3((unsigned)(p->a.requests + column_blocks)), 256, 0, s>>>(
-      *p, column_blocks);
+  const int64_t tiles = (int64_t)p->a.requests * p->a.c.kv_heads *
+                        ((p->a.group * (int64_t)p->row_tiles + 1) / 2 * 2);
+  const int column_blocks = (int)(tiles < 4 * 4096 ? (tiles + 3) / 4 : 4096);
   dispatch(p->a, [&](auto t, auto c, auto d) {
+    weigh_columns_kernel<d.value><<<dim3((unsigned)(p->a.requests + column_blocks)), 256, 0, s>>>(
+        *p, column_blocks);
     weigh_wide_kernel<t.value, c.value, d.value><<<grid, 512, 0, s>>>(*p);
   });
   const int cap = p->a.c.cap < p->width ? p->a.c.cap : p->width;

@@ -17,6 +17,7 @@ from .attend import (DTYPES, NO_WORKSPACE, KVLayout, _Cache, _cache, _dense, _he
                      _raise, _rows_per_request, _stream)
 
 EXPORTS = ("mqa_norm_rotate", "mqa_kv_weigh", "workspace_size_weigh", "mqa_kv_select",
+           "workspace_size_select",
            "mqa_kv_keep", "workspace_size_keep")
 
 
@@ -42,8 +43,10 @@ def _load() -> ctypes.CDLL:
         lib.mqa_kv_weigh.restype = I
         lib.workspace_size_weigh.argtypes = [I, I, I, I, I, I, I]
         lib.workspace_size_weigh.restype = SZ
-        lib.mqa_kv_select.argtypes = [P, I, P, I, I, I, P, P, P, I, P]
+        lib.mqa_kv_select.argtypes = [P, I, P, I, I, I, P, P, P, I, P, SZ, P]
         lib.mqa_kv_select.restype = I
+        lib.workspace_size_select.argtypes = [I, I]
+        lib.workspace_size_select.restype = SZ
         lib.mqa_kv_keep.argtypes = [C, P, P, P, I, I, P, SZ, P]
         lib.mqa_kv_keep.restype = I
         lib.workspace_size_keep.argtypes = [I, I, I, I, I]
@@ -172,7 +175,14 @@ def mqa_kv_weigh(layout: KVLayout, q, cache, page_table, starts, ends, lse, weig
     return weights
 
 
-def mqa_kv_select(weights, lengths, keep: int, sinks: int = 0, recent: int = 0, kept=None, stream=None):
+def workspace_size_select(requests: int, width: int) -> int:
+    """Bytes of workspace that suffice for every mqa_kv_select of up to so many requests and
+    weights of each."""
+    return int(_load().workspace_size_select(int(requests), int(width)))
+
+
+def mqa_kv_select(weights, lengths, keep: int, sinks: int = 0, recent: int = 0, kept=None,
+                  workspace=None, stream=None):
     """Which `keep` positions of each request stay: of its lengths[i] positions the first
     `sinks`, the last `recent` and the largest weights [requests, width] fp32 between them
     (equal ones: the smallest positions). Returns (positions [requests, keep] int32 in
@@ -197,9 +207,18 @@ def mqa_kv_select(weights, lengths, keep: int, sinks: int = 0, recent: int = 0, 
         s = _stream(dev, stream)
         positions = torch.empty((requests, keep), dtype=torch.int32, device=dev)
         counts = torch.empty(requests, dtype=torch.int32, device=dev)
-        rc = _load().mqa_kv_select(weights.data_ptr(), width, lengths.data_ptr(), keep, sinks, recent,
-                                   positions.data_ptr(), counts.data_ptr(),
-                                   None if kept is None else kept.data_ptr(), requests, s)
+        lib = _load()
+        if workspace is not None:
+            _workspace(workspace, dev)
+        else:
+            n = lib.workspace_size_select(requests, width)
+            if n > NO_WORKSPACE:
+                workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        rc = lib.mqa_kv_select(weights.data_ptr(), width, lengths.data_ptr(), keep, sinks, recent,
+                               positions.data_ptr(), counts.data_ptr(),
+                               None if kept is None else kept.data_ptr(), requests,
+                               None if workspace is None else workspace.data_ptr(),
+                               0 if workspace is None else workspace.numel(), s)
     _raise(rc, "mqa_kv_select")
     return positions, counts
 

@@ -99,12 +99,19 @@ size_t workspace_size_weigh(int requests, int R, int heads, int kv_heads, int he
  *   kept      dense [requests, width] fp32 or NULL, not overlapping weights: the chosen
  *             positions' weights in the same order, then 0 -- what mqa_kv_weigh goes on
  *             with after mqa_kv_keep
- *   keep, width in [1, MQA_MAX_KEYS], requests * keep <= MQA_MAX_KEPT, sinks and recent
- *   >= 0, sinks + recent <= keep; all pointers 4-B aligned
+ *   workspace >= workspace_size_select(requests, width) bytes, 256-B aligned, owned by the
+ *             call until the stream reaches its end; nothing needs clearing. NULL where that
+ *             is 256.
+ *   keep, width in [1, MQA_MAX_KEYS], requests in [1, MQA_MAX_ROWS], requests * keep <=
+ *   MQA_MAX_KEPT, sinks and recent >= 0, sinks + recent <= keep; other pointers 4-B aligned
  */
 int mqa_kv_select(const float* weights, int width, const int32_t* lengths, int keep, int sinks,
                   int recent, int32_t* positions, int32_t* counts, float* kept, int requests,
-                  void* stream);
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that suffice for every mqa_kv_select of up to so many requests and
+ * weights of each; 256 where none is needed, 0 for sizes out of range. */
+size_t workspace_size_select(int requests, int width);
 
 /*
  * Moves the first counts[i] (clamped to [0, width]) listed positions of request i to its

@@ -148,12 +148,12 @@ def weigh(c=None, **kw):
 
 def select(**kw):
     a = dict(weights=A16, width=256, lengths=A16, keep=64, sinks=4, recent=16, positions=A16, counts=A16,
-             kept=A16, requests=2)
+             kept=A16, requests=2, ws=WS, wsb=1 << 40)
     assert set(kw) <= set(a)
     a.update(kw)
     return S._load().mqa_kv_select(P(a["weights"]), a["width"], P(a["lengths"]), a["keep"], a["sinks"],
                                    a["recent"], P(a["positions"]), P(a["counts"]), P(a["kept"]),
-                                   a["requests"], None)
+                                   a["requests"], P(a["ws"]), a["wsb"], None)
 
 
 def keep(c=None, **kw):
@@ -183,6 +183,7 @@ def test_select_errors():
         assert select(**{name: 0}) == 1, name
         assert select(**{name: 0x10002}) == 2, name
     assert select(kept=0x10002) == 2
+    assert select(ws=0x20080) == 2
     for kw in (dict(width=0), dict(width=(1 << 20) + 1), dict(keep=0), dict(keep=(1 << 20) + 1), dict(sinks=-1),
                dict(recent=-1), dict(sinks=60, recent=5), dict(sinks=(1 << 31) - 1, recent=(1 << 31) - 1),
                dict(requests=0), dict(requests=(1 << 20) + 1), dict(requests=1 << 20, keep=65)):
@@ -205,3 +206,16 @@ def test_keep_errors():
     most = size(16, 4096, 8, 128, 64)
     for n, w in ((16, 4096), (1, 4096), (16, 1), (3, 777)):
         assert 0 < size(n, w, 8, 128, 64) <= most
+
+
+def test_workspaces_of_selection_serve_smaller_calls():
+    size = S._load().workspace_size_select
+    for bad in ((0, 1), (1, 0), ((1 << 20) + 1, 1), (1, (1 << 20) + 1)):
+        assert size(*bad) == 0, bad
+    assert size(1, 4096) == 256 and size(1 << 20, 4096) == 256 and size(1, 20000) > 256
+    for requests, width in ((1, 65536), (40, 20000), (600, 1 << 20), (511, 4097)):
+        most = size(requests, width)
+        for n in (1, 2, 3, 7, 8, 31, 40, 100, 256, 511, 512, 600):
+            for w in (1, 4096, 4097, 8192, 20000, 65536, 1 << 20):
+                if n <= requests and w <= width:
+                    assert size(n, w) <= most

@@ -262,6 +262,292 @@ void select(const SelectParams& p, int fillers, hipStream_t s) {
 }
 
 // -------------------------------------------------------------------- moving
+//
+// A moved block is made in three steps: its tokens' codes and scales are gathered, its
+// scale is found (the smallest power of two that holds the largest of them), and the
+// codes are written under it. Lists ascend and name no position before the first moved
+// one's place, so that a token's place is never behind its source. Hence what a
+// workgroup gathers for later blocks is still there when it has written the earlier ones,
+// and one that goes through a request's blocks in their order, of one head's keys or
+// values, can work in place: kv_move_kernel<DIRECT>. With too few requests and heads for
+// that, blocks are gathered by all workgroups at once into the workspace
+// (kv_move_kernel) and put in place by a second launch (kv_place_kernel).
+
+// What a block keeps, `bytes` codes, under its larger scale; thread t of `threads`.
+template <int C>
+__device__ __forceinline__ void round_again(uint8_t* codes, int bytes, float was, float scale, int t,
+                                            int threads) {
+  const float shrink = was * (1.f / scale);
+  constexpr int AHEAD = 8;  // reads on their way
+  for (int i0 = t; i0 < bytes / 8; i0 += AHEAD * threads) {
+    uint2 x[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (i0 + k * threads < bytes / 8) x[k] = *reinterpret_cast<uint2*>(codes + (i0 + k * threads) * 8);
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      if (i0 + k * threads >= bytes / 8) continue;
+      float v[8];
+      decode8<C>(x[k], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= shrink;
+      *reinterpret_cast<uint2*>(codes + (i0 + k * threads) * 8) = encode8<C>(v);
+    }
+  }
+}
+
+// A wave moves TOK tokens at a time (blocks of B <= 64): 16 codes a lane and read, every
+// read within one block. Its largest is sought among the codes themselves, four in a word,
+// and codes are rounded without regard to what is not finite, where neither a NaN nor an
+// overflow nor a scale that is no power of two is there.
+// The largest magnitude of 16 codes; odd: whether one is NaN.
+template <int C>
+__device__ __forceinline__ float largest_code(const uint4& code, bool& odd) {
+  typedef uint16_t U2 __attribute__((ext_vector_type(2)));
+  typedef int16_t I2 __attribute__((ext_vector_type(2)));
+  const uint32_t word[4] = {code.x, code.y, code.z, code.w};
+  if constexpr (C == kE4m3) {
+    // magnitudes are ordered as their bits
+    U2 lo{0, 0}, hi{0, 0};
+    uint32_t nan = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      lo = __builtin_elementwise_max(lo, __builtin_bit_cast(U2, word[k] & 0x007F007Fu));
+      hi = __builtin_elementwise_max(hi, __builtin_bit_cast(U2, word[k] & 0x7F007F00u));
+      nan |= (word[k] & 0x7F7F7F7Fu) + 0x01010101u;
+    }
+    odd |= (nan & 0x80808080u) != 0;
+    const U2 top = __builtin_elementwise_max(lo, (U2)(hi >> 8));
+    return __builtin_amdgcn_cvt_f32_fp8(max((int)top.x, (int)top.y), 0);
+  } else {
+    I2 most{0, 0}, least{0, 0};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const I2 hi = __builtin_bit_cast(I2, word[k] & 0xFF00FF00u);
+      const I2 lo = __builtin_bit_cast(I2, word[k]) << 8;
+      most = __builtin_elementwise_max(most, __builtin_elementwise_max(hi, lo));
+      least = __builtin_elementwise_min(least, __builtin_elementwise_min(hi, lo));
+    }
+    const int up = max((int)most.x, (int)most.y), down = min((int)least.x, (int)least.y);
+    return (float)(max(up, -down) >> 8);
+  }
+}
+
+// Four codes of scale s under the power of two 1 / inv, where all is finite and no result
+// is too large.
+template <int C>
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float s, float inv) {
+  if constexpr (C == kE4m3) {
+    float v[4] = {__builtin_amdgcn_cvt_f32_fp8((int)w, 0), __builtin_amdgcn_cvt_f32_fp8((int)w, 1),
+                  __builtin_amdgcn_cvt_f32_fp8((int)w, 2), __builtin_amdgcn_cvt_f32_fp8((int)w, 3)};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = v[j] * s * inv;
+    const int d = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], d, true);
+  } else {
+    // added to 1.5 * 2^23, a number is rounded to the integer in the sum's last byte
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      u[j] = __float_as_uint(
+          __builtin_fmaf((float)(int8_t)(w >> (8 * j)) * s, inv, 12582912.f));
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(u[3], u[2], 0x0C0C0400u),
+                                 __builtin_amdgcn_perm(u[1], u[0], 0x0C0C0400u), 0x05040100u);
+  }
+}
+
+template <int C, int D, int B, bool DIRECT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 4) void kv_move_kernel(KeepParams p) {
+  constexpr int TOK = 64, PER = D / 16, AT = 64 / PER;  // tokens a read
+  constexpr int NL = TOK / AT, LB = B / AT, NB = TOK / B;            // reads; of a block; blocks
+  const KvCache& c = p.c;
+  const int h = blockIdx.y, w = blockIdx.z, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int request = DIRECT ? blockIdx.x : blockIdx.x / p.chunks;
+  int count = p.counts[request];
+  count = count < 0 ? 0 : (count > p.width ? p.width : count);
+  const int64_t first = p.starts ? p.starts[request] : 0;
+  if (count == 0) return;
+  const int64_t begin = first & ~(int64_t)(B - 1);
+  const int kept = (int)(first - begin);  // tokens of the first block that stand before
+  const int32_t* const list = p.positions + (int64_t)request * p.width;
+  const int chunks = (kept + count + WAVES * TOK - 1) / (WAVES * TOK);
+
+  struct Held {
+    uint4 code[NL];
+    float s[NL];
+    uint32_t moves;  // bit i: read i's token does not stay where it is
+  };
+  // tokens of a chunk, from - kept ..: token 0's place is `first`
+  auto from_of = [&](int chunk) { return (chunk * WAVES + wave) * TOK - kept; };
+  auto fetch = [&](Held& f, int chunk) {
+    // (what has no place or no source is read from some page, and cleared)
+    int pos[NL], page[NL];
+    uint32_t none = 0;  // bit i: read i stands for zeros
+    f.moves = 0;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const int t = from_of(chunk) + i * AT + lane / PER;
+      pos[i] = list[min(max(t, 0), count - 1)];
+      const bool real = t >= 0 && t < count;
+      f.moves |= (real && pos[i] != first + t ? 1u : 0u) << i;
+      none |= (!real || pos[i] < 0 || pos[i] >= c.cap ? 1u : 0u) << i;
+    }
+    const int32_t* const table = c.table + (int64_t)request * c.table_stride;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      pos[i] = min(max(pos[i], 0), c.cap - 1);
+      page[i] = table[pos[i] >> c.page_shift];
+    }
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      none |= (page[i] < 0 || page[i] >= c.num_pages ? 1u : 0u) << i;
+      const uint8_t* const base =
+          c.pages + (int64_t)min(max(page[i], 0), c.num_pages - 1) * c.page_stride;
+      const int slot = pos[i] & ((1 << c.page_shift) - 1);
+      f.s[i] = *reinterpret_cast<const float*>(base + scale_at(c, w, h, slot));
+      f.code[i] = *reinterpret_cast<const uint4*>(base + code_at(c, w, h, slot) + lane % PER * 16);
+    }
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      if (none >> i & 1) {
+        f.s[i] = 0.f;
+        f.code[i] = uint4{0, 0, 0, 0};
+      }
+    }
+  };
+  // half k of read i, in loops that are not unrolled (what is seldom needed stays small)
+  auto half = [&](const Held& f, int i, int k, float& s) {
+    uint2 x{0, 0};
+    s = 0.f;
+#pragma unroll
+    for (int r = 0; r < NL; ++r) {
+      x.x = i == r ? (k ? f.code[r].z : f.code[r].x) : x.x;
+      x.y = i == r ? (k ? f.code[r].w : f.code[r].y) : x.y;
+      s = i == r ? f.s[r] : s;
+    }
+    return x;
+  };
+  // the block's new codes, in place of its old ones; its scale
+  auto round = [&](Held& f, int b, float was) {
+    // the largest magnitude among a lane's codes of a read, times its scale
+    float amax = 0.f;
+    bool odd = false;  // NaN or overflow
+#pragma unroll
+    for (int i = b * LB; i < (b + 1) * LB; ++i) {
+      const float a = largest_code<C>(f.code[i], odd) * f.s[i];
+      odd |= !(a >= 0.f && a < __builtin_inff());
+      amax = __builtin_fmaxf(amax, a);
+    }
+    const bool plain = !__any(odd);
+    if (!plain) {
+      amax = 0.f;
+#pragma unroll 1
+      for (int i = b * LB; i < (b + 1) * LB; ++i)
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          float v[8], s;
+          decode8<C>(half(f, i, k, s), v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float a = __builtin_fabsf(v[j] * s);
+            amax = a < __builtin_inff() ? __builtin_fmaxf(amax, a) : amax;
+          }
+        }
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o, 64));
+    const float fresh = __builtin_ldexpf(1.f, scale_exponent<C>(amax));
+    const float scale = fresh > was ? fresh : was, inv = 1.f / scale;
+    // (a kept scale may be any; a subnormal inverse would lose bits)
+    if (plain && (__float_as_uint(scale) & 0x807FFFFFu) == 0 && scale < 0x1p120f) {
+#pragma unroll
+      for (int i = b * LB; i < (b + 1) * LB; ++i) {
+        uint32_t* const word = &f.code[i].x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) word[k] = rescale4<C>(word[k], f.s[i], inv);
+      }
+    } else {
+#pragma unroll 1
+      for (int i = b * LB; i < (b + 1) * LB; ++i)
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          float v[8], s;
+          decode8<C>(half(f, i, k, s), v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = v[j] * s * inv;
+          const uint2 x = encode8<C>(v);
+#pragma unroll
+          for (int r = 0; r < NL; ++r) {
+            f.code[r].x = i == r && k == 0 ? x.x : f.code[r].x;
+            f.code[r].y = i == r && k == 0 ? x.y : f.code[r].y;
+            f.code[r].z = i == r && k == 1 ? x.x : f.code[r].z;
+            f.code[r].w = i == r && k == 1 ? x.y : f.code[r].w;
+          }
+        }
+    }
+    return scale;
+  };
+  // whether block b of a chunk has a place and something moves in it; its page and slot
+  struct Place {
+    uint8_t* base;
+    int slot, kept;
+    bool any;
+  };
+  auto place = [&](const Held& f, int chunk, int b) {
+    Place x{nullptr, 0, 0, false};
+    const int t = from_of(chunk) + b * B;  // of the block's first token
+    const int64_t at = first + t;
+    if (t >= count || at < 0 || at >= c.cap) return x;
+    if (!__any(f.moves >> (b * LB) & ((1ull << LB) - 1))) return x;
+    const int page = page_of(c, request, (int)at);
+    if (page < 0) return x;
+    return Place{c.pages + (int64_t)page * c.page_stride, (int)at & ((1 << c.page_shift) - 1),
+                 t < 0 ? -t : 0, true};
+  };
+
+  Held f;
+  for (int chunk = DIRECT ? 0 : blockIdx.x % p.chunks; chunk < chunks; ++chunk) {
+    fetch(f, chunk);
+    float scale[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const Place x = place(f, chunk, b);
+      const float was =
+          x.any && x.kept ? *reinterpret_cast<const float*>(x.base + scale_at(c, w, h, x.slot)) : 0.f;
+      scale[b] = x.any ? round(f, b, was) : 0.f;
+    }
+    if (DIRECT) __syncthreads();  // (every wave has what it gathers from these places)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const Place x = place(f, chunk, b);
+      if (!x.any) continue;
+      uint8_t* to;
+      if constexpr (DIRECT) {
+        to = x.base + code_at(c, w, h, x.slot);
+      } else {
+        const int64_t item =
+            (((int64_t)request * p.blocks + (chunk * WAVES + wave) * NB + b) * 2 + w) *
+                c.kv_heads + h;
+        to = p.codes + item * (B * D);
+        if (lane == 0) p.scales[item] = scale[b];
+      }
+#pragma unroll
+      for (int i = b * LB; i < (b + 1) * LB; ++i) {
+        const int t = from_of(chunk) + i * AT + lane / PER;
+        if (t >= 0 && t < count)
+          *reinterpret_cast<uint4*>(to + ((i - b * LB) * 64 + lane) * 16) = f.code[i];
+      }
+      if constexpr (DIRECT) {
+        float* const scale_p = reinterpret_cast<float*>(x.base + scale_at(c, w, h, x.slot));
+        const float was = x.kept ? *scale_p : 0.f;
+        if (x.kept && scale[b] > was) round_again<C>(to, x.kept * D, was, scale[b], lane, 64);
+        if (lane == 0 && !(x.kept && scale[b] == was)) *scale_p = scale[b];
+      }
+    }
+    if (!DIRECT) break;
+  }
+}
 
 constexpr int kKeepThreads = 256;
 
@@ -297,7 +583,8 @@ __device__ __forceinline__ bool target(const KeepParams& p, int block_index, Tar
   return __syncthreads_or(moves);
 }
 
-// Gathers a block's tokens: their values, the block's scale (the smallest power of two
+// kv_move_kernel's part for blocks of more than 64 tokens, a workgroup each, which reads
+// them twice. Gathers a block's tokens: their values, the block's scale (the smallest power of two
 // that holds the largest of them), and their codes under it, into the workspace.
 template <int C, int D>
 __global__ __launch_bounds__(kKeepThreads) void kv_gather_kernel(KeepParams p) {
@@ -365,7 +652,7 @@ __global__ __launch_bounds__(kKeepThreads) void kv_gather_kernel(KeepParams p) {
 // where its scale grew.
 template <int C, int D>
 __global__ __launch_bounds__(kKeepThreads) void kv_place_kernel(KeepParams p) {
-  constexpr int PER = D / 8;
+  constexpr int PER = D / 16;
   const KvCache& c = p.c;
   const int h = blockIdx.y, w = blockIdx.z;
   Target x;
@@ -380,19 +667,9 @@ __global__ __launch_bounds__(kKeepThreads) void kv_place_kernel(KeepParams p) {
   const uint8_t* const from = p.codes + item * ((int64_t)D << c.block_shift);
   __syncthreads();
   for (int i = threadIdx.x; i < (x.hi - x.lo) * PER; i += kKeepThreads)
-    *reinterpret_cast<uint2*>(to + x.kept * D + i * 8) =
-        *reinterpret_cast<const uint2*>(from + x.kept * D + i * 8);
-  if (x.kept && scale > was) {
-    const float shrink = was * (1.f / scale);
-    for (int i = threadIdx.x; i < x.kept * PER; i += kKeepThreads) {
-      uint2* const at = reinterpret_cast<uint2*>(to + i * 8);
-      float v[8];
-      decode8<C>(*at, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= shrink;
-      *at = encode8<C>(v);
-    }
-  }
+    *reinterpret_cast<uint4*>(to + x.kept * D + i * 16) =
+        *reinterpret_cast<const uint4*>(from + x.kept * D + i * 16);
+  if (x.kept && scale > was) round_again<C>(to, x.kept * D, was, scale, threadIdx.x, kKeepThreads);
   if (threadIdx.x == 0 && !(x.kept && scale == was)) *scale_p = scale;
 }
 
@@ -429,9 +706,29 @@ extern "C" int mqa_kv_select_launch(const mqa::SelectParams* p, hipStream_t s) {
 extern "C" int mqa_kv_keep_launch(const mqa::KeepParams* p, hipStream_t s) {
   using namespace mqa;
   dispatch(p->c, [&](auto c, auto d) {
+    auto move = [&](auto block) {
+      constexpr int B = block.value;
+      if (p->direct) {
+        // short lists: as many workgroups a compute unit as there are
+        const dim3 grid(p->requests, p->c.kv_heads, 2);
+        if (p->width + B <= 128)
+          kv_move_kernel<c.value, d.value, B, true, 2><<<grid, 128, 0, s>>>(*p);
+        else
+          kv_move_kernel<c.value, d.value, B, true, 16><<<grid, 1024, 0, s>>>(*p);
+      } else {
+        KeepParams all = *p;
+        all.chunks = (int)(((int64_t)p->blocks * B + 255) / 256);
+        kv_move_kernel<c.value, d.value, B, false, 4>
+            <<<dim3((unsigned)p->requests * all.chunks, p->c.kv_heads, 2), 256, 0, s>>>(all);
+      }
+    };
     const dim3 grid((unsigned)p->requests * p->blocks, p->c.kv_heads, 2);
-    kv_gather_kernel<c.value, d.value><<<grid, kKeepThreads, 0, s>>>(*p);
-    kv_place_kernel<c.value, d.value><<<grid, kKeepThreads, 0, s>>>(*p);
+    const int B = 1 << p->c.block_shift;
+    if (B == 16) move(std::integral_constant<int, 16>{});
+    if (B == 32) move(std::integral_constant<int, 32>{});
+    if (B == 64) move(std::integral_constant<int, 64>{});
+    if (B > 64) kv_gather_kernel<c.value, d.value><<<grid, kKeepThreads, 0, s>>>(*p);
+    if (!p->direct) kv_place_kernel<c.value, d.value><<<grid, kKeepThreads, 0, s>>>(*p);
   });
   return (int)hipGetLastError();
 }

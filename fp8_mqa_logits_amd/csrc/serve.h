@@ -45,6 +45,8 @@ struct KeepParams {
   const int32_t* counts;
   const int32_t* starts;  // nullptr: 0
   int width, requests, blocks;  // blocks of a request that moved tokens can fall into
+  bool direct;                  // in place, without the workspace
+  int chunks;
   // moved blocks on their way: codes [item][B][head_dim], scales [item], item =
   // ((request * blocks + block) * 2 + w) * kv_heads + head
   uint8_t* codes;

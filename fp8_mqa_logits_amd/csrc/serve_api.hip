@@ -70,10 +70,22 @@ SelectLayout select_layout(int requests, int width) {
   return a;
 }
 
+// Whether mqa_kv_keep works in place: a workgroup for the keys or the values of a
+// request's head, where these are enough to fill half the card or lists are so short that
+// none has more than two rounds to go.
+constexpr int kDirectGroups = 128;
+bool keep_direct(int requests, int width, int kv_heads, int block) {
+  return block <= 64 &&
+         ((int64_t)requests * kv_heads * 2 >= kDirectGroups || width + block <= 1024);
+}
+
 struct KeepLayout {
   size_t scales, total;
 };
 KeepLayout keep_layout(int requests, int width, int kv_heads, int head_dim, int block) {
+  KeepLayout none{};
+  none.total = kNoWorkspace;
+  if (keep_direct(requests, width, kv_heads, block)) return none;
   const size_t items = (size_t)requests * blocks_of(width, block) * 2 * kv_heads;
   KeepLayout a{};
   a.scales = (items * block * head_dim + 255) / 256 * 256;
@@ -118,8 +130,8 @@ int mqa_kv_weigh(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
   const WeighLayout l =
       weigh_layout(requests, R, heads, cache->kv_heads, cache->head_dim,
                    at_most_keys(positions_of(cache)));
-  if (l.wide && !workspace) return MQA_ERR_NULL;
-  if (l.wide && workspace_bytes < l.total)
+  if (!workspace && l.total > kNoWorkspace) return MQA_ERR_NULL;
+  if (workspace && workspace_bytes < l.total)
     return workspace_failed("the workspace is smaller than workspace_size_weigh()");
   WeighParams p{};
   p.a.c = kernel_cache(cache);
@@ -167,8 +179,8 @@ int mqa_kv_select(const float* weights, int width, const int32_t* lengths, int k
     return MQA_ERR_SHAPE;
   if (!current_device_cus()) return MQA_ERR_DEVICE;
   const SelectLayout l = select_layout(requests, width);
-  if (l.parts > 1 && !workspace) return MQA_ERR_NULL;
-  if (l.parts > 1 && workspace_bytes < l.total)
+  if (!workspace && l.total > kNoWorkspace) return MQA_ERR_NULL;
+  if (workspace && workspace_bytes < l.total)
     return workspace_failed("the workspace is smaller than workspace_size_select()");
   SelectParams p{};
   p.parts = l.parts;
@@ -197,7 +209,14 @@ size_t workspace_size_select(int requests, int width) {
 
 size_t workspace_size_keep(int requests, int width, int kv_heads, int head_dim, int block) {
   if (!keep_sizes_ok(requests, width) || page_bytes(kv_heads, head_dim, block, block) == 0) return 0;
-  return keep_layout(requests, width, kv_heads, head_dim, block).total;
+  // (more requests may need none)
+  int most = requests;
+  if (keep_direct(requests, width, kv_heads, block)) {
+    const int few = (kDirectGroups - 1) / (2 * kv_heads);
+    most = few < requests ? few : requests;
+    if (most < 1) return kNoWorkspace;
+  }
+  return keep_layout(most, width, kv_heads, head_dim, block).total;
 }
 
 int mqa_kv_keep(const mqa_kv_cache* cache, const int32_t* positions, const int32_t* counts,
@@ -213,8 +232,8 @@ int mqa_kv_keep(const mqa_kv_cache* cache, const int32_t* positions, const int32
   if (!current_device_cus()) return MQA_ERR_DEVICE;
   const KeepLayout a =
       keep_layout(requests, width, cache->kv_heads, cache->head_dim, cache->block);
-  if (!workspace) return MQA_ERR_NULL;
-  if (workspace_bytes < a.total)
+  if (!workspace && a.total > kNoWorkspace) return MQA_ERR_NULL;
+  if (workspace && workspace_bytes < a.total)
     return workspace_failed("the workspace is smaller than workspace_size_keep()");
   KeepParams p{};
   p.c = kernel_cache(cache);
@@ -224,6 +243,7 @@ int mqa_kv_keep(const mqa_kv_cache* cache, const int32_t* positions, const int32
   p.width = width;
   p.requests = requests;
   p.blocks = (int)blocks_of(width, cache->block);
+  p.direct = a.total == kNoWorkspace;
   p.codes = static_cast<uint8_t*>(workspace);
   p.scales = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + a.scales);
   const int err = mqa_kv_keep_launch(&p, static_cast<hipStream_t>(stream));

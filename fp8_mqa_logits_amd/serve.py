@@ -248,13 +248,15 @@ def mqa_kv_keep(layout: KVLayout, cache, page_table, positions, counts, starts=N
     lib = _load()
     with _launch(dev, stream):
         s = _stream(dev, stream)
-        if workspace is None:
-            n = lib.workspace_size_keep(requests, width, layout.kv_heads, layout.head_dim, layout.block)
-            workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
-        else:
+        if workspace is not None:
             _workspace(workspace, dev)
+        else:
+            n = lib.workspace_size_keep(requests, width, layout.kv_heads, layout.head_dim, layout.block)
+            if n > NO_WORKSPACE:
+                workspace = torch.empty(n, dtype=torch.uint8, device=dev)
         rc = lib.mqa_kv_keep(c, positions.data_ptr(), counts.data_ptr(),
                              None if starts is None else starts.data_ptr(), width, requests,
-                             workspace.data_ptr(), workspace.numel(), s)
+                             None if workspace is None else workspace.data_ptr(),
+                             0 if workspace is None else workspace.numel(), s)
     _raise(rc, "mqa_kv_keep")
     return cache

@@ -124,7 +124,7 @@ size_t workspace_size_select(int requests, int width);
  *   positions [requests, width] int32, counts and starts [requests] int32, 4-B aligned
  *   workspace >= workspace_size_keep(requests, width, kv_heads, head_dim, block) bytes,
  *             256-B aligned, owned by the call until the stream reaches its end; nothing
- *             needs clearing
+ *             needs clearing. NULL where that is 256.
  *   width in [1, MQA_MAX_KEYS], requests in [1, MQA_MAX_ROWS], requests * width <=
  *   MQA_MAX_KEPT
  */
@@ -132,8 +132,8 @@ int mqa_kv_keep(const mqa_kv_cache* cache, const int32_t* positions, const int32
                 const int32_t* starts, int width, int requests, void* workspace,
                 size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace of an mqa_kv_keep of up to so many requests and listed positions; 0
- * for sizes out of range. */
+/* Bytes of workspace that suffice for every mqa_kv_keep of up to so many requests and
+ * listed positions; 256 where none is needed, 0 for sizes out of range. */
 size_t workspace_size_keep(int requests, int width, int kv_heads, int head_dim, int block);
 
 #ifdef __cplusplus

@@ -199,7 +199,8 @@ def test_keep_errors():
         assert keep(**kw) == 3, kw
     assert keep(cache(head_dim=96)) == 3
     size = S._load().workspace_size_keep
-    assert size(1, 1, 1, 64, 16) >= 2 * 16 * 64
+    assert size(1, 5000, 1, 64, 16) >= 2 * 5000 * 64 and size(64, 5000, 8, 64, 16) >= 7 * 5000 * 8 * 64
+    assert size(1, 100, 1, 64, 16) == 256
     for bad in ((0, 1, 1, 64, 16), (1, 0, 1, 64, 16), (1, 1, 0, 64, 16), (1, 1, 1, 96, 16), (1, 1, 1, 64, 8),
                 (1, 1, 1, 64, 48), (1 << 20, 65, 1, 64, 16)):
         assert size(*bad) == 0, bad

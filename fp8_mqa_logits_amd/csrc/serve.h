@@ -10,7 +10,8 @@ struct WeighParams {
   const float* lse;  // [rows][heads]
   float* weights;    // [requests][width]
   int width;
-  int tiles;  // workgroups of a request
+  int tiles;   // workgroups of a request
+  bool split;  // few columns: waves share keys
   // Many columns, tile by tile of 32 (row_tiles for a query head's rows, an even number
   // for a key head's): the queries [tile][32][head_dim]; {lse', its factor} [tile][32];
   // {largest start, smallest end, smallest start, largest end} [tile]. The sums of a

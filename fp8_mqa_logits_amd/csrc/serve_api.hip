@@ -160,9 +160,13 @@ int mqa_kv_weigh(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
   p.part = reinterpret_cast<float*>(base + l.part);
   p.sight = reinterpret_cast<int4*>(base + l.sight);
   p.cut = reinterpret_cast<int4*>(base + l.cut);
-  const int keys = cache->kv_heads >= 4 ? 32 : cache->kv_heads >= 2 ? 64 : 128;
-  const int most = (p.a.c.cap + keys - 1) / keys, share = 16 * cus / requests;
-  if (!l.wide) p.tiles = most < share ? most : share < 1 ? 1 : share;
+  if (!l.wide) {
+    // few columns: 256 keys a workgroup where that gives every compute unit four, else 64
+    p.split = (int64_t)requests * p.a.c.cap < (int64_t)4 * 256 * cus;
+    const int keys = p.split ? 64 : 256;
+    const int most = (p.a.c.cap + keys - 1) / keys, share = 16 * cus / requests;
+    p.tiles = most < share ? most : share < 1 ? 1 : share;
+  }
   const int err = mqa_kv_weigh_launch(&p, static_cast<hipStream_t>(stream));
   return err != 0 ? launch_failed(err) : MQA_OK;
 }

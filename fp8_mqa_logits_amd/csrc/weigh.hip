@@ -24,104 +24,147 @@ __device__ __forceinline__ float lacking(float lse, float to) {
   return __builtin_fabsf(to) < 3e38f ? by : 1.f;
 }
 
-// Few columns: a wave takes 32 keys of every HW-th key head, widened once for all
-// column tiles of 16; HW waves that share keys are joined through LDS.
-template <int T, int C, int D>
-__global__ __launch_bounds__(256, 4) void weigh_narrow_kernel(WeighParams p) {
+// The sum of 16 neighbouring lanes' values, in all of them.
+__device__ __forceinline__ float sum16(float x) {
+  auto add = [&](auto control) {
+    x += __int_as_float(
+        __builtin_amdgcn_update_dpp(0, __float_as_int(x), control.value, 0xF, 0xF, false));
+  };
+  add(std::integral_constant<int, 0xB1>{});   // lane ^ 1
+  add(std::integral_constant<int, 0x4E>{});   // lane ^ 2
+  add(std::integral_constant<int, 0x141>{});  // the other four of eight
+  add(std::integral_constant<int, 0x140>{});  // the other eight
+  return x;
+}
+
+// Few columns: a wave takes 64 keys, head by head, in the layout of attend_narrow.hip's
+// scores: lane (g, n) has those of keys 4 g + i of every 16 and column n. Bound by the
+// keys' bytes in long contexts, so that reads of several waves a SIMD are what counts.
+// SPLIT: the four waves of a workgroup share the keys, each with every fourth head, and
+// are joined through LDS; for calls with too few keys to give every wave its own.
+template <int T, int C, int D, bool SPLIT>
+__global__ __launch_bounds__(256, 3) void weigh_narrow_kernel(WeighParams p) {
   constexpr int KC = D / 64;  // 16-byte pieces of a key per lane
+  constexpr int HW = SPLIT ? 4 : 1, KEYS = SPLIT ? 64 : 256;  // of a workgroup
   const AttendParams& a = p.a;
   const KvCache& c = a.c;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, n = lane & 15;
   const int unit = blockIdx.x / p.tiles, tile = blockIdx.x % p.tiles;
   const int columns = a.R * a.group;
-  const int HW = c.kv_heads >= 4 ? 4 : c.kv_heads >= 2 ? 2 : 1, KW = 4 / HW;
-  const int hw = wave % HW, kb = wave / HW;
-  __shared__ float s_part[4][32];
+  __shared__ float s_part[SPLIT ? 4 : 1][64];
 
-  const Span span = uniform(row_span<kRange>(a, unit * a.R, a.R, lane, 64));
+  Span span;
+  if (a.R == 1) {
+    int s, e;
+    row_range(a, unit, s, e);
+    span = uniform(s < e ? Span{s, e, s, e, 0, 0} : Span{c.cap, 0, 0, c.cap, 0, 0});
+  } else {
+    span = uniform(row_span<kRange>(a, unit * a.R, a.R, lane, 64));
+  }
   const int first = span.lo & ~15;
   const float cs = a.scale * kLog2e;
-  const int32_t* const table = c.table + (int64_t)unit * c.table_stride;
+  const auto* const table = constant(c.table + (int64_t)unit * c.table_stride);
 
-  for (int at = first + tile * KW * 32; at < span.hi; at += p.tiles * KW * 32) {
-    const int pos0 = at + kb * 32;
-    float acc[8];
+  for (int at = first + tile * KEYS; at < span.hi; at += p.tiles * KEYS) {
+    const int pos0 = SPLIT ? at : at + wave * 64;
+    float acc[16];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+    for (int j = 0; j < 16; ++j) acc[j] = 0.f;
     if (pos0 < span.hi) {
-      const uint8_t* page[2];
-      int slot[2];
+      // 16 keys lie in one page and block: their page and scale are scalars (behind the
+      // last position that some row sees: the last ones again, masked)
+      const uint8_t* page[4];
+      int slot[4];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < 4; ++b) {
         const int pos = min(pos0 + 16 * b, (span.hi - 1) & ~15);
         page[b] = c.pages + (int64_t)clamp_page(c, table[pos >> c.page_shift]) * c.page_stride;
         slot[b] = pos & ((1 << c.page_shift) - 1);
       }
-      const bool clean = pos0 >= span.in_lo && pos0 + 32 <= span.in_hi;
-      for (int h = hw; h < c.kv_heads; h += HW) {
-        v4u kf[2][2 * KC];
-        float f[2];
+      const bool clean = pos0 >= span.in_lo && pos0 + 64 <= span.in_hi;
+      v4u raw[4][KC], q[2 * KC];
+      float f[4], lse;
+      auto load_k = [&](int b, int h) {
+        const uint8_t* const k = page[b] + code_at(c, 0, h, slot[b]) + n * D + 16 * g;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const uint8_t* const k = page[b] + code_at(c, 0, h, slot[b]) + n * D + 16 * g;
+        for (int x = 0; x < KC; ++x) raw[b][x] = *reinterpret_cast<const v4u*>(k + 64 * x);
+        f[b] = *constant(reinterpret_cast<const float*>(page[b] + scale_at(c, 0, h, slot[b])));
+      };
+      auto row_of = [&](int col0) {
+        return unit * a.R + (col0 + n < columns ? (col0 + n) / a.group : 0);
+      };
+      auto load_q = [&](int h, int col0) {
+        const int row = row_of(col0);
+        const int head = h * a.group + (col0 + n < columns ? (col0 + n) % a.group : 0);
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head;
 #pragma unroll
-          for (int x = 0; x < KC; ++x) {
-            const v4u raw = *reinterpret_cast<const v4u*>(k + 64 * x);
-            kf[b][2 * x] = widen8<T, C>(raw[0], raw[1]);
-            kf[b][2 * x + 1] = widen8<T, C>(raw[2], raw[3]);
+        for (int k = 0; k < 2 * KC; ++k)
+          q[k] = *reinterpret_cast<const v4u*>(src + 64 * (k >> 1) + 16 * g + 8 * (k & 1));
+        lse = p.lse[(int64_t)row * a.heads + head];
+      };
+      // a head's keys against 16 columns; what is read next takes the registers as soon as
+      // they are free: the next columns, or the next head's keys and first columns
+      auto step = [&](auto is_last, int h, int col0) {
+        const float to = lse * kLog2e, by = lacking(lse, to);
+        int s, e;
+        row_range(a, row_of(col0), s, e);
+        const uint32_t adds =
+            col0 + n < columns && s < e && lse != -__builtin_inff() ? ~0u : 0u;
+        const int h_next = min(h + HW, c.kv_heads - 1);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const float by_block = f[b] * cs;
+          v4f x = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < KC; ++k) {
+            x = mfma<T>(widen8<T, C>(raw[b][k][0], raw[b][k][1]), q[2 * k], x);
+            x = mfma<T>(widen8<T, C>(raw[b][k][2], raw[b][k][3]), q[2 * k + 1], x);
           }
-          f[b] = *reinterpret_cast<const float*>(page[b] + scale_at(c, 0, h, slot[b])) * cs;
-        }
-        for (int col0 = 0; col0 < columns; col0 += 16) {
-          const int col = col0 + n;
-          const bool real = col < columns;
-          const int row = unit * a.R + (real ? col / a.group : 0);
-          const int head = h * a.group + (real ? col % a.group : 0);
-          const uint16_t* src =
-              static_cast<const uint16_t*>(a.q) + row * a.q_row + head * a.q_head;
-          v4u q[2 * KC];
+          if (is_last.value) load_k(b, h_next);
+          if (b == 3) load_q(is_last.value ? h_next : h, is_last.value ? 0 : col0 + 16);
+          const uint32_t sees = clean ? adds : adds & (seen_bits(pos0 + 16 * b, s, e) >> (4 * g));
 #pragma unroll
-          for (int k = 0; k < 2 * KC; ++k)
-            q[k] = *reinterpret_cast<const v4u*>(src + 64 * (k >> 1) + 16 * g + 8 * (k & 1));
-          const float lse = p.lse[(int64_t)row * a.heads + head];
-          const float to = lse * kLog2e;
-          const float by = lacking(lse, to);
-          int s, e;
-          row_range(a, row, s, e);
-          uint32_t sees = real && lse != -__builtin_inff() ? ~0u : 0u;
-          if (!clean) sees &= seen_bits(pos0, s, e);
-          sees >>= 4 * g;
-          if (s >= e) sees = 0;
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            v4f x = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < 2 * KC; ++k) x = mfma<T>(kf[b][k], q[k], x);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], f[b], -to)) * by;
-              acc[4 * b + i] += or_zero(w, bit(sees, 16 * b + i));
-            }
+          for (int i = 0; i < 4; ++i) {
+            const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], by_block, -to)) * by;
+            acc[4 * b + i] += or_zero(w, bit(sees, i));
           }
         }
+      };
+      const int h0 = SPLIT ? wave : 0;
+      if (h0 < c.kv_heads) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) load_k(b, h0);
+        load_q(h0, 0);
+      }
+      for (int h = h0; h < c.kv_heads; h += HW) {
+        int col0 = 0;
+        for (; col0 + 16 < columns; col0 += 16) step(std::false_type{}, h, col0);
+        step(std::true_type{}, h, col0);
       }
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 16; ++j) acc[j] = sum16(acc[j]);
+    float* const weights = p.weights + (int64_t)unit * p.width;
+    auto put = [&](int key, float sum) {
+      const int pos = pos0 + key;
+      if (pos >= span.lo && pos < span.hi && pos < p.width) weights[pos] += sum;
+    };
+    if constexpr (SPLIT) {
 #pragma unroll
-      for (int o = 1; o < 16; o <<= 1) acc[j] += __shfl_xor(acc[j], o, 64);
-      if (n == 0) s_part[wave][16 * (j >> 2) + 4 * g + (j & 3)] = acc[j];
+      for (int j = 0; j < 16; ++j)
+        if (n == j) s_part[wave][16 * (j >> 2) + 4 * g + (j & 3)] = acc[j];
+      __syncthreads();
+      if (wave == 0)
+        put(lane, s_part[0][lane] + s_part[1][lane] + s_part[2][lane] + s_part[3][lane]);
+      __syncthreads();
+    } else {
+      // lane (g, n): key 16 (n / 4) + 4 g + n % 4
+      float sum = acc[0];
+#pragma unroll
+      for (int j = 1; j < 16; ++j) sum = n == j ? acc[j] : sum;
+      put(16 * (n >> 2) + 4 * g + (n & 3), sum);
     }
-    __syncthreads();
-    if ((int)threadIdx.x < 32 * KW) {
-      const int k = threadIdx.x / 32, pos = at + threadIdx.x;
-      float sum = 0.f;
-      for (int w = 0; w < HW; ++w) sum += s_part[k * HW + w][threadIdx.x % 32];
-      if (pos >= span.lo && pos < span.hi && pos < p.width)
-        p.weights[(int64_t)unit * p.width + pos] += sum;
-    }
-    __syncthreads();
   }
 }
 
@@ -480,7 +523,10 @@ extern "C" int mqa_kv_weigh_launch(const mqa::WeighParams* p, hipStream_t s) {
   const dim3 grid((unsigned)p->a.requests * p->tiles);
   if (!p->wide) {
     dispatch(p->a, [&](auto t, auto c, auto d) {
-      weigh_narrow_kernel<t.value, c.value, d.value><<<grid, 256, 0, s>>>(*p);
+      if (p->split)
+        weigh_narrow_kernel<t.value, c.value, d.value, true><<<grid, 256, 0, s>>>(*p);
+      else
+        weigh_narrow_kernel<t.value, c.value, d.value, false><<<grid, 256, 0, s>>>(*p);
     });
     return (int)hipGetLastError();
   }

@@ -312,7 +312,7 @@ def run_own(state):
         return {"out": out, "lse": lse}
     if case["op"] == "weigh":
         return {"weights": mqa.mqa_kv_weigh(layout, s["q"], s["cache"], s["table"], s["starts"],
-                                            s["ends"], s["lse"], s["weights"])}
+                                            s["ends"], s["lse"].contiguous(), s["weights"])}
     if case["op"] == "evict":
         listed, count = mqa.mqa_kv_select(s["weights"], s["lens"], case["keep"], case["sinks"],
                                           case["recent"], kept=s["kept"])

@@ -28,6 +28,7 @@ struct WeighParams {
 
 // Tiles of keys that a workgroup of the wide kernel takes.
 constexpr int kWeighKeys = 512;
+constexpr int kWeighRounds = 4;  // of workgroups, at most, unless there are more tiles
 
 struct SelectParams {
   const float* weights;  // [requests][width]

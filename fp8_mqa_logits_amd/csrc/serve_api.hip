@@ -17,8 +17,8 @@ int64_t blocks_of(int width, int block) {
 }
 
 // Calls of more columns (rows x query heads of a key head) run on the wide kernel.
-constexpr int kNarrowColumns = 64;
-constexpr int kWeighGroups = 1024;  // workgroups that the wide kernel's work is cut for
+constexpr int kNarrowColumns = 384;
+constexpr int kWeighGroups = 256;  // workgroups that the wide kernel's work is cut for
 
 struct WeighLayout {
   bool wide;
@@ -35,16 +35,16 @@ WeighLayout weigh_layout(int requests, int R, int heads, int kv_heads, int head_
   }
   const int keys = (positions + kWeighKeys - 1) / kWeighKeys;
   a.tiles = kWeighGroups / requests < 1 ? 1 : kWeighGroups / requests;
-  a.slots = keys > a.tiles ? keys : a.tiles;
+  a.slots = keys > kWeighRounds * a.tiles ? keys : kWeighRounds * a.tiles;
   a.row_tiles = (R + 31) / 32;
   const size_t tiles =
       (size_t)requests * kv_heads * ((heads / kv_heads * (size_t)a.row_tiles + 1) / 2 * 2);
   // (fewer requests have more workgroups each: never more than kWeighGroups in all)
-  const size_t slots = (size_t)requests * a.slots;
+  const size_t slots = (size_t)requests * a.slots, few = kWeighRounds * kWeighGroups;
   a.columns = tiles * 32 * head_dim * 2;
   a.sight = a.columns + tiles * 32 * sizeof(float2);
   a.part = a.sight + tiles * sizeof(int4);
-  a.cut = a.part + (slots > kWeighGroups ? slots : kWeighGroups) * kWeighKeys * 4;
+  a.cut = a.part + (slots > few ? slots : few) * kWeighKeys * 4;
   a.total = a.cut + (size_t)requests * 2 * sizeof(int4);
   return a;
 }

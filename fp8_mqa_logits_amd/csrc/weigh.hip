@@ -189,7 +189,17 @@ __global__ __launch_bounds__(256) void weigh_columns_kernel(WeighParams p, int b
     for (int w = 1; w < 4; ++w) span = join<kRange>(span, s_span[w]);
     const int first = span.lo & ~15, stages = per_head * a.c.kv_heads;
     const int tiles = span.hi > first ? (span.hi - first + kWeighKeys - 1) / kWeighKeys : 0;
-    p.cut[2 * unit] = int4{first, tiles, tiles > 0 ? min(max(p.tiles / tiles, 1), stages) : 1, 0};
+    // shares of a tile for up to kWeighRounds rounds of workgroups, in which a share takes
+    // the time of its stages and of a start and an end as long as six
+    int shares = 1, best = 0;
+    for (int k = 1; k <= kWeighRounds && tiles > 0; ++k) {
+      const int n = min(max(k * p.tiles / tiles, 1), stages);
+      const int cost = (tiles * n + p.tiles - 1) / p.tiles * ((stages + n - 1) / n + 6);
+      if (k > 1 && cost >= best) continue;
+      best = cost;
+      shares = n;
+    }
+    p.cut[2 * unit] = int4{first, tiles, shares, 0};
     p.cut[2 * unit + 1] = int4{span.lo, span.hi, 0, 0};
     return;
   }

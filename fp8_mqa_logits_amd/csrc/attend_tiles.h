@@ -322,24 +322,25 @@ struct Walk {
     else
       return first + st * STEP;
   }
-  // Where the 16 keys from `at` keys into step st are read: those that lie outside what
-  // some row sees, from the nearest that does not.
+  // Where the 16 keys from `at` keys into step st are read: those behind what some row
+  // sees, or before it, from the nearest that some row sees; what lies between the sinks
+  // and the windows (kWindow), as it is.
   __device__ __forceinline__ int read_pos(int st, int at) const {
     if constexpr (M == kWindow)
-      if (st < s_steps || span.hi <= span.lo)
-        return min(max(pos(st) + at, span.s_lo), span.s_hi - 1) & ~15;
-    return min(max(pos(st) + at, span.lo), span.hi - 1) & ~15;
+      return min(pos(st) + at, max(span.hi, span.s_hi) - 1) & ~15;
+    else
+      return min(max(pos(st) + at, span.lo), span.hi - 1) & ~15;
   }
   __device__ __forceinline__ bool inside(int at) const {  // every row sees keys at .. at + STEP - 1
     return at >= span.in_lo && at + STEP <= span.in_hi;
   }
-  __device__ __forceinline__ bool some(int at) const {  // position `at` is in what some rows see
-    return (at >= span.lo && at < span.hi) ||
-           (M == kWindow && at >= span.s_lo && at < span.s_hi);
+  // Position `at` is in what some rows see (kWindow: is not asked, as its values have no
+  // weight and are not NaN).
+  __device__ __forceinline__ bool some(int at) const {
+    return M == kWindow || (at >= span.lo && at < span.hi);
   }
   __device__ __forceinline__ uint32_t some_bits(int at) const {
-    return seen_bits(at, span.lo, span.hi) |
-           (M == kWindow ? seen_bits(at, span.s_lo, span.s_hi) : 0u);
+    return M == kWindow ? ~0u : seen_bits(at, span.lo, span.hi);
   }
 };
 

@@ -107,12 +107,15 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   const int per_split = (walk.steps + p.splits - 1) / p.splits;
   const int tile_lo = split * per_split;
   const int tiles = min(walk.steps - tile_lo, per_split);
-  const int base = __builtin_amdgcn_readfirstlane(walk.first + tile_lo * 64);
+  // Behind the sinks' tiles (kWindow) come the windows', `jump` positions further on.
+  const int base = __builtin_amdgcn_readfirstlane(
+      (M == kWindow && walk.s_steps > 0 ? walk.s_first : walk.first) + tile_lo * 64);
+  const int sink_tiles = M == kWindow ? walk.s_steps - tile_lo : 0;
+  const int jump = M == kWindow && walk.s_steps > 0
+                       ? walk.first - walk.s_first - walk.s_steps * 64 : 0;
+  const int last_pos = M == kWindow ? max(walk.span.hi, walk.span.s_hi) - 1 : 0;
   auto tile_pos = [&](int i) {
-    if constexpr (M == kWindow)
-      return walk.pos(tile_lo + i);
-    else
-      return base + i * 64;
+    return base + i * 64 + (M == kWindow && i >= sink_tiles ? jump : 0);
   };
 
   // staging: piece x = t + THREADS r of the keys is KB bytes of key x / (D /
@@ -136,7 +139,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
   asm("" : "+v"(zero));
   auto group_pos = [&](int i, int r) {
     if constexpr (M == kWindow)
-      return walk.read_pos(tile_lo + i, 16 * group(r));
+      return min(tile_pos(i) + 16 * group(r), last_pos) & ~15;
     else
       return min(max(base + i * 64 + 16 * group(r), walk.span.lo), walk.span.hi - 1) & ~15;
   };

@@ -265,8 +265,8 @@ def mqa_kv_read(layout: KVLayout, cache, page_table, starts, counts, rows_per_re
 def workspace_size_attend(requests: int, rows_per_request: int, heads: int, layout: KVLayout,
                           positions: int, device: int | None = None) -> int:
     """Bytes of workspace that suffice for every attention call of up to so many
-    requests, rows of each and positions (table_stride * page_size for
-    mqa_attend_paged, the list's width for mqa_attend_topk)."""
+    requests, rows of each and positions (table_stride * page_size; the list's
+    width for mqa_attend_topk)."""
     if device is None:
         device = torch.cuda.current_device()
     return int(_load().workspace_size_attend(int(requests), int(rows_per_request), int(heads),
@@ -317,9 +317,9 @@ def _attend(layout, q, cache, page_table, indices, starts, ends, scale, out, lse
         elif return_lse:
             lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
         if workspace is None:
+            kind = 1 if indices is not None else 2 if window is not None else 3 if mask is not None else 0
             n = lib.workspace_size_attend_call(requests, R, heads, layout.kv_heads,
-                                               layout.head_dim, positions,
-                                               int(indices is not None), dev.index)
+                                               layout.head_dim, positions, kind, dev.index)
             if n > NO_WORKSPACE:
                 workspace = torch.empty(n, dtype=torch.uint8, device=dev)
         else:

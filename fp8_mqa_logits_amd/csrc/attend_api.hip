@@ -75,6 +75,57 @@ Plan plan(int requests, int R, int heads, int kv_heads, int head_dim, int positi
   return a;
 }
 
+// The plan of windows and trees (window: what a row sees of the table's positions, 0: any
+// of them). Narrower tiles span fewer positions of their rows' windows and waste fewer
+// columns, wider ones take less time a column and key: a workgroup's time for a key, with
+// its compute unit full, was measured as `ns`, for heads of 64 and of 128 (tiles of 64
+// columns are the slowest a column). The time of a start and an end is that of 512 keys, of
+// 1024 for the wide tiles, as above. 2000 rows of 12 heads, each its own key head, through
+// 504 positions: 30 us on 32 columns, 73 on 256; 4096 rows of 32 heads on 4 key heads
+// through 1027: 129 on 256, 158 on 32.
+Plan fitted_plan(int requests, int R, int heads, int kv_heads, int head_dim, int positions,
+                 int window, int cus) {
+  static const struct {
+    int cols;
+    double ns[2];
+  } kTiles[] = {{16, {9, 18}}, {32, {14.4, 14.8}}, {128, {16.1, 39}}, {256, {19.7, 34}}};
+  Plan a{};
+  const int group = heads / kv_heads, columns = R * group, most = widest(columns, false);
+  const int64_t units = (int64_t)requests * kv_heads;
+  double best = 0;
+  int64_t slots = 0;
+  for (const auto& t : kTiles) {
+    if (t.cols > most) continue;
+    const int64_t tiles = (columns + t.cols - 1) / t.cols, n = units * tiles;
+    const int64_t room = resident(t.cols, head_dim, false, cus), ends = t.cols > 64 ? 1024 : 512;
+    const int64_t rows = (t.cols + group - 1) / group;
+    const int64_t span = window > 0 && window + rows < positions ? window + rows : positions;
+    for (int s = 1; s <= mqa::kMaxSplits && (s == 1 || s * 256 <= span); ++s) {
+      const int64_t rounds = (n * s + room - 1) / room;
+      if (s > 1 && rounds > kMostRounds) break;
+      const double cost =
+          t.ns[head_dim == 128] * (rounds * ((span + s - 1) / s + ends) + (s > 1 ? 2 * ends : 0));
+      if (a.cols > 0 && cost >= best) continue;
+      best = cost;
+      a.cols = t.cols;
+      a.tiles = (int)tiles;
+      a.splits = s;
+      slots = s > 1 ? n * s * t.cols : 0;
+    }
+  }
+  lay_out(a, slots, head_dim);
+  return a;
+}
+
+// kind: 0 ranges, 1 lists, 2 windows (positions: of a row's, and those that R - 1 rows
+// behind it add), 3 trees.
+Plan plan_of(int kind, int requests, int R, int heads, int kv_heads, int head_dim, int positions,
+             int cus) {
+  if (kind < 2) return plan(requests, R, heads, kv_heads, head_dim, positions, kind == 1, cus);
+  const int window = kind == 2 && positions >= R ? positions - R + 1 : 0;
+  return fitted_plan(requests, R, heads, kv_heads, head_dim, positions, window, cus);
+}
+
 // Bytes that suffice for every plan of up to so many requests, rows of each and
 // positions: no plan has more parts than the positions allow, nor more than
 // kMostRounds rounds of workgroups.
@@ -130,8 +181,9 @@ int attend(const mqa_kv_cache* cache, const void* q, int64_t q_row, int64_t q_he
     return MQA_ERR_SHAPE;
   const int cus = mqa::current_device_cus();
   if (!cus) return MQA_ERR_DEVICE;
-  const Plan a = plan(requests, R, heads, cache->kv_heads, cache->head_dim,
-                      at_most_keys(positions), p.indices != nullptr, cus);
+  const int kind = p.indices ? 1 : p.sight == mqa::kWindow ? 2 : p.sight == mqa::kTree ? 3 : 0;
+  const Plan a = plan_of(kind, requests, R, heads, cache->kv_heads, cache->head_dim,
+                         at_most_keys(positions), cus);
   if (!workspace && a.total > kNoWorkspace) return MQA_ERR_NULL;
   if (workspace && workspace_bytes < a.total)
     return mqa::workspace_failed("the workspace is smaller than workspace_size_attend_call()");
@@ -231,12 +283,11 @@ size_t workspace_size_attend(int requests, int R, int heads, int kv_heads, int h
 }
 
 size_t workspace_size_attend_call(int requests, int R, int heads, int kv_heads, int head_dim,
-                                  int positions, int listed, int device) {
-  if (!sizes_ok(requests, R, heads, kv_heads, head_dim, positions)) return 0;
+                                  int positions, int kind, int device) {
+  if (!sizes_ok(requests, R, heads, kv_heads, head_dim, positions) || kind < 0 || kind > 3) return 0;
   const int cus = mqa::device_cus(device);
   if (!cus) return 0;
-  return plan(requests, R, heads, kv_heads, head_dim, at_most_keys(positions), listed != 0, cus)
-      .total;
+  return plan_of(kind, requests, R, heads, kv_heads, head_dim, at_most_keys(positions), cus).total;
 }
 
 int mqa_attend_paged(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,

@@ -108,8 +108,7 @@ int mqa_kv_read(const mqa_kv_cache* cache, void* k, void* v, int dtype, const in
 /*
  * Bytes of workspace on `device` that suffice for every attention call of up to
  * `requests` requests, up to R rows of each and up to `positions` positions a row
- * may see (mqa_attend_paged: table_stride * page_size; mqa_attend_topk: the list's
- * width; more than MQA_MAX_KEYS count as that), with `heads` query heads: what a
+ * may see (mqa_attend_topk: the list's width; else table_stride * page_size; more than MQA_MAX_KEYS count as that), with `heads` query heads: what a
  * caller allocates once, for its largest batch. 256 where no such call needs any; 0 for
  * sizes out of range or a device that is not gfx950.
  */
@@ -117,12 +116,13 @@ size_t workspace_size_attend(int requests, int R, int heads, int kv_heads, int h
                              int positions, int device);
 
 /*
- * Bytes that one call of exactly these sizes needs (listed: 0 mqa_attend_paged, 1
- * mqa_attend_topk). Few rows need more than many, as their keys are split over
- * more workgroups. 256 where it needs none (its workspace may then be NULL).
+ * Bytes that one call of exactly these sizes needs (kind: 0 mqa_attend_paged, 1
+ * mqa_attend_topk, 2 mqa_attend_window, 3 mqa_attend_tree). Few rows need more than many,
+ * as their keys are split over more workgroups. 256 where it needs none (its workspace may
+ * then be NULL).
  */
 size_t workspace_size_attend_call(int requests, int R, int heads, int kv_heads, int head_dim,
-                                  int positions, int listed, int device);
+                                  int positions, int kind, int device);
 
 /*
  * Attention of every row over its range: with h = query head / (heads /
@@ -181,7 +181,7 @@ int mqa_attend_topk(const mqa_kv_cache* cache, const void* q, int64_t q_row_stri
  * none of them may be in other use, their table entries anything.
  *   window    >= 1; sinks >= 0
  *   workspace >= workspace_size_attend_call(requests, R, heads, kv_heads, head_dim,
- *             min(window + sinks + R - 1, table_stride * page_size), 0, device) bytes
+ *             min(window + sinks + R - 1, table_stride * page_size), 2, device) bytes
  */
 int mqa_attend_window(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
                       int64_t q_head_stride, int dtype, const int32_t* starts, const int32_t* ends,
@@ -195,6 +195,8 @@ int mqa_attend_window(const mqa_kv_cache* cache, const void* q, int64_t q_row_st
  * where drafts are stored in any order.
  *   mask      [requests * R, words] int32, dense, 4-B aligned, words in [1,
  *             MQA_MAX_DRAFT_WORDS]
+ *   workspace >= workspace_size_attend_call(requests, R, heads, kv_heads, head_dim,
+ *             table_stride * page_size, 3, device) bytes
  */
 int mqa_attend_tree(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
                     int64_t q_head_stride, int dtype, const int32_t* starts, const int32_t* ends,

@@ -79,16 +79,17 @@ Plan plan(int requests, int R, int heads, int kv_heads, int head_dim, int positi
 // of them). Narrower tiles span fewer positions of their rows' windows and waste fewer
 // columns, wider ones take less time a column and key: a workgroup's time for a key, with
 // its compute unit full, was measured as `ns`, for heads of 64 and of 128 (tiles of 64
-// columns are the slowest a column). The time of a start and an end is that of 512 keys, of
-// 1024 for the wide tiles, as above. 2000 rows of 12 heads, each its own key head, through
+// columns are the slowest a column). A start and an end take the time of 640 keys, of 1024
+// for the wide tiles, a join 6 us. 2000 rows of 12 heads, each its own key head, through
 // 504 positions: 30 us on 32 columns, 73 on 256; 4096 rows of 32 heads on 4 key heads
-// through 1027: 129 on 256, 158 on 32.
+// through 1027: 129 on 256, 158 on 32; 8 uneven trees of 13 drafts, 40 heads of 64 on 8 key
+// heads, up to 9001 positions: 37 on 128, 45 on 32.
 Plan fitted_plan(int requests, int R, int heads, int kv_heads, int head_dim, int positions,
                  int window, int cus) {
   static const struct {
     int cols;
     double ns[2];
-  } kTiles[] = {{16, {9, 18}}, {32, {14.4, 14.8}}, {128, {16.1, 39}}, {256, {19.7, 34}}};
+  } kTiles[] = {{16, {12, 22}}, {32, {17, 15}}, {128, {16.1, 39}}, {256, {19.7, 34}}};
   Plan a{};
   const int group = heads / kv_heads, columns = R * group, most = widest(columns, false);
   const int64_t units = (int64_t)requests * kv_heads;
@@ -97,14 +98,17 @@ Plan fitted_plan(int requests, int R, int heads, int kv_heads, int head_dim, int
   for (const auto& t : kTiles) {
     if (t.cols > most) continue;
     const int64_t tiles = (columns + t.cols - 1) / t.cols, n = units * tiles;
-    const int64_t room = resident(t.cols, head_dim, false, cus), ends = t.cols > 64 ? 1024 : 512;
+    const int64_t room = resident(t.cols, head_dim, false, cus), ends = t.cols > 64 ? 1024 : 640;
     const int64_t rows = (t.cols + group - 1) / group;
     const int64_t span = window > 0 && window + rows < positions ? window + rows : positions;
     for (int s = 1; s <= mqa::kMaxSplits && (s == 1 || s * 256 <= span); ++s) {
       const int64_t rounds = (n * s + room - 1) / room;
       if (s > 1 && rounds > kMostRounds) break;
-      const double cost =
-          t.ns[head_dim == 128] * (rounds * ((span + s - 1) / s + ends) + (s > 1 ? 2 * ends : 0));
+      // (a last round that leaves compute units part of their workgroups takes less)
+      const int64_t full = n * s / room, rest = n * s % room, held = room / cus;
+      const double part = rest ? 0.4 + 0.6 * (double)((rest + cus - 1) / cus) / held : 0;
+      const double cost = t.ns[head_dim == 128] * ((span + s - 1) / s + ends) * (full + part) +
+                          (s > 1 ? 6000 : 0);
       if (a.cols > 0 && cost >= best) continue;
       best = cost;
       a.cols = t.cols;

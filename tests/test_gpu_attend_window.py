@@ -111,10 +111,15 @@ def test_pages_between_may_be_in_other_use(shape, window, sinks, codes):
 
 
 def test_a_window_past_the_range_is_the_range():
-    # the same sums in the same order: the same bits
+    # the same sums; keys may be cut into other parts, so that either call is within the
+    # tolerance of the exact values, and the two within twice that
     pool, table, q, starts, ends = problem([700, 3, 129], 1, 32, 8, 128, 64, 32, BF16, "e4m3")
     args = (layout(pool), q.cuda(), pool.bytes().cuda(), table.cuda(), starts.cuda(), ends.cuda())
-    assert torch.equal(mqa.mqa_attend_window(*args, 1 << 20), mqa.mqa_attend_paged(*args))
+    cap = table.shape[1] * 64
+    want, _, tol, _ = serve_ref.attend(pool, q, table, serve_ref.window_seen(starts, ends, cap, 0, cap))
+    window, paged = mqa.mqa_attend_window(*args, 1 << 20), mqa.mqa_attend_paged(*args)
+    assert ref.differs(window, want, tol) == 0 and ref.differs(paged, want, tol) == 0
+    assert ref.differs(window, paged.double().cpu(), 2 * tol) == 0
 
 
 @pytest.mark.parametrize("shape", [([20000, 9000], 1, 16, 2, 128, 64, 64), ([30000], 2, 8, 1, 64, 64, 64)],

@@ -9,7 +9,7 @@ namespace {
 // at a time. HW waves share 32 entries: each loads its part of their rows (16
 // bytes a lane, whole rows next to each other), a step ahead, into registers
 // and then into LDS, and every one of them reads all of it for its own 16 NT
-// heads, with the products of attend_narrow.hip. For 64 heads two waves take 32
+// heads, with the products of attend_narrow.h. For 64 heads two waves take 32
 // each: with one wave for all, its sums leave room for one wave per SIMD only
 // and a gather's latency shows; with four of 16, every code is widened and read
 // from LDS four times (4096 rows of 64 heads and 2048 positions, when they were

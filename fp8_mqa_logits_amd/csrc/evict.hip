@@ -133,7 +133,8 @@ __global__ __launch_bounds__(kSelectThreads) void kv_select_kernel(SelectParams 
     }
     if (lane == 63) s_wave[wave] = sum;
     __syncthreads();
-    for (int v = 0; v < wave; ++v) sum += s_wave[v];
+#pragma unroll
+    for (int v = 0; v < kSelectWaves; ++v) sum += v < wave ? s_wave[v] : 0;
     const uint32_t before = sum - b1 - b0;  // above this thread's bins
     if (before < left && before + b1 >= left) {
       s_digit = 2047 - 2 * t;
@@ -157,20 +158,25 @@ __global__ __launch_bounds__(kSelectThreads) void kv_select_kernel(SelectParams 
     } else {
       uint32_t* const mine = p.hist + ((int64_t)i * p.parts + g) * 3 * 2048;
       uint32_t sure = 0, ties = 0;  // in this thread's bins
-      for (int level = 0; level < LEVEL; ++level) {
-        const uint32_t* h = p.hist + (int64_t)i * p.parts * 3 * 2048 + level * 2048 + 2046 - 2 * t;
-        uint32_t b1 = 0, b0 = 0, p1 = 0, p0 = 0;
+      // sums over all parts and those before this one, of all levels at once: what other
+      // workgroups wrote comes from far
+      uint32_t b1[3] = {}, b0[3] = {}, p1[3] = {}, p0[3] = {};
+      const uint32_t* const h = p.hist + (int64_t)i * p.parts * 3 * 2048 + 2046 - 2 * t;
 #pragma unroll 8
-        for (int v = 0; v < p.parts; ++v) {
-          const uint2 x = *reinterpret_cast<const uint2*>(h + v * (3 * 2048));
-          b0 += x.x;
-          b1 += x.y;
-          p0 += v < g ? x.x : 0;
-          p1 += v < g ? x.y : 0;
+      for (int v = 0; v < p.parts; ++v)
+#pragma unroll
+        for (int level = 0; level < (LEVEL < 3 ? LEVEL : 3); ++level) {
+          const uint2 x = *reinterpret_cast<const uint2*>(h + (v * 3 + level) * 2048);
+          b0[level] += x.x;
+          b1[level] += x.y;
+          p0[level] += v < g ? x.x : 0;
+          p1[level] += v < g ? x.y : 0;
         }
-        const uint32_t digit = pick(b1, b0), top = 2047 - 2 * t;
-        sure += (top > digit ? p1 : 0) + (top - 1 > digit ? p0 : 0);
-        if (level == 2) ties = top == digit ? p1 : top - 1 == digit ? p0 : 0;
+#pragma unroll
+      for (int level = 0; level < (LEVEL < 3 ? LEVEL : 3); ++level) {
+        const uint32_t digit = pick(b1[level], b0[level]), top = 2047 - 2 * t;
+        sure += (top > digit ? p1[level] : 0) + (top - 1 > digit ? p0[level] : 0);
+        if (level == 2) ties = top == digit ? p1[2] : top - 1 == digit ? p0[2] : 0;
         found |= digit << digit_shift(level);
         __syncthreads();
       }
@@ -188,6 +194,7 @@ __global__ __launch_bounds__(kSelectThreads) void kv_select_kernel(SelectParams 
           s_ties[wave] = ties;
         }
         __syncthreads();
+#pragma unroll
         for (int v = 0; v < kSelectWaves; ++v) {
           sure_before += s_wave[v];
           ties_before += s_ties[v];
@@ -221,9 +228,10 @@ __global__ __launch_bounds__(kSelectThreads) void kv_select_kernel(SelectParams 
   const int middle = min(max(begin - lo, 0), hi - lo);
   uint32_t at = begin - middle + (search ? sure_before : need > 0 ? middle : 0);
   uint32_t tied = ties_before;
-  for (int v = 0; v < wave; ++v) {
-    at += s_wave[v];
-    tied += s_ties[v];
+#pragma unroll
+  for (int v = 0; v < kSelectWaves; ++v) {
+    at += v < wave ? s_wave[v] : 0;
+    tied += v < wave ? s_ties[v] : 0;
   }
   at += tied < left ? tied : (search ? left : 0);
   const uint64_t below = (1ull << lane) - 1;

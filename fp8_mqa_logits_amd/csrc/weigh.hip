@@ -37,7 +37,7 @@ __device__ __forceinline__ float sum16(float x) {
   return x;
 }
 
-// Few columns: a wave takes 64 keys, head by head, in the layout of attend_narrow.hip's
+// Few columns: a wave takes 64 keys, head by head, in the layout of attend_narrow.h's
 // scores: lane (g, n) has those of keys 4 g + i of every 16 and column n. Bound by the
 // keys' bytes in long contexts, so that reads of several waves a SIMD are what counts.
 // SPLIT: the four waves of a workgroup share the keys, each with every fourth head, and

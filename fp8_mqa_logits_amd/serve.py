@@ -102,11 +102,17 @@ def mqa_norm_rotate(q, k, q_weight, k_weight, positions, inv_freq, eps: float | 
     with _launch(dev, stream):
         s = _stream(dev, stream)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype, device=dev)
-        if k_out is None and k is not None:
-            k_out = torch.empty(k.shape, dtype=dtype, device=dev)
-        _, q_to = _head_rows(q_out, "q_out", dtype, rows, heads, dim, dev)
-        k_to = None if k is None else _head_rows(k_out, "k_out", dtype, rows, kv_heads, dim, dev)[1]
+            q_out = torch.empty((rows, heads, dim), dtype=dtype, device=dev)
+            q_to = _HeadRows(q_out.data_ptr(), heads * dim, dim)
+        else:
+            _, q_to = _head_rows(q_out, "q_out", dtype, rows, heads, dim, dev)
+        if k is None:
+            k_to = None
+        elif k_out is None:
+            k_out = torch.empty((rows, kv_heads, dim), dtype=dtype, device=dev)
+            k_to = _HeadRows(k_out.data_ptr(), kv_heads * dim, dim)
+        else:
+            _, k_to = _head_rows(k_out, "k_out", dtype, rows, kv_heads, dim, dev)
         rc = _load().mqa_norm_rotate(
             q_in, q_to, heads, k_in, k_to, kv_heads, None if q_weight is None else q_weight.data_ptr(),
             None if k is None or k_weight is None else k_weight.data_ptr(), DTYPES[weight_type],

@@ -5,13 +5,16 @@
 //
 // Angles. position * inv_freq is formed in 64 bits and, in turns, reduced to [-1/2, 1/2]
 // there, so that far positions lose nothing; the sine and cosine of what is left are
-// taken in fp32 by the unit that takes turns: within 2^-20, below a hundredth of a last
-// place of a 16-bit result.
+// taken in fp32 by the unit that takes turns: within 2^-20 (1.3e-7 at most where it
+// was measured), below a hundredth of a last place of a 16-bit result.
 //
 // A wave takes EACH times 64 / (D / 8) heads, of the queries or of the keys, of one
 // row, eight elements a lane, so that a row's angles are formed once for all of them.
 // The other element of a pair i, i + rot / 2 comes from another lane as it was read
 // (four words, and normed again there, instead of eight sums).
+//
+// Bound by the bytes of long inputs: 16384 rows of 32 + 8 heads of 128 take 69 to 74 us,
+// 4.5 to 4.9 TB/s read and written, where a large copy reaches 4.7 to 5.2.
 #include <type_traits>
 
 #include "attend.h"
@@ -277,7 +280,9 @@ extern "C" int mqa_norm_rotate(const mqa_head_rows* q, const mqa_head_rows* q_ou
   p.eps = eps;
   hipStream_t s = static_cast<hipStream_t>(stream);
   dispatch(p, head_dim, [&](auto t, auto d, auto pr) {
-    // few rows: a wave for every four (D = 128) heads; many: 4 times as many
+    // Few rows: a wave for every four (D = 128) heads, for a short chain; many: four times
+    // as many heads, for angles formed once. 32 + 8 heads of 128: 256 rows 4.8 us on the
+    // first, 5.4 on the second, 512 6.0 and 6.1, 1024 8.5 and 7.7, 16384 94 and 74.
     if ((int64_t)rows * (heads + kv_heads) * head_dim < (int64_t)1 << 21)
       launch<t.value, d.value, pr.value, 1>(p, s);
     else

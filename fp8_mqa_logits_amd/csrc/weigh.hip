@@ -40,6 +40,9 @@ __device__ __forceinline__ float sum16(float x) {
 // Few columns: a wave takes 64 keys, head by head, in the layout of attend_narrow.h's
 // scores: lane (g, n) has those of keys 4 g + i of every 16 and column n. Bound by the
 // keys' bytes in long contexts, so that reads of several waves a SIMD are what counts.
+// Rows of 32 heads over 32 x 32768 positions of 8 key heads of 128: 198 us, 5.4 TB/s of
+// keys (the counters see each of them read from memory once); without the next head's keys
+// on their way 226, with 32 keys a wave 243.
 // SPLIT: the four waves of a workgroup share the keys, each with every fourth head, and
 // are joined through LDS; for calls with too few keys to give every wave its own.
 template <int T, int C, int D, bool SPLIT>
@@ -269,6 +272,16 @@ __device__ __forceinline__ int lane_again() {
 // before it are independent, so that the matrix and the vector unit work at the same
 // time; `late` are the scores whose exponentials are still to be taken. Stages that some
 // column sees in part are done unit by unit, with masks.
+//
+// 2048 rows of 32 heads over 32768 positions of 8 key heads: 552 us with the two small
+// launches beside it (9 and 5 us), 0.97 PFLOP/s; by the counters the matrix unit is busy
+// 46% of the cycles, vector instructions take 49% or more at four cycles each (exponentials need twice
+// that), and two waves per SIMD overlap them in part. When it took 605 us it took 570
+// without exponentials and 476 without most products. Steps on the way: keys of a narrow
+// workgroup against all columns 2015 us; this layout, a stage's products, then its
+// exponentials 742; one unit's products beside another's exponentials 632; in an order
+// that alternates them 605; queries laid out beforehand 572; addresses formed anew instead
+// of reloaded from scratch 556.
 template <int T, int C, int D>
 __global__ __launch_bounds__(512, 2) void weigh_wide_kernel(WeighParams p) {
   constexpr int KS = D / 16, COLS = 64, QROW = 2 * D + 16;
@@ -337,7 +350,7 @@ __global__ __launch_bounds__(512, 2) void weigh_wide_kernel(WeighParams p) {
     };
     // The products of a unit, s = keys b x q, one at a time, each beside a part of the
     // exponentials of another, pb and pc's keys and column, in the order written (the
-    // compiler's own puts products behind products: 632 us for those 2048 rows).
+    // compiler's own puts products behind products: 632 us for those 2048 rows, 605 in this one).
     // `beside` comes after product k.
     auto unit = [&](v16f& s, int b, const v16f& prev, int pb, const float* pf, const float2& pc,
                     auto beside) {

@@ -290,12 +290,12 @@ __device__ __forceinline__ Span uniform(Span a) {
 
 // The keys that a tile of columns walks over, STEP at a time from a multiple of 16:
 // its span, and before it the sinks' (kWindow), where they do not meet. A window costs its
-// tile the keys that some of its rows see, two to four masked steps among them, and a step
-// for the sinks: 4096 rows of 32 heads on 4 key heads, 4095 + 5 positions each, 311 us,
-// 0.88 PFLOP/s. (When it took 322, 253 of them went by the keys, at 1.09 PFLOP/s as in
-// chunks, and 57 were starts, ends and masked steps of two rounds, 12 the sinks'.) Trees:
-// 16 x 64 drafts of 32 heads on 8 key heads behind 32768 positions 655 to 680 us, up to 0.84
-// PFLOP/s, of which the join of split keys takes 21.
+// tile the keys that some of its rows see, masked steps at both ends among them, and a
+// step for the sinks: 4096 rows of 32 heads on 4 key heads, 4095 + 5 positions each, 311
+// to 319 us, up to 0.88 PFLOP/s. (When it took 322, 253 of them went by the keys, at 1.09
+// PFLOP/s as in chunks, 57 were starts, ends and masked steps of two rounds, 12 the
+// sinks'.) Trees: 16 x 64 drafts of 32 heads on 8 key heads behind 32768 positions 655 to
+// 680 us, up to 0.84 PFLOP/s, of which the join of split keys takes 21.
 template <int M, int STEP>
 struct Walk {
   Span span;

@@ -350,8 +350,8 @@ __global__ __launch_bounds__(512, 2) void weigh_wide_kernel(WeighParams p) {
     };
     // The products of a unit, s = keys b x q, one at a time, each beside a part of the
     // exponentials of another, pb and pc's keys and column, in the order written (the
-    // compiler's own puts products behind products: 632 us for those 2048 rows, 605 in this one).
-    // `beside` comes after product k.
+    // compiler's own puts products behind products: 632 us for those 2048 rows, 605 in this
+    // one). `beside` comes after product k.
     auto unit = [&](v16f& s, int b, const v16f& prev, int pb, const float* pf, const float2& pc,
                     auto beside) {
       constexpr int E = 16 / KS;

@@ -22,8 +22,8 @@ MAX_LIST = 1 << 16
 NO_WORKSPACE = 256  # workspace_size_attend_call of a call that needs none
 
 EXPORTS = ("mqa_kv_page_bytes", "mqa_kv_append", "mqa_kv_read", "workspace_size_attend",
-           "workspace_size_attend_call", "mqa_attend_paged", "mqa_attend_topk",
-           "mqa_attend_window", "mqa_attend_tree")
+           "workspace_size_attend_call", "workspace_size_attend_window", "mqa_attend_cut",
+           "mqa_attend_paged", "mqa_attend_topk", "mqa_attend_window", "mqa_attend_tree")
 
 
 class _Cache(ctypes.Structure):
@@ -56,6 +56,10 @@ def _load() -> ctypes.CDLL:
         lib.workspace_size_attend.restype = SZ
         lib.workspace_size_attend_call.argtypes = [I, I, I, I, I, I, I, I]
         lib.workspace_size_attend_call.restype = SZ
+        lib.workspace_size_attend_window.argtypes = [I, I, I, I, I, I, I, I, I]
+        lib.workspace_size_attend_window.restype = SZ
+        lib.mqa_attend_cut.argtypes = [I, I, I, I, I, I, I, I, I, I, ctypes.POINTER(ctypes.c_int32)]
+        lib.mqa_attend_cut.restype = I
         lib.mqa_attend_paged.argtypes = [C, P, I64, I64, I, P, P, P, P, I, I, I, F, P, SZ, P]
         lib.mqa_attend_paged.restype = I
         lib.mqa_attend_topk.argtypes = [C, P, I64, I64, I, P, I, P, P, P, P, I, I, I, F, P, SZ, P]
@@ -292,7 +296,6 @@ def _attend(layout, q, cache, page_table, indices, starts, ends, scale, out, lse
             for name, n in zip(("window", "sinks"), window):
                 if not 0 <= n < 1 << 31:
                     raise ValueError(f"{name}: {n} out of range")
-            positions = min(positions, max(window[0], 1) + window[1] + R - 1)
         elif mask is not None:
             if not isinstance(mask, torch.Tensor) or mask.dim() != 2:
                 raise ValueError("mask must be a tensor [rows, words]")
@@ -317,9 +320,12 @@ def _attend(layout, q, cache, page_table, indices, starts, ends, scale, out, lse
         elif return_lse:
             lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
         if workspace is None:
-            kind = 1 if indices is not None else 2 if window is not None else 3 if mask is not None else 0
-            n = lib.workspace_size_attend_call(requests, R, heads, layout.kv_heads,
-                                               layout.head_dim, positions, kind, dev.index)
+            sizes = (requests, R, heads, layout.kv_heads, layout.head_dim, positions)
+            if window is not None:
+                n = lib.workspace_size_attend_window(*sizes, *window, dev.index)
+            else:
+                kind = 1 if indices is not None else 3 if mask is not None else 0
+                n = lib.workspace_size_attend_call(*sizes, kind, dev.index)
             if n > NO_WORKSPACE:
                 workspace = torch.empty(n, dtype=torch.uint8, device=dev)
         else:

@@ -75,40 +75,58 @@ Plan plan(int requests, int R, int heads, int kv_heads, int head_dim, int positi
   return a;
 }
 
-// The plan of windows and trees (window: what a row sees of the table's positions, 0: any
-// of them). Narrower tiles span fewer positions of their rows' windows and waste fewer
-// columns, wider ones take less time a column and key: a workgroup's time for a key, with
-// its compute unit full, was measured as `ns`, for heads of 64 and of 128 (tiles of 64
-// columns are the slowest a column). A start and an end take the time of 640 keys, of 1024
-// for the wide tiles, a join 6 us. 2000 rows of 12 heads, each its own key head, through
-// 504 positions: 30 us on 32 columns, 73 on 256; 4096 rows of 32 heads on 4 key heads
-// through 1027: 129 on 256, 158 on 32; 8 uneven trees of 13 drafts, 40 heads of 64 on 8 key
-// heads, up to 9001 positions: 37 on 128, 45 on 32.
+// The plan of windows and trees (window: how many positions a row sees at most, 0: any
+// number; positions: what the rows of a request may span). Narrower tiles span fewer
+// positions of their rows' windows and waste fewer columns, wider ones take less time a
+// column and key: a workgroup's time for a key, with its compute unit full, was measured as
+// `ns`, for heads of 64 and of 128 (0: not taken. Tiles of 64 columns are the slowest a
+// column; for heads of 64 those of 256 take between 0.91 and 1.6 times those of 128). A start and an end take the time of 640
+// keys, of 1024 for the wide tiles; a join 7 us, or 2 and its parts' way to memory and back
+// where they are many (8192 rows of 12 heads through 8196 positions: 335 us in two parts,
+// 259 in one).
+// Where the table's room, not the window, bounds what rows span (a prompt that fills its
+// table), the first of them see less than a window: the rounds take the mean row's time, and
+// all of it no less than the longest workgroup's.
+// All rows of a prompt of 12 heads of 128, each its own key head, in a table of its size:
+// 16384 through 8196 positions 700 us on 256 columns, 946 on 32; 8192 through 2052 225 and
+// 174; 4096 through 4100 136 and 108. 2000 through 504 73 and 29; 4096 of 32 heads on 4 key
+// heads through 1027 of many positions 129 and 158; 8 uneven trees of 13 drafts, 40 heads of
+// 64 on 8 key heads, up to 9001 positions: 37 on 128, 45 on 32.
 Plan fitted_plan(int requests, int R, int heads, int kv_heads, int head_dim, int positions,
                  int window, int cus) {
   static const struct {
     int cols;
     double ns[2];
-  } kTiles[] = {{16, {12, 22}}, {32, {17, 15}}, {128, {16.1, 39}}, {256, {19.7, 34}}};
+  } kTiles[] = {{16, {12, 22}}, {32, {17, 12.5}}, {128, {18, 39}}, {256, {0, 31}}};
   Plan a{};
   const int group = heads / kv_heads, columns = R * group, most = widest(columns, false);
   const int64_t units = (int64_t)requests * kv_heads;
+  // positions that a row sees in the mean: the first see lo, lo + 1, ..
+  const int64_t lo = positions >= R ? positions - R + 1 : 1;
+  const int64_t fewer = window <= lo ? 0 : window - lo < R ? window - lo : R;
+  const double mean = window > 0 ? ((2 * lo + fewer - 1) * 0.5 * fewer +
+                                    (double)(R - fewer) * window) / R : positions;
   double best = 0;
   int64_t slots = 0;
   for (const auto& t : kTiles) {
-    if (t.cols > most) continue;
+    const double ns = t.ns[head_dim == 128];
+    if (t.cols > most || ns == 0) continue;
     const int64_t tiles = (columns + t.cols - 1) / t.cols, n = units * tiles;
     const int64_t room = resident(t.cols, head_dim, false, cus), ends = t.cols > 64 ? 1024 : 640;
     const int64_t rows = (t.cols + group - 1) / group;
     const int64_t span = window > 0 && window + rows < positions ? window + rows : positions;
+    const double usual = mean + rows < span ? mean + rows : span;
     for (int s = 1; s <= mqa::kMaxSplits && (s == 1 || s * 256 <= span); ++s) {
       const int64_t rounds = (n * s + room - 1) / room;
       if (s > 1 && rounds > kMostRounds) break;
-      // (a last round that leaves compute units part of their workgroups takes less)
+      // (a round that leaves compute units part of their workgroups takes less)
       const int64_t full = n * s / room, rest = n * s % room, held = room / cus;
       const double part = rest ? 0.4 + 0.6 * (double)((rest + cus - 1) / cus) / held : 0;
-      const double cost = t.ns[head_dim == 128] * ((span + s - 1) / s + ends) * (full + part) +
-                          (s > 1 ? 6000 : 0);
+      const double all = ns * (usual / s + ends) * (full + part);
+      const double longest = ns * ((double)span / s + ends) * (full ? 1 : part);
+      const double parts = (double)units * columns * s * (4 * head_dim + 8);  // bytes
+      const double join = 2000 + 2 * parts / 5000 > 7000 ? 2000 + 2 * parts / 5000 : 7000;
+      const double cost = (all > longest ? all : longest) + (s > 1 ? join : 0);
       if (a.cols > 0 && cost >= best) continue;
       best = cost;
       a.cols = t.cols;
@@ -121,13 +139,16 @@ Plan fitted_plan(int requests, int R, int heads, int kv_heads, int head_dim, int
   return a;
 }
 
-// kind: 0 ranges, 1 lists, 2 windows (positions: of a row's, and those that R - 1 rows
-// behind it add), 3 trees.
+// kind: 0 ranges, 1 lists, 2 windows (window: of a row, its sinks among them), 3 trees.
 Plan plan_of(int kind, int requests, int R, int heads, int kv_heads, int head_dim, int positions,
-             int cus) {
+             int window, int cus) {
   if (kind < 2) return plan(requests, R, heads, kv_heads, head_dim, positions, kind == 1, cus);
-  const int window = kind == 2 && positions >= R ? positions - R + 1 : 0;
-  return fitted_plan(requests, R, heads, kv_heads, head_dim, positions, window, cus);
+  return fitted_plan(requests, R, heads, kv_heads, head_dim, positions, kind == 2 ? window : 0, cus);
+}
+
+// What the windows of a request's R rows span of `room` positions, in a row.
+int64_t spanned(int64_t window, int R, int64_t room) {
+  return window + R - 1 < room ? window + R - 1 : room;
 }
 
 // Bytes that suffice for every plan of up to so many requests, rows of each and
@@ -187,10 +208,12 @@ int attend(const mqa_kv_cache* cache, const void* q, int64_t q_row, int64_t q_he
   if (!cus) return MQA_ERR_DEVICE;
   const int kind = p.indices ? 1 : p.sight == mqa::kWindow ? 2 : p.sight == mqa::kTree ? 3 : 0;
   const Plan a = plan_of(kind, requests, R, heads, cache->kv_heads, cache->head_dim,
-                         at_most_keys(positions), cus);
+                         at_most_keys(positions), at_most_keys((int64_t)p.window + p.sinks), cus);
   if (!workspace && a.total > kNoWorkspace) return MQA_ERR_NULL;
   if (workspace && workspace_bytes < a.total)
-    return mqa::workspace_failed("the workspace is smaller than workspace_size_attend_call()");
+    return mqa::workspace_failed(kind == 2
+                                     ? "the workspace is smaller than workspace_size_attend_window()"
+                                     : "the workspace is smaller than workspace_size_attend_call()");
   p.c = kernel_cache(cache);
   p.q = q;
   p.q_row = q_row;
@@ -289,9 +312,41 @@ size_t workspace_size_attend(int requests, int R, int heads, int kv_heads, int h
 size_t workspace_size_attend_call(int requests, int R, int heads, int kv_heads, int head_dim,
                                   int positions, int kind, int device) {
   if (!sizes_ok(requests, R, heads, kv_heads, head_dim, positions) || kind < 0 || kind > 3) return 0;
+  const int cus = mqa::device_cus(device), most = at_most_keys(positions);
+  if (!cus) return 0;
+  // Windows: `positions` may be the table's room and says nothing of a row's window then.
+  // Where the narrowest tile holds all rows they span it all, else any plan is possible.
+  if (kind == 2 && (int64_t)R * (heads / kv_heads) > 16)
+    return most_workspace(requests, R, heads, kv_heads, head_dim, most, false, cus);
+  return plan_of(kind, requests, R, heads, kv_heads, head_dim, most, 0, cus).total;
+}
+
+size_t workspace_size_attend_window(int requests, int R, int heads, int kv_heads, int head_dim,
+                                    int positions, int window, int sinks, int device) {
+  if (!sizes_ok(requests, R, heads, kv_heads, head_dim, positions) || window < 1 || sinks < 0)
+    return 0;
   const int cus = mqa::device_cus(device);
   if (!cus) return 0;
-  return plan_of(kind, requests, R, heads, kv_heads, head_dim, at_most_keys(positions), cus).total;
+  const int64_t seen = (int64_t)window + sinks;
+  return plan_of(2, requests, R, heads, kv_heads, head_dim,
+                 at_most_keys(spanned(seen, R, positions)), at_most_keys(seen), cus)
+      .total;
+}
+
+int mqa_attend_cut(int kind, int requests, int R, int heads, int kv_heads, int head_dim,
+                   int positions, int window, int sinks, int compute_units, int32_t* cut) {
+  if (!cut) return MQA_ERR_NULL;
+  if (!sizes_ok(requests, R, heads, kv_heads, head_dim, positions) || kind < 0 || kind > 3 ||
+      compute_units < 1 || compute_units > 4096 || (kind == 2 && (window < 1 || sinks < 0)))
+    return MQA_ERR_SHAPE;
+  const int64_t seen = (int64_t)window + sinks;
+  const Plan a = plan_of(kind, requests, R, heads, kv_heads, head_dim,
+                         at_most_keys(kind == 2 ? spanned(seen, R, positions) : positions),
+                         at_most_keys(seen), compute_units);
+  cut[0] = a.cols;
+  cut[1] = a.tiles;
+  cut[2] = a.splits;
+  return MQA_OK;
 }
 
 int mqa_attend_paged(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
@@ -325,10 +380,9 @@ int mqa_attend_window(const mqa_kv_cache* cache, const void* q, int64_t q_row_st
   p.sight = mqa::kWindow;
   p.window = window;
   p.sinks = sinks;
-  const int64_t most = positions_of(cache), spanned = (int64_t)window + sinks + R - 1;
   return attend(cache, q, q_row_stride, q_head_stride, dtype, p, window >= 1 && sinks >= 0, starts,
                 ends, out, lse, requests, R, heads, scale, workspace, workspace_bytes,
-                spanned < most ? spanned : most, stream);
+                spanned((int64_t)window + sinks, R, positions_of(cache)), stream);
 }
 
 int mqa_attend_tree(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,

@@ -117,12 +117,28 @@ size_t workspace_size_attend(int requests, int R, int heads, int kv_heads, int h
 
 /*
  * Bytes that one call of exactly these sizes needs (kind: 0 mqa_attend_paged, 1
- * mqa_attend_topk, 2 mqa_attend_window, 3 mqa_attend_tree). Few rows need more than many,
- * as their keys are split over more workgroups. 256 where it needs none (its workspace may
- * then be NULL).
+ * mqa_attend_topk, 3 mqa_attend_tree), or that suffice for mqa_attend_window (2) with
+ * any window and sinks whose min(window + sinks + R - 1, table_stride * page_size) is
+ * `positions`. Few rows need more than many, as their keys are split over more
+ * workgroups. 256 where it needs none (its workspace may then be NULL); 0 for another kind.
  */
 size_t workspace_size_attend_call(int requests, int R, int heads, int kv_heads, int head_dim,
                                   int positions, int kind, int device);
+
+/* Bytes that one mqa_attend_window of exactly these sizes needs (positions: table_stride *
+ * page_size); 256 where it needs none. */
+size_t workspace_size_attend_window(int requests, int R, int heads, int kv_heads, int head_dim,
+                                    int positions, int window, int sinks, int device);
+
+/*
+ * How a call of these sizes is cut on a device of so many compute units: cut[0] columns (a
+ * row of a query head each) a tile, cut[1] tiles of a request (of a row, for lists) and
+ * key head, cut[2] parts of a tile's keys. kind as above; positions: table_stride *
+ * page_size, or the list's width; window and sinks are looked at for kind 2 only. Needs
+ * no device. MQA_ERR_SHAPE for sizes out of range.
+ */
+int mqa_attend_cut(int kind, int requests, int R, int heads, int kv_heads, int head_dim,
+                   int positions, int window, int sinks, int compute_units, int32_t* cut);
 
 /*
  * Attention of every row over its range: with h = query head / (heads /
@@ -180,8 +196,8 @@ int mqa_attend_topk(const mqa_kv_cache* cache, const void* q, int64_t q_row_stri
  * j < e or s <= j < min(s + sinks, e), each once. Only these are read: pages that hold
  * none of them may be in other use, their table entries anything.
  *   window    >= 1; sinks >= 0
- *   workspace >= workspace_size_attend_call(requests, R, heads, kv_heads, head_dim,
- *             min(window + sinks + R - 1, table_stride * page_size), 2, device) bytes
+ *   workspace >= workspace_size_attend_window(requests, R, heads, kv_heads, head_dim,
+ *             table_stride * page_size, window, sinks, device) bytes
  */
 int mqa_attend_window(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
                       int64_t q_head_stride, int dtype, const int32_t* starts, const int32_t* ends,

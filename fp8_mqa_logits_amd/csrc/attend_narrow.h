@@ -286,7 +286,9 @@ template <int M, int T, int C, int D>
 void launch_narrow(const AttendParams& p, dim3 grid, hipStream_t s) {
   if (p.cols == 16) attend_narrow_kernel<M, T, C, D, 1><<<grid, 256, 0, s>>>(p);
   if (p.cols == 32) attend_narrow_kernel<M, T, C, D, 2><<<grid, 256, 0, s>>>(p);
-  if (p.cols == 64) attend_narrow_kernel<M, T, C, D, 4><<<grid, 256, 0, s>>>(p);
+  // (windows and trees are not planned on 64 columns)
+  if constexpr (M == kRange)
+    if (p.cols == 64) attend_narrow_kernel<M, T, C, D, 4><<<grid, 256, 0, s>>>(p);
 }
 
 }  // namespace

@@ -537,10 +537,10 @@ __global__ __launch_bounds__(64 * W, 2) void attend_wide_kernel(AttendParams p) 
 
 template <int M, int T, int C, int D>
 void launch_wide(const AttendParams& p, dim3 grid, hipStream_t s) {
-  if (p.cols == 128)
-    attend_wide_kernel<M, T, C, D, 4><<<grid, 256, 0, s>>>(p);
-  else
-    attend_wide_kernel<M, T, C, D, 8><<<grid, 512, 0, s>>>(p);
+  if (p.cols == 128) attend_wide_kernel<M, T, C, D, 4><<<grid, 256, 0, s>>>(p);
+  // (windows and trees of heads of 64 are not planned on 256 columns)
+  if constexpr (M == kRange || D == 128)
+    if (p.cols == 256) attend_wide_kernel<M, T, C, D, 8><<<grid, 512, 0, s>>>(p);
 }
 
 }  // namespace

@@ -52,6 +52,20 @@ def test_tiles_hold_all_columns():
     assert cut(WINDOWS, 1, 1, 8, 8, 64, 1 << 20, (1 << 31) - 1, (1 << 31) - 1)[2] >= 1
 
 
+def test_windows_and_trees_are_planned_on_tiles_that_are_built():
+    # no kernels of 64 columns, nor of 256 for heads of 64
+    for kind in (WINDOWS, TREES):
+        for head_dim, built in ((64, {16, 32, 128}), (128, {16, 32, 128, 256})):
+            seen = set()
+            for heads, kv_heads in ((1, 1), (8, 2), (32, 8), (12, 12), (64, 1), (1024, 1), (1024, 1024)):
+                for requests in (1, 3, 30, 300):
+                    for R in (1, 5, 17, 40, 64, 333, 2000):
+                        for room in (16, 1000, 9000, 131072, 1 << 20):
+                            for window in (1, 300, 5000, 1 << 20) if kind == WINDOWS else (1,):
+                                seen.add(cut(kind, requests, R, heads, kv_heads, head_dim, room, window, 4)[0])
+            assert seen == built
+
+
 def test_errors():
     call = A._load().mqa_attend_cut
     out = (ctypes.c_int32 * 3)(7, 7, 7)

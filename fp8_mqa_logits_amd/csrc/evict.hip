@@ -707,7 +707,10 @@ void dispatch(const KvCache& c, F f) {
 
 extern "C" int mqa_kv_select_launch(const mqa::SelectParams* p, hipStream_t s) {
   using namespace mqa;
-  const int fillers = p->width > 4 * kSelectThreads || p->keep > 4 * kSelectThreads ? 4 : 1;
+  // (requests that fill the card many times over take one each, so that a grid stays below
+  // 2^32 threads; rows cut into parts are of fewer than 512 requests)
+  const bool much = p->width > 4 * kSelectThreads || p->keep > 4 * kSelectThreads;
+  const int fillers = much && p->requests < 1 << 16 ? 4 : 1;
   if (p->part <= 4 * kSelectThreads)
     select<4>(*p, fillers, s);
   else if (p->part <= 16 * kSelectThreads)

@@ -274,13 +274,13 @@ void select(const SelectParams& p, int fillers, hipStream_t s) {
 //
 // A moved block is made in three steps: its tokens' codes and scales are gathered, its
 // scale is found (the smallest power of two that holds the largest of them), and the
-// codes are written under it. Lists ascend and name no position before the first moved
-// one's place, so that a token's place is never behind its source. Hence what a
-// workgroup gathers for later blocks is still there when it has written the earlier ones,
-// and one that goes through a request's blocks in their order, of one head's keys or
-// values, can work in place: kv_move_kernel<DIRECT>. With too few requests and heads for
-// that, blocks are gathered by all workgroups at once into the workspace
-// (kv_move_kernel) and put in place by a second launch (kv_place_kernel).
+// codes are written under it. Entry t of a list names no position before its place, starts
+// + t (the caller sees to it). Hence what a workgroup gathers for later blocks is still
+// there when it has written the earlier ones, and one that goes through a request's blocks
+// in their order, of one head's keys or values, can work in place: kv_move_kernel<DIRECT>.
+// With too few requests and heads for that, blocks are gathered by all workgroups at once
+// into the workspace (kv_move_kernel) and put in place by a second launch
+// (kv_place_kernel).
 //
 // 32 requests cut to 2048 positions of 4 heads of 128 in place: 37 us, 3.4 TB/s read
 // and written (selecting, moving and reading back 112 us, 197 with gather and place);

@@ -239,8 +239,8 @@ def workspace_size_keep(requests: int, width: int, layout: KVLayout) -> int:
 def mqa_kv_keep(layout: KVLayout, cache, page_table, positions, counts, starts=None, workspace=None,
                 stream=None) -> torch.Tensor:
     """Moves the first counts[i] listed positions [requests, width] int32 of every request
-    (ascending, none before starts[i]) to its positions starts[i] .. (int32; None: 0 ..), as
-    mqa_kv_append would store what mqa_kv_read returns for them in fp32: an eviction
+    (ascending; entry t none before starts[i] + t) to its positions starts[i] .. (int32; None:
+    0 ..), as mqa_kv_append would store what mqa_kv_read returns for them in fp32: an eviction
     (mqa_kv_select's output), or the accepted tokens of a draft's tree. The request is
     starts[i] + counts[i] long afterwards. Writes and returns cache."""
     c, dev, requests = _cache(layout, cache, page_table)

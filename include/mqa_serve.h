@@ -117,10 +117,12 @@ size_t workspace_size_select(int requests, int width);
  * Moves the first counts[i] (clamped to [0, width]) listed positions of request i to its
  * positions starts[i] .. (starts NULL: 0 ..): what mqa_kv_append makes of what
  * mqa_kv_read returns for them in fp32, but for blocks whose tokens all stay where they
- * are, which stay as they are. A list ascends and names no position before starts[i]; an
- * entry without a position in [0, K) or without a page stands for zeros. What stood behind
- * the moved tokens stands for nothing afterwards: the request is starts[i] + counts[i]
- * long. Requests must not share a page that they write to.
+ * are, which stay as they are. Tokens move towards the front, or stay: entry t of a list
+ * names no position before starts[i] + t, as ascending positions from starts[i] on do
+ * (where one does, what the request holds from starts[i] on is unspecified). An entry
+ * without a position in [0, K) or without a page stands for zeros, wherever it is; a position
+ * may be named twice. What stood behind the moved tokens stands for nothing afterwards: the
+ * request is starts[i] + counts[i] long. Requests must not share a page that they write to.
  *   positions [requests, width] int32, counts and starts [requests] int32, 4-B aligned
  *   workspace >= workspace_size_keep(requests, width, kv_heads, head_dim, block) bytes,
  *             256-B aligned, owned by the call until the stream reaches its end; nothing

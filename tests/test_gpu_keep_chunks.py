@@ -65,6 +65,28 @@ def test_moving_behind_what_stays(shape, codes):
         check_keep(pool, table, listed, counts, torch.tensor(starts).int())
 
 
+@pytest.mark.parametrize("codes", ["e4m3", "int8"])
+@pytest.mark.parametrize("back", [0, 21])
+def test_positions_named_twice_and_entries_that_name_none(codes, back):
+    shape = SHAPES[1]
+    say(f"case: keep in rounds, any entries {codes} {back}")
+    table, pool = pool_of(shape, codes, 5)
+    g = torch.Generator().manual_seed(6)
+    lens, width = shape[0], 2500
+    counts = torch.tensor([2500, 1000, 1500, 2100]).int()
+    listed = torch.full((4, width), -1, dtype=torch.int32)
+    for i, (n, c) in enumerate(zip(lens, counts.tolist())):
+        # entry t names back + t or a position behind it, up to the last; ascending
+        x = back + torch.arange(c) + torch.randint(0, 40, (c,), generator=g)
+        x = torch.maximum(x.sort().values, back + torch.arange(c)).clamp(max=n - 1)
+        assert bool((x >= back + torch.arange(c)).all()) and bool((x.diff() == 0).any())
+        listed[i, :c] = x.int()
+        none = torch.rand(c, generator=g) < 0.1
+        listed[i, :c][none] = torch.where(torch.rand(int(none.sum()), generator=g) < 0.5, -1, 1 << 20).int()
+    assert in_place(pool, table, listed)
+    check_keep(pool, table, listed, counts, torch.full((4,), back).int())
+
+
 def test_replays_and_another_stream():
     shape = SHAPES[2]
     table, pool = pool_of(shape, "e4m3", 7)

@@ -166,8 +166,11 @@ int mqa_kv_weigh(const mqa_kv_cache* cache, const void* q, int64_t q_row_stride,
   p.cut = reinterpret_cast<int4*>(base + l.cut);
   if (!l.wide) {
     // Few columns: 256 keys a workgroup where that gives every compute unit four, else 64,
-    // whose heads its waves share. Rows of 32 heads on 8 key heads: 1 x 777 positions 6.6 us
-    // shared, 14.8 not; 8 x 30000 55 and 59; 16 x 16384 60 and 51; 32 x 32768 260 and 227.
+    // whose heads its waves share. One row each of 32 heads on 8 key heads of 128: 1 x 32768
+    // positions 12.6 us shared, 16.5 not, 8 x 30000 54 and 58, 16 x 16384 59 and 51, 32 x
+    // 32768 245 and 199. (Where all keys fit into one round of three workgroups a compute
+    // unit, not sharing is faster already: 8 x 16384 32.5 and 27.4; but not for many rows or
+    // a little more of them: 40 rows 114 and 133, 8 x 30000 205 and 255.)
     p.split = (int64_t)requests * p.a.c.cap < (int64_t)4 * 256 * cus;
     const int keys = p.split ? 64 : 256;
     const int most = (p.a.c.cap + keys - 1) / keys, share = 16 * cus / requests;

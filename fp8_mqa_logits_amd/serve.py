@@ -145,7 +145,8 @@ def mqa_kv_weigh(layout: KVLayout, q, cache, page_table, starts, ends, lse, weig
     """Adds the attention weight that every position receives from a request's rows and
     heads, exp(score - lse), to weights [requests, width] fp32 (positions from width on are
     left out); returns weights. lse [requests * R, heads] fp32 as mqa_attend_paged returns it
-    for the same q, starts, ends and scale; other arguments as there."""
+    for the same q, starts, ends and scale (not that of a window or a tree, whose rows see
+    other positions than their ranges); other arguments as there."""
     c, dev, requests = _cache(layout, cache, page_table)
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a tensor")

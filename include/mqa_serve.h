@@ -62,7 +62,9 @@ int mqa_norm_rotate(const mqa_head_rows* q, const mqa_head_rows* q_out, int head
  *     weights[i][j] += sum over request i's rows r and heads h with s_r <= j < e_r of
  *                      exp(S_j - lse[r][h]),   S_j, s_r and e_r as in mqa_attend_paged
  * With the lse that mqa_attend_paged returned for the same q, ranges and scale, a row's
- * heads share out `heads` in all.
+ * heads share out `heads` in all. Rows are weighed over whole ranges: what a row saw through
+ * mqa_attend_window or mqa_attend_tree cannot be (the lse of either leaves positions of the
+ * range out, or has others, and the sums above would not be the weights of that attention).
  *   lse       dense [requests * R, heads] fp32, 4-B aligned; a row and head of -inf adds
  *             nothing
  *   weights   dense [requests, width] fp32, 4-B aligned, width >= 1; positions from width

@@ -108,9 +108,10 @@ int mqa_kv_read(const mqa_kv_cache* cache, void* k, void* v, int dtype, const in
 /*
  * Bytes of workspace on `device` that suffice for every attention call of up to
  * `requests` requests, up to R rows of each and up to `positions` positions a row
- * may see (mqa_attend_topk: the list's width; else table_stride * page_size; more than MQA_MAX_KEYS count as that), with `heads` query heads: what a
- * caller allocates once, for its largest batch. 256 where no such call needs any; 0 for
- * sizes out of range or a device that is not gfx950.
+ * may see (mqa_attend_topk: the list's width; else table_stride * page_size; more than
+ * MQA_MAX_KEYS count as that), with `heads` query heads: what a caller allocates once, for
+ * its largest batch. 256 where no such call needs any; 0 for sizes out of range or a device
+ * that is not gfx950.
  */
 size_t workspace_size_attend(int requests, int R, int heads, int kv_heads, int head_dim,
                              int positions, int device);
